@@ -22,6 +22,7 @@ E4M3, E5M2 = 0, 1
 DT_BF16, DT_FP32 = 0, 1
 AMAX_MAX, AMAX_MOST_RECENT = 0, 1
 COLUMNWISE_FROM_ORIGINAL, COLUMNWISE_FROM_ROWWISE_DEQUANTIZED = 0, 1
+B_NK, B_KN = 0, 1
 FP8_MAX = {E4M3: 448.0, E5M2: 57344.0}
 
 __all__ = [
@@ -30,6 +31,7 @@ __all__ = [
     "fp8_quantize_block", "fp8_dequantize", "fp8_quantize_delayed", "fp8_quantize_mx", "fp8_dequantize_mx",
     "fp8_block128_scales_to_mx", "fp8_amax_noalloc", "fp8_quantize_current", "fp8_quantize_hybrid", "fp8_quantize_block_cast_transpose",
     "fp8_amax_grouped", "fp8_quantize_grouped", "COLUMNWISE_FROM_ORIGINAL", "COLUMNWISE_FROM_ROWWISE_DEQUANTIZED",
+    "B_NK", "B_KN", "fp8_gemm_block", "fp8_gemm_block_grouped", "fp8_gemm_block_grouped_wgrad",
     "launch_count", "version", "library", "release_stream_workspace", "wait_timeouts",
 ]
 
@@ -337,3 +339,71 @@ def fp8_quantize_current(x, fmt, q_out, margin=0, amax_out=None, scale_out=None,
     _check(library().fp8_quantize_current(_p(x), _dt(x), x.numel(), fmt, margin, _p(q_out),
                                           _f32(amax_out, "amax_out"), _f32(scale_out, "scale_out"),
                                           _f32(scale_inv_out, "scale_inv_out"), _stream(stream)))
+
+
+def _operand(q, scale_inv, shape, scale_shape, name):
+    """Shape and type checks of one operand of a product."""
+    if not isinstance(q, torch.Tensor) or q.dtype != torch.uint8 or tuple(q.shape) != shape:
+        raise ValueError(f"{name} must be uint8 {shape}")
+    if not isinstance(scale_inv, torch.Tensor) or scale_inv.dtype != torch.float32 \
+            or tuple(scale_inv.shape) != scale_shape:
+        raise ValueError(f"scale_inv_{name} must be float32 {scale_shape}")
+
+
+def _ends(group_ends):
+    if not isinstance(group_ends, torch.Tensor) or group_ends.dtype != torch.int64 or group_ends.dim() != 1:
+        raise ValueError("group_ends must be a 1-D int64 tensor")
+    return int(group_ends.shape[0])
+
+
+def fp8_gemm_block(a, scale_inv_a, b, scale_inv_b, d, fmt_a=E4M3, fmt_b=E4M3, b_layout=B_NK, b_block_rows=128,
+                   accumulate=False, stream=None):
+    """d[m, n] = the product of block-scaled operands: a [m, k] codes with 1 x 128 factors,
+    b [n, k] (B_NK) or [k, n] (B_KN) codes with 128 x 128 factors (or, with b_block_rows=1
+    and B_NK, 1 x 128 factors).  d is bfloat16 or float32; accumulate adds to a float32 d."""
+    m, k = _rows_cols(a)
+    n = int(d.shape[1]) if d.dim() == 2 else -1
+    if tuple(d.shape) != (m, n):
+        raise ValueError(f"d must be [{m}, n]")
+    kb = -(-k // 128)
+    rows_b = n if b_block_rows == 1 else -(-n // 128)
+    shape, scales = ((k, n), (kb, rows_b)) if b_layout == B_KN else ((n, k), (rows_b, kb))
+    _operand(a, scale_inv_a, (m, k), (m, kb), "a")
+    _operand(b, scale_inv_b, shape, scales, "b")
+    _check(library().fp8_gemm_block(_p(a), fmt_a, _p(scale_inv_a), _p(b), fmt_b, _p(scale_inv_b), b_layout, b_block_rows,
+                                    m, n, k, _p(d), _dt(d), int(accumulate), _stream(stream)))
+
+
+def fp8_gemm_block_grouped(a, scale_inv_a, b, scale_inv_b, group_ends, d, fmt_a=E4M3, fmt_b=E4M3, b_layout=B_NK,
+                           stream=None):
+    """The product per expert over rows sorted by expert: rows group_ends[e-1] .. group_ends[e]-1
+    of a [rows, k] times b[e] ([groups, n, k], or [groups, k, n] with B_KN) into d [rows, n];
+    rows after the last end become zeros.  group_ends: int64 on the device."""
+    rows, k = _rows_cols(a)
+    groups = _ends(group_ends)
+    n = int(d.shape[1]) if d.dim() == 2 else -1
+    if tuple(d.shape) != (rows, n):
+        raise ValueError(f"d must be [{rows}, n]")
+    kb, nb = -(-k // 128), -(-n // 128)
+    shape, scales = ((groups, k, n), (groups, kb, nb)) if b_layout == B_KN else ((groups, n, k), (groups, nb, kb))
+    _operand(a, scale_inv_a, (rows, k), (rows, kb), "a")
+    _operand(b, scale_inv_b, shape, scales, "b")
+    _check(library().fp8_gemm_block_grouped(groups, _p(group_ends), _p(a), fmt_a, _p(scale_inv_a), _p(b), fmt_b,
+                                            _p(scale_inv_b), b_layout, rows, n, k, _p(d), _dt(d), _stream(stream)))
+
+
+def fp8_gemm_block_grouped_wgrad(a, scale_inv_a, b, scale_inv_b, group_ends, d, fmt_a=E4M3, fmt_b=E4M3,
+                                 accumulate=False, stream=None):
+    """One weight gradient per expert: d[e] [m, n] = sum over the rows of expert e of
+    a [m, rows] times b [n, rows], both with 1 x 128 factors along the rows."""
+    m, rows = _rows_cols(a)
+    n, _ = _rows_cols(b)
+    groups = _ends(group_ends)
+    if tuple(d.shape) != (groups, m, n):
+        raise ValueError(f"d must be [{groups}, {m}, {n}]")
+    rb = -(-rows // 128)
+    _operand(a, scale_inv_a, (m, rows), (m, rb), "a")
+    _operand(b, scale_inv_b, (n, rows), (n, rb), "b")
+    _check(library().fp8_gemm_block_grouped_wgrad(groups, _p(group_ends), _p(a), fmt_a, _p(scale_inv_a), _p(b), fmt_b,
+                                                  _p(scale_inv_b), m, n, rows, _p(d), _dt(d), int(accumulate),
+                                                  _stream(stream)))

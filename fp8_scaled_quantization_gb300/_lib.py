@@ -43,6 +43,12 @@ SIGNATURES = {
     "fp8_quantize_block_cast_transpose": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "fp8_amax_grouped": (c_i32, [c_i32, c_vp, c_vp, c_i32, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp]),
     "fp8_quantize_grouped": (c_i32, [c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp]),
+    "fp8_gemm_block": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_i32, c_i32, c_i64, c_i64, c_i64, c_vp, c_i32,
+                               c_i32, c_vp]),
+    "fp8_gemm_block_grouped": (c_i32, [c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_i32, c_i64, c_i64, c_i64,
+                                       c_vp, c_i32, c_vp]),
+    "fp8_gemm_block_grouped_wgrad": (c_i32, [c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_i64, c_i64, c_i64,
+                                             c_vp, c_i32, c_i32, c_vp]),
     "fp8_amax_noalloc": (c_i32, [c_vp, c_i32, c_i64, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp]),
 }
 

@@ -90,6 +90,12 @@ typedef enum {
     FP8_COLUMNWISE_FROM_ROWWISE_DEQUANTIZED = 1  /* quantize the BF16 dequantized rowwise value */
 } fp8_columnwise_source_t;
 
+/* Storage of the second operand of a product (row-major). */
+typedef enum {
+    FP8_B_NK = 0, /* [n, k]: each row runs along the contraction */
+    FP8_B_KN = 1  /* [k, n]: a weight read the other way round   */
+} fp8_b_layout_t;
+
 typedef enum {
     FP8_OK = 0,
     FP8_ERR_INVALID_ARG = 1, /* NULL pointer, negative size, bad enum or margin */
@@ -440,6 +446,86 @@ fp8_status_t fp8_dequantize_mx(const uint8_t* q, const uint8_t* scales, fp8_form
  * else).  One memset node (bad_blocks_out) + one launch. */
 fp8_status_t fp8_block128_scales_to_mx(const float* scale_inv, int64_t rows, int64_t cols, uint8_t* mx_scales,
                                        unsigned long long* bad_blocks_out, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Products of block-scaled FP8 operands                                     */
+/* ------------------------------------------------------------------------ */
+/* "Megatron FP8" §6 (forward, dgrad and wgrad GEMMs over FP8 operands, FP32
+ * accumulation); "Low Precision Training and Rollout" (128 x 128 weight
+ * blocks); "[Pytorch][Common] Hybrid quantization #2817" (1 x 128 activations
+ * and a columnwise copy for the backward GEMMs).  For every block b of 128
+ * steps of the contraction (the last one may be shorter)
+ *   P_b[i, j] = sum over k in b of decode(A[i, k]) * decode(B[j, k])
+ *   D[i, j]   = sum over b of (sa[i, b] * sb[j, b]) * P_b[i, j]
+ * with P_b and the sum over b in fp32 and one rounding to D's type.
+ *
+ *   a, scale_inv_a  device uint8[m, k] and float[m, ceil(k/128)]: codes and
+ *                   factors as fp8_quantize_block(1, 128) or
+ *                   fp8_quantize_block_cast_transpose write them.
+ *   b, scale_inv_b  b_layout FP8_B_NK: device uint8[n, k]; scales
+ *                     b_block_rows 128: float[ceil(n/128), ceil(k/128)]
+ *                                       (a weight, 128 x 128 blocks),
+ *                     b_block_rows 1:   float[n, ceil(k/128)] (1 x 128 tiles,
+ *                                       the weight gradient's operand).
+ *                   b_layout FP8_B_KN: device uint8[k, n] with 128 x 128
+ *                     blocks, float[ceil(k/128), ceil(n/128)]: the same
+ *                     weight codes read the other way round, so that the
+ *                     input gradient needs no transposed copy.
+ *                     b_block_rows 1 is FP8_ERR_UNSUPPORTED here.
+ *   fmt_a, fmt_b    may differ (E5M2 gradients, E4M3 weights).
+ *   d               device [m, n] of out_dtype (BF16 or fp32), element-aligned.
+ *   accumulate      nonzero: D += the product (fp32 D only; the order of the
+ *                   sum is the product first, then one addition).
+ *   Sizes           m, n, k >= 0, each below 2^31 - 256; k == 0 gives zeros
+ *                   (or leaves an accumulated D alone).
+ * NaN codes and E5M2 infinities follow fp32 arithmetic (the sign and payload
+ * of a NaN are not specified).  Results do not depend on the stream, on other
+ * calls or on earlier ones: every sum has a fixed order for given sizes.
+ *
+ * The forward product of a layer with weight W [out, in] and tokens X [t, in]
+ * is (A = X, B = W, FP8_B_NK); the input gradient is (A = dY [t, out], B = W,
+ * FP8_B_KN); the weight gradient is (A = dY^T [out, t], B = X^T [in, t],
+ * b_block_rows 1), both operands the columnwise halves of
+ * fp8_quantize_block_cast_transpose. */
+fp8_status_t fp8_gemm_block(const uint8_t* a, fp8_format_t fmt_a, const float* scale_inv_a, const uint8_t* b,
+                            fp8_format_t fmt_b, const float* scale_inv_b, fp8_b_layout_t b_layout, int b_block_rows,
+                            int64_t m, int64_t n, int64_t k, void* d, fp8_dtype_t out_dtype, int accumulate,
+                            void* stream);
+
+/* "Megatron FP8" §21: the products of an MoE layer's experts over rows sorted
+ * by expert, ragged sizes.  Group e (1 <= groups <= 1024) owns rows
+ * group_ends[e-1] .. group_ends[e] - 1 of A and D (group_ends[-1] = 0):
+ *   D[i, :] = A[i, :] * B[e]   for the rows i of group e,
+ *   D[i, :] = 0                for rows after the last group's end.
+ *   group_ends      device int64[groups], non-decreasing; read by the kernel,
+ *                   so no host copy or synchronisation is needed.  A value
+ *                   outside [0, rows] or below an earlier one is taken as the
+ *                   nearest allowed value.  A group may be empty.
+ *   a, scale_inv_a  [rows, k] as above.
+ *   b, scale_inv_b  [groups, n, k] or [groups, k, n], 128 x 128 blocks,
+ *                   scales per group ([groups, ceil(n/128), ceil(k/128)] or
+ *                   [groups, ceil(k/128), ceil(n/128)]).
+ *   d               [rows, n]. */
+fp8_status_t fp8_gemm_block_grouped(int groups, const int64_t* group_ends, const uint8_t* a, fp8_format_t fmt_a,
+                                    const float* scale_inv_a, const uint8_t* b, fp8_format_t fmt_b,
+                                    const float* scale_inv_b, fp8_b_layout_t b_layout, int64_t rows, int64_t n,
+                                    int64_t k, void* d, fp8_dtype_t out_dtype, void* stream);
+
+/* The weight gradients of the experts: the contraction is ragged.
+ *   D[e][i, j] = sum over the rows t of group e of A[i, t] * B[j, t]
+ *   a  uint8[m, rows], scales float[m, ceil(rows/128)]   (dY^T)
+ *   b  uint8[n, rows], scales float[n, ceil(rows/128)]   (X^T)
+ *   d  [groups, m, n] of out_dtype; zeros (or, accumulated, unchanged) for an
+ *      empty group.
+ * Both are the columnwise halves of fp8_quantize_block_cast_transpose over the
+ * whole sorted buffer: the 128-row scale tiles sit at multiples of 128 of the
+ * buffer whatever the group ends are, and a tile that a group end cuts counts
+ * for each group with the codes of its own rows only (codes of other rows,
+ * NaN included, never reach the sum).  group_ends as above. */
+fp8_status_t fp8_gemm_block_grouped_wgrad(int groups, const int64_t* group_ends, const uint8_t* a, fp8_format_t fmt_a,
+                                          const float* scale_inv_a, const uint8_t* b, fp8_format_t fmt_b,
+                                          const float* scale_inv_b, int64_t m, int64_t n, int64_t rows, void* d,
+                                          fp8_dtype_t out_dtype, int accumulate, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* amax without any device allocation                                       */
