@@ -13,6 +13,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 import torch
 
@@ -32,6 +33,7 @@ __all__ = [
     "fp8_block128_scales_to_mx", "fp8_amax_noalloc", "fp8_quantize_current", "fp8_quantize_hybrid", "fp8_quantize_block_cast_transpose",
     "fp8_amax_grouped", "fp8_quantize_grouped", "COLUMNWISE_FROM_ORIGINAL", "COLUMNWISE_FROM_ROWWISE_DEQUANTIZED",
     "B_NK", "B_KN", "fp8_gemm_block", "fp8_gemm_block_grouped", "fp8_gemm_block_grouped_wgrad",
+    "fp8_grad_norm_grouped", "fp8_grad_clip_grouped",
     "launch_count", "version", "library", "release_stream_workspace", "wait_timeouts",
 ]
 
@@ -407,3 +409,52 @@ def fp8_gemm_block_grouped_wgrad(a, scale_inv_a, b, scale_inv_b, group_ends, d, 
     _check(library().fp8_gemm_block_grouped_wgrad(groups, _p(group_ends), _p(a), fmt_a, _p(scale_inv_a), _p(b), fmt_b,
                                                   _p(scale_inv_b), m, n, rows, _p(d), _dt(d), int(accumulate),
                                                   _stream(stream)))
+
+
+_GRAD_DTYPES = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}
+
+
+def _grad_table(tensors, name):
+    """Host arrays (pointers, dtypes) of a list of contiguous BF16 / fp32 tensors on the current device."""
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("tensors passed to the FP8 library must live on a CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to the FP8 library must be contiguous")
+    here = torch.cuda.current_device()
+    if any(t.get_device() != here for t in tensors):
+        raise ValueError(f"every tensor must be on the current CUDA device cuda:{here}")
+    try:
+        dtypes = array("i", [_GRAD_DTYPES[t.dtype] for t in tensors])
+    except KeyError as e:
+        raise TypeError(f"{name} must be bfloat16 or float32 tensors, got {e.args[0]}") from None
+    return array("Q", [t.data_ptr() for t in tensors]), dtypes
+
+
+def _at(a):
+    return a.buffer_info()[0]
+
+
+def fp8_grad_norm_grouped(xs, norm_out, stream=None):
+    """norm_out[0] = sqrt of the sum of squares over all elements of all tensors in xs."""
+    if not xs:
+        raise ValueError("xs must be a non-empty list of tensors")
+    ptrs, dtypes = _grad_table(xs, "xs")
+    ns = array("q", [t.numel() for t in xs])
+    _check(library().fp8_grad_norm_grouped(len(xs), _at(ptrs), _at(ns), _at(dtypes), _f32(norm_out, "norm_out"),
+                                           _stream(stream)))
+
+
+def fp8_grad_clip_grouped(xs, max_norm, norm_out=None, ys=None, coef_out=None, eps=1e-6, stream=None):
+    """ys[i] = xs[i] * min(1, max_norm / (norm + eps)), norm over all tensors of xs; in place
+    without ys.  A norm that is NaN or Inf leaves the values as they are."""
+    if not xs or (ys is not None and len(ys) != len(xs)):
+        raise ValueError("xs must be a non-empty list of tensors, and ys as long as xs")
+    ns = array("q", [t.numel() for t in xs])
+    if ys is not None and any(y.numel() != n for y, n in zip(ys, ns)):
+        raise ValueError("each y must have as many elements as its x")
+    ptrs, dtypes = _grad_table(xs, "xs")
+    outs, out_dtypes = _grad_table(ys, "ys") if ys is not None else (None, None)
+    _check(library().fp8_grad_clip_grouped(len(xs), _at(ptrs), _at(ns), _at(dtypes), outs and _at(outs),
+                                           out_dtypes and _at(out_dtypes), max_norm, eps, _f32(norm_out, "norm_out"),
+                                           _f32(coef_out, "coef_out"), _stream(stream)))

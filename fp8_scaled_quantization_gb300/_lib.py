@@ -49,6 +49,9 @@ SIGNATURES = {
                                        c_vp, c_i32, c_vp]),
     "fp8_gemm_block_grouped_wgrad": (c_i32, [c_i32, c_vp, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_i64, c_i64, c_i64,
                                              c_vp, c_i32, c_i32, c_vp]),
+    "fp8_grad_norm_grouped": (c_i32, [c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "fp8_grad_clip_grouped": (c_i32, [c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, ctypes.c_float, ctypes.c_float, c_vp, c_vp,
+                                      c_vp]),
     "fp8_amax_noalloc": (c_i32, [c_vp, c_i32, c_i64, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp]),
 }
 

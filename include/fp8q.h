@@ -528,6 +528,36 @@ fp8_status_t fp8_gemm_block_grouped_wgrad(int groups, const int64_t* group_ends,
                                           fp8_dtype_t out_dtype, int accumulate, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Global gradient norm and clipping                                         */
+/* ------------------------------------------------------------------------ */
+/* "Megatron FP8" §24 (the work around the FP8 step should stay a small share
+ * of it): one call over all gradients of a model.
+ *   norm = sqrt(sum over all elements of all tensors of x^2)
+ *   coef = min(1, max_norm / (norm + eps)); 1 when norm is NaN or Inf, so that
+ *          a step with an overflow leaves its gradients as they are and the
+ *          caller decides by the norm
+ *   ys[i] = xs[i] * coef, rounded to ys[i]'s type
+ *   count            1 .. 4096; xs, ns, dtypes, ys, y_dtypes are HOST arrays of
+ *                    `count` entries (device pointers, element counts,
+ *                    fp8_dtype_t values; types may differ from tensor to
+ *                    tensor).
+ *   ys, y_dtypes     both NULL: in place (and nothing is written when coef is
+ *                    1).  Else ys[i] is xs[i] with the same type, or does not
+ *                    overlap any xs.
+ *   norm_out, coef_out  device float[1] each, nullable in the clip.
+ * Squares are added in fp32 per thread and in 64 bits across threads, in a
+ * fixed order; values whose squares leave the fp32 range are taken scaled, so
+ * the norm is right up to fp32's largest value (Inf beyond it).
+ * Tensors that are 16-byte aligned take the vector path, others the element
+ * path.  Launches: per 1024 nonempty tensors one reduction and one clip, and a
+ * one-CTA finalize when the reduction leaves more than 512 partials. */
+fp8_status_t fp8_grad_norm_grouped(int count, const void* const* xs, const int64_t* ns, const int* dtypes,
+                                   float* norm_out, void* stream);
+fp8_status_t fp8_grad_clip_grouped(int count, const void* const* xs, const int64_t* ns, const int* dtypes,
+                                   void* const* ys, const int* y_dtypes, float max_norm, float eps, float* norm_out,
+                                   float* coef_out, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* amax without any device allocation                                       */
 /* ------------------------------------------------------------------------ */
 /* The pages have no counterpart to this entry point; it serves callers that

@@ -115,3 +115,60 @@ def test_grouped_bindings_check_shapes(native_lib):
         fq.fp8_gemm_block_grouped_wgrad(at, st, _u8(256, 7), tt, ends, torch.zeros(3, 130, 256))
     with pytest.raises(ValueError, match="CUDA device"):
         fq.fp8_gemm_block_grouped_wgrad(at, st, bt, tt, ends, torch.zeros(3, 130, 256))
+
+
+# ------------------------------------------------------------ gradient clipping
+
+def _arr(kind, vals):
+    from array import array
+    return array(kind, vals)
+
+
+def clip(L, count=1, xs=(BAD,), ns=(4,), dt=(0,), ys=None, yd=None, max_norm=1.0, eps=1e-6, norm=BAD, coef=None, norm_only=False):
+    a = [_arr(k, v) if v is not None else None for k, v in (("Q", xs), ("q", ns), ("i", dt), ("Q", ys), ("i", yd))]
+    p = [v.buffer_info()[0] if v is not None else None for v in a]
+    if norm_only:
+        return L.fp8_grad_norm_grouped(count, p[0], p[1], p[2], norm, None)
+    return L.fp8_grad_clip_grouped(count, *p, max_norm, eps, norm, coef, None)
+
+
+@pytest.mark.parametrize("call,status,msg", [
+    (lambda L: clip(L, count=0), 1, "count must be"),
+    (lambda L: clip(L, count=4097), 1, "count must be"),
+    (lambda L: clip(L, xs=None), 1, "is NULL"),
+    (lambda L: clip(L, ns=(-1,)), 1, "n < 0"),
+    (lambda L: clip(L, dt=(5,)), 1, "unknown dtype"),
+    (lambda L: clip(L, xs=(0,)), 1, "tensor 0 is NULL"),
+    (lambda L: clip(L, xs=(BAD + 1,)), 1, "element-aligned"),
+    (lambda L: clip(L, ys=(BAD,)), 1, "both"),
+    (lambda L: clip(L, ys=(BAD,), yd=(7,)), 1, "unknown dtype"),
+    (lambda L: clip(L, ys=(0,), yd=(0,)), 1, "output 0 is NULL"),
+    (lambda L: clip(L, ys=(BAD + 2,), yd=(1,)), 1, "element-aligned"),
+    (lambda L: clip(L, ys=(BAD,), yd=(1,)), 2, "another type"),
+    (lambda L: clip(L, max_norm=-1.0), 1, "max_norm"),
+    (lambda L: clip(L, max_norm=float("nan")), 1, "max_norm"),
+    (lambda L: clip(L, max_norm=float("inf")), 1, "max_norm"),
+    (lambda L: clip(L, eps=-1.0), 1, "eps"),
+    (lambda L: clip(L, norm=BAD + 2), 1, "4-byte aligned"),
+    (lambda L: clip(L, norm=None, norm_only=True), 1, "norm_out is NULL"),
+    (lambda L: clip(L, count=4097, norm_only=True), 1, "count must be"),
+])
+def test_clip_refuses_before_launch(native_lib, call, status, msg):
+    before = native_lib.fp8_launch_count()
+    assert call(native_lib) == status
+    assert msg in native_lib.fp8_last_error_message().decode()
+    assert native_lib.fp8_launch_count() == before
+
+
+def test_clip_binding_checks(native_lib):
+    xs = [torch.zeros(8), torch.zeros(4, dtype=torch.bfloat16)]
+    with pytest.raises(ValueError, match="CUDA device"):
+        fq.fp8_grad_clip_grouped(xs, 1.0)
+    with pytest.raises(ValueError, match="non-empty"):
+        fq.fp8_grad_clip_grouped([], 1.0)
+    with pytest.raises(ValueError, match="as long as"):
+        fq.fp8_grad_clip_grouped(xs, 1.0, ys=xs[:1])
+    with pytest.raises(ValueError, match="as many elements"):
+        fq.fp8_grad_clip_grouped(xs, 1.0, ys=xs[::-1])
+    with pytest.raises(ValueError, match="non-empty"):
+        fq.fp8_grad_norm_grouped([], torch.zeros(1))
