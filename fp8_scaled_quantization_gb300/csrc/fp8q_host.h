@@ -31,9 +31,16 @@ int sm_count();
 fp8_status_t encode_tile_map_u16(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows,
                                  int box_cols);
 
+// Tensor map of `groups` row-major [rows, inner] matrices of bytes, one after
+// another (16-byte aligned base, inner a multiple of 16), read as 128 x 128
+// tiles in the 128-byte swizzle of the tensor core's operands.
+fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups);
+
 // The wait-timeout counter of the pipelined kernels' translation unit on the
 // current device (no synchronisation: call after the device is idle).
 fp8_status_t block_ct_wait_timeouts(unsigned long long* count);
+
+fp8_status_t gemm_pair_wait_timeouts(unsigned long long* count);
 
 // Workspace of (current device, stream) for per-CTA partials; nullptr on
 // failure (the error message is set).

@@ -180,7 +180,7 @@ extern "C" fp8_status_t fp8_gemm_block(const uint8_t* a, fp8_format_t fmt_a, con
                            b_layout == FP8_B_KN, b_block_rows == 1, out_dtype == FP8_DT_FP32, accumulate != 0};
     const fp8_status_t s = check(fn, p, b_layout, b_block_rows, out_dtype);
     if (s != FP8_OK || m == 0 || n == 0 || (k == 0 && p.accumulate)) return s;
-    return run_guarded(fn, p, false, static_cast<cudaStream_t>(stream));
+    return p.k > 0 ? run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream)) : run_guarded(fn, p, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" fp8_status_t fp8_gemm_block_grouped(int groups, const int64_t* group_ends, const uint8_t* a,
@@ -195,7 +195,7 @@ extern "C" fp8_status_t fp8_gemm_block_grouped(int groups, const int64_t* group_
                            b_layout == FP8_B_KN, false, out_dtype == FP8_DT_FP32, false};
     s = check(fn, p, b_layout, kBlk, out_dtype);
     if (s != FP8_OK || rows == 0 || n == 0) return s;
-    return run_guarded(fn, p, false, static_cast<cudaStream_t>(stream));
+    return p.k > 0 ? run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream)) : run_guarded(fn, p, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" fp8_status_t fp8_gemm_block_grouped_wgrad(int groups, const int64_t* group_ends, const uint8_t* a,
@@ -210,5 +210,5 @@ extern "C" fp8_status_t fp8_gemm_block_grouped_wgrad(int groups, const int64_t* 
                            false, true, out_dtype == FP8_DT_FP32, accumulate != 0};
     s = check(fn, p, FP8_B_NK, 1, out_dtype);
     if (s != FP8_OK || m == 0 || n == 0 || (rows == 0 && p.accumulate)) return s;
-    return run_guarded(fn, p, true, static_cast<cudaStream_t>(stream));
+    return p.k > 0 ? run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream)) : run_guarded(fn, p, true, static_cast<cudaStream_t>(stream));
 }

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "fp8q_device.cuh"
+#include "fp8q_host.h"
 
 namespace fp8q {
 
@@ -33,6 +34,9 @@ struct GemmProblem {
     bool out_f32;
     bool accumulate; // D += (fp32 only)
 };
+
+// gemm_block_pair.cu: 256 x 256 outputs per CTA pair.
+fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st);
 
 __host__ __device__ inline int64_t blocks_of(int64_t n) { return (n + kBlk - 1) / kBlk; }
 

@@ -55,26 +55,50 @@ int sm_count() {
     return n;
 }
 
+namespace {
+// The driver's tensor-map encoder, reached through the runtime.
+fp8_status_t tile_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (encode == nullptr) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || fn == nullptr)
+            return fail(FP8_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    *out = encode;
+    return FP8_OK;
+}
+}  // namespace
+
 fp8_status_t encode_tile_map_u16(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows,
                                  int box_cols) {
-    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        if (encode == nullptr) {
-            void* fn = nullptr;
-            cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-            cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-            if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || fn == nullptr)
-                return fail(FP8_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-        }
-    }
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const fp8_status_t s = tile_map_encoder(&encode);
+    if (s != FP8_OK) return s;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t elem_strides[2] = {1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box,
                               elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FP8_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return FP8_OK;
+}
+
+fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const fp8_status_t s = tile_map_encoder(&encode);
+    if (s != FP8_OK) return s;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)groups};
+    const cuuint64_t strides[2] = {(cuuint64_t)inner, (cuuint64_t)inner * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {128, 128, 1};
+    const cuuint32_t elem_strides[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                              elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(FP8_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
     return FP8_OK;
@@ -133,7 +157,10 @@ fp8_status_t fp8_wait_timeouts(unsigned long long* count) {
     using namespace fp8q;
     if (count == nullptr) return fail(FP8_ERR_INVALID_ARG, "fp8_wait_timeouts: count is NULL");
     fp8_status_t st = cuda_status(cudaDeviceSynchronize(), "fp8_wait_timeouts");
+    unsigned long long pair = 0;
     if (st == FP8_OK) st = block_ct_wait_timeouts(count);
+    if (st == FP8_OK) st = gemm_pair_wait_timeouts(&pair);
+    if (st == FP8_OK) *count += pair;
     return st;
 }
 
