@@ -36,6 +36,11 @@ fp8_status_t encode_tile_map_u16(CUtensorMap* map, const void* base, int64_t row
 // tiles in the 128-byte swizzle of the tensor core's operands.
 fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups);
 
+// Tensor map of `groups` row-major [rows, cols] outputs, one after another
+// (16-byte aligned base and rows), written as 32 rows of 128 bytes in the same
+// swizzle.
+fp8_status_t encode_out_map(CUtensorMap* map, void* base, bool f32, int64_t cols, int64_t rows, int64_t groups);
+
 // The wait-timeout counter of the pipelined kernels' translation unit on the
 // current device (no synchronisation: call after the device is idle).
 fp8_status_t block_ct_wait_timeouts(unsigned long long* count);

@@ -56,11 +56,22 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// Arrival in any CTA of the cluster.  RELEASE orders this thread's writes before
+// it; without, it orders only what tcgen05.fence::before_thread_sync did (a
+// release waits for the thread's copies in flight, far longer than a block).
+template <bool RELEASE>
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    if constexpr (RELEASE)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The expectation of a bulk copy: relaxed, since the bytes that it announces are
+// not this thread's writes.  (With release semantics the arrival waited for the
+// thread's earlier bulk copies: the pair's ring ran at 20 bytes per cycle and SM
+// instead of more than 40.)
 __device__ __forceinline__ void cluster_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
 
@@ -70,32 +81,62 @@ __device__ __forceinline__ void cluster_arrive_expect_tx(uint32_t bar, uint32_t 
 struct Waiter {
     bool dead = false;
 
+    template <bool CLUSTER>
     static __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
         uint32_t done;
+        if constexpr (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(bar), "r"(parity)
+                : "memory");
+        return done != 0;
+    }
+
+    // The same without waiting at all: asked for early, used later.
+    static __device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) {
+        uint32_t done;
         asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
+            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
             : "r"(bar), "r"(parity)
             : "memory");
         return done != 0;
     }
 
-    __device__ __forceinline__ void slow(uint32_t bar, uint32_t parity) {
+    // CLUSTER: acquire what the other CTA's threads wrote before they arrived.
+    template <bool CLUSTER = false>
+    __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
+        if (poll<CLUSTER>(bar, parity) || dead) return;
+        // Reading the timer takes longer than most waits do: not before many polls.
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (poll<CLUSTER>(bar, parity)) return;
         const uint64_t t0 = global_ns();
+#pragma unroll 1
         for (uint32_t i = 0; i < kMbarWaitMaxPolls; ++i) {
-            if (poll(bar, parity)) return;
+            if (poll<CLUSTER>(bar, parity)) return;
             if ((i & 15) == 15 && global_ns() - t0 > kMbarWaitLimitNs) break;
         }
         dead = true;
         atomicAdd(&g_wait_timeouts, 1ull);
     }
-
-    __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
-        if (poll(bar, parity) || dead) return;
-        slow(bar, parity);
-    }
 };
+
+// One thread of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
 
 // ------------------------------------------------------------------- tcgen05
 
@@ -188,7 +229,7 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, i
             : "memory");
 }
 
-// The generic form of the same load, by 128 threads (t: 0 .. 127) with plain
+// The generic form of the same load, by THREADS threads (t: 0 ..) with plain
 // loads and shared stores: bytes of rows below `row_hi` and columns in
 // [x_lo, x_hi), zero elsewhere.  `base` .. `base_end` are the matrix's own
 // bytes: nothing outside is read.  Any alignment.
@@ -221,14 +262,16 @@ __device__ __forceinline__ uint4 load_piece(const TileSource& s, int64_t at, int
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+template <int THREADS>
 __device__ __forceinline__ void load_tile(uint32_t dst, const TileSource& s, int64_t x0, int64_t x_lo, int64_t x_hi,
                                           int64_t row0, int64_t row_hi, int t) {
+    static_assert(THREADS % 8 == 0, "a thread keeps its piece");
     const int piece = t & 7;
     const int64_t x = x0 + piece * 16;
     const int lo = x_lo > x ? (int)(x_lo - x < 16 ? x_lo - x : 16) : 0;
     const int hi = x_hi < x + 16 ? (int)(x_hi > x ? x_hi - x : 0) : 16;
 #pragma unroll 4
-    for (int r = t >> 3; r < 128; r += 16) {
+    for (int r = t >> 3; r < 128; r += THREADS / 8) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (row0 + r < row_hi && lo < hi) v = load_piece(s, (row0 + r) * s.stride + x, lo, hi);
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * 128 + ((piece ^ (r & 7)) << 4)),
@@ -239,15 +282,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const TileSource& s, int
 
 // Shared-memory writes of this thread become visible to the tensor core.
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// 4 bytes of global memory into shared memory, asynchronously; `pending` ones
-// of a thread arrive on a barrier together.
-__device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 // ----------------------------------------------------------- packed fp32 math
 

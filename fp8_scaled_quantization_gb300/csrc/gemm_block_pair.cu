@@ -8,11 +8,18 @@
 // columns per thread, packed two-lane fused multiply-adds).  Two TMEM buffers
 // of 256 columns let the next block's product run meanwhile.
 //
-// Roles per CTA of 512 threads: warps 0-7 scale and add, then store; warps 8-11
-// fill the ring of operand tiles (one thread issuing bulk copies, or all four
-// warps with plain loads where sizes or addresses are not multiples of 16, or
-// where a ragged group's end cuts a block); warp 12 of the pair's first CTA
-// issues the products for both; warps 13 and 14 gather the scales.
+// Roles per CTA of 384 threads: warps 0-7 scale and add, then store; warp 8 of
+// the pair's first CTA issues the products for both; warp 9 gathers the scales;
+// warps 10 and 11 fill the ring of operand tiles (one thread issuing bulk
+// copies, or both warps with plain loads where sizes or addresses are not
+// multiples of 16, or where a ragged group's end cuts a block).
+//
+// What bounds it: a warp's arithmetic takes 146 of the 512 cycles that the
+// tensor core needs for a block, and two warps share a scheduler, so the
+// latencies between (a barrier's answer 150-180 cycles, a load of TMEM, shared
+// memory, a local-memory spill 300) decide.  Hence: barriers are asked one step
+// early, TMEM is read one piece ahead, the scales lie ready as one word per row
+// and block, and nothing may spill.
 #include "fp8q_host.h"
 #include "fp8q_tcgen05.cuh"
 #include "gemm_block.cuh"
@@ -20,32 +27,39 @@
 namespace fp8q {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384, kLoaders = 64;
 constexpr int kPairM = 256, kPairN = 256;  // outputs of a pair
-constexpr int kStages = 6;                 // operand ring: A and B tile, 32 KB per CTA and stage
-constexpr int kScaleSlots = 8;             // scale ring, blocks ahead
+constexpr int kStages = 5;                 // operand ring: A and B tile, 32 KB per CTA and stage
+constexpr int kScaleBlocks = 4;            // blocks whose scales are gathered together
+constexpr int kScaleSlots = 3;             // such groups in the scale ring
 constexpr int kRaster = 8;                 // tiles along m that are walked before the next tile along n
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
+constexpr uint32_t kOutBytes = 32 * 128;   // one warp's staging: 32 rows of 128 bytes
 
 struct Shared {
-    float sa[kScaleSlots][128];
-    alignas(16) float sb[kScaleSlots][kPairN];  // 128 x 128 blocks use entries 0 and 128
+    union {
+        alignas(16) float rows[kScaleSlots][kScaleBlocks][2][128];  // 128 x 128 blocks: row scale x column block scale
+        struct {
+            alignas(16) float a[kScaleSlots][kScaleBlocks][128];    // 1 x 128 tiles: rows
+            alignas(16) float b[kScaleSlots][kScaleBlocks][kPairN]; // and columns
+        } tile;
+    } sc;
     uint64_t full[kStages], empty[kStages];
     uint64_t tmem_full[2], tmem_empty[2];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint32_t tmem;
     GroupTable groups;
 };
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared);
+constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 8 * kOutBytes + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
 // Where a tile's operands and outputs lie.
 struct Tile {
     int group;
-    int64_t row0, row_end;   // of A (and D)
-    int64_t col0;
-    int64_t k_lo, k_hi;      // contraction range
-    int blk0, blks;          // its 128-blocks
+    int row0, row_end;  // of A (and D)
+    int col0;
+    int k_lo, k_hi;     // contraction range
+    int blk0, blks;     // its 128-blocks
 };
 
 template <bool RAGGED_K>
@@ -53,20 +67,151 @@ __device__ __forceinline__ Tile locate(const GemmProblem& p, const GroupTable& g
     Tile r;
     const int e = find_group(&g, count, t);
     const int local = t - g.tile[e], begin = e > 0 ? g.end[e - 1] : 0, end = g.end[e];
-    const int64_t rows = RAGGED_K ? p.m : end - begin;
-    const int tiles_m = (int)((rows + kPairM - 1) / kPairM);
+    const int m = (int)p.m, k = (int)p.k, rows = RAGGED_K ? m : end - begin;
+    const int tiles_m = (rows + kPairM - 1) / kPairM;
     // columns of kRaster tiles along m: what runs at one time shares operands in L2
     const int strip = local / (kRaster * tiles_n), in_strip = local - strip * kRaster * tiles_n;
     const int high = min(kRaster, tiles_m - strip * kRaster);
     r.group = e;
-    r.row0 = (RAGGED_K ? 0 : begin) + (int64_t)(strip * kRaster + in_strip % high) * kPairM;
-    r.row_end = RAGGED_K ? p.m : end;
-    r.col0 = (int64_t)(in_strip / high) * kPairN;
+    r.row0 = (RAGGED_K ? 0 : begin) + (strip * kRaster + in_strip % high) * kPairM;
+    r.row_end = RAGGED_K ? m : end;
+    r.col0 = in_strip / high * kPairN;
     r.k_lo = RAGGED_K ? begin : 0;
-    r.k_hi = RAGGED_K ? end : (e < p.groups ? p.k : 0);
-    r.blk0 = (int)(r.k_lo / kBlk);
-    r.blks = r.k_hi > r.k_lo ? (int)((r.k_hi + kBlk - 1) / kBlk) - r.blk0 : 0;
+    r.k_hi = RAGGED_K ? end : (e < p.groups ? k : 0);
+    // an empty contraction has no blocks, wherever it lies
+    r.blk0 = r.k_hi > r.k_lo ? r.k_lo / kBlk : 0;
+    r.blks = r.k_hi > r.k_lo ? (r.k_hi + kBlk - 1) / kBlk - r.blk0 : 0;
     return r;
+}
+
+// 128 columns of one row of D from column c0 on, by plain stores (and, when
+// accumulating, loads): rows that a group's end cuts, unaligned outputs.
+__device__ __forceinline__ void store_row(const GemmProblem& p, const uint64_t (&acc)[64], int64_t row_at, int64_t c0) {
+    const int cols = (int)(p.n - c0 < 128 ? p.n - c0 : 128);
+    if (p.out_f32) {
+        float* d = static_cast<float*>(p.d) + row_at + c0;
+        if ((p.n & 3) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 15u) == 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                if (j * 4 >= cols) continue;
+                const float2 a = unpack2(acc[2 * j]), b = unpack2(acc[2 * j + 1]);
+                float4 o = make_float4(a.x, a.y, b.x, b.y);
+                float4* q = reinterpret_cast<float4*>(d) + j;
+                if (p.accumulate) {
+                    const float4 old = *q;
+                    o = make_float4(__fadd_rn(old.x, o.x), __fadd_rn(old.y, o.y), __fadd_rn(old.z, o.z),
+                                    __fadd_rn(old.w, o.w));
+                }
+                *q = o;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 128; ++j) {
+                if (j >= cols) continue;
+                const float2 a = unpack2(acc[j >> 1]);
+                const float o = j & 1 ? a.y : a.x;
+                d[j] = p.accumulate ? __fadd_rn(d[j], o) : o;
+            }
+        }
+    } else {
+        uint16_t* d = static_cast<uint16_t*>(p.d) + row_at + c0;
+        if ((p.n & 7) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 15u) == 0) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (j * 8 >= cols) continue;
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = unpack2(acc[4 * j + i]);
+                    o[i] = f32x2_to_bf16x2(a.x, a.y);
+                }
+                reinterpret_cast<uint4*>(d)[j] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 128; ++j) {
+                if (j >= cols) continue;
+                const float2 a = unpack2(acc[j >> 1]);
+                d[j] = (uint16_t)f32x2_to_bf16x2(j & 1 ? a.y : a.x, 0.0f);
+            }
+        }
+    }
+}
+
+// The same for a warp whose 32 rows are all in the group: staged in shared
+// memory 128 bytes of each row at a time (16-byte pieces swizzled, so that the
+// stores spread over all banks) and written by the bulk-copy engine, which
+// drops what lies outside D.
+__device__ __forceinline__ void store_rows_bulk(const GemmProblem& p, const CUtensorMap* map, const uint64_t (&acc)[64],
+                                                uint32_t stage, int lane, int64_t row, int64_t c0, int z) {
+    constexpr int kRowPairs = 64;
+#pragma unroll
+    for (int part = 0; part < 4; ++part) {
+        if (part >= 2 && !p.out_f32) break;
+        const int64_t x = c0 + part * (p.out_f32 ? 32 : 64);
+        if (x >= p.n) break;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the staging is free
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t o[4];
+            if (p.out_f32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 a = unpack2(acc[(part * 16 + 2 * j + i) % kRowPairs]);
+                    o[2 * i] = __float_as_uint(a.x);
+                    o[2 * i + 1] = __float_as_uint(a.y);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = unpack2(acc[(part * 32 + 4 * j + i) % kRowPairs]);
+                    o[i] = f32x2_to_bf16x2(a.x, a.y);
+                }
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                         : "memory");
+        }
+        fence_to_async();
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                             reinterpret_cast<uint64_t>(map)),
+                         "r"((int)x), "r"((int)row), "r"(z), "r"(stage)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+
+// Scales of blocks g0 .. g0 + 3 of one row of scales: those in [from, to), as
+// one 16-byte load where rows are multiples of it.
+__device__ __forceinline__ float4 load_scales(const float* row, int g0, int from, int to, bool wide) {
+    if (wide) return __ldg(reinterpret_cast<const float4*>(row + g0));
+    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (from <= 0 && to > 0) r.x = __ldg(row + g0);
+    if (from <= 1 && to > 1) r.y = __ldg(row + g0 + 1);
+    if (from <= 2 && to > 2) r.z = __ldg(row + g0 + 2);
+    if (from <= 3 && to > 3) r.w = __ldg(row + g0 + 3);
+    return r;
+}
+
+// acc += s * P for 32 columns.
+template <bool B_TILES>
+__device__ __forceinline__ void scale_add(uint64_t* acc, const uint32_t (&v)[32], uint64_t s2, uint32_t sb) {
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        uint64_t x = pack2(v[2 * j], v[2 * j + 1]), y = pack2(v[2 * j + 2], v[2 * j + 3]);
+        if constexpr (B_TILES) {
+            uint64_t s0, s1;  // scales of columns 2j .. 2j + 3
+            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(s0), "=l"(s1) : "r"(sb + 8 * j));
+            x = mul2(x, s0);
+            y = mul2(y, s1);
+        }
+        acc[j] = fma2(x, s2, acc[j]);
+        acc[j + 1] = fma2(y, s2, acc[j + 1]);
+    }
 }
 
 // FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: both
@@ -75,11 +220,12 @@ __device__ __forceinline__ Tile locate(const GemmProblem& p, const GroupTable& g
 template <int FORM, bool TMA>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ CUtensorMap map_a,
-                 const __grid_constant__ CUtensorMap map_b) {
+                 const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d, bool bulk_store) {
     constexpr bool RAGGED_K = FORM == 2, B_KN = FORM == 1, B_TILES = FORM == 2;
     extern __shared__ uint8_t raw[];
     uint8_t* const tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    Shared& sh = *reinterpret_cast<Shared*>(tiles + kStages * kStageBytes);
+    uint8_t* const out = tiles + kStages * kStageBytes;
+    Shared& sh = *reinterpret_cast<Shared*>(out + 8 * kOutBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
 
@@ -93,12 +239,12 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             mbar_init(&sh.tmem_empty[i], 16);  // eight warps of each CTA
         }
         for (int i = 0; i < kScaleSlots; ++i) {
-            mbar_init(&sh.sc_full[i], 64);  // the lanes of two warps
+            mbar_init(&sh.sc_full[i], 1);
             mbar_init(&sh.sc_empty[i], 8);
         }
         mbar_init_fence();
     }
-    if (warp == 12) tmem_alloc<2>(&sh.tmem, 512);
+    if (warp == 8) tmem_alloc<2>(&sh.tmem, 512);
     pdl_begin();
     const int tiles_n = (int)((p.n + kPairN - 1) / kPairN);
     const int count = RAGGED_K ? p.groups : p.groups + 1;
@@ -111,143 +257,226 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
     Waiter w;
 
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
-        const uint32_t empty0 = cluster_addr(smem_addr(&sh.tmem_empty[0]), 0);
-        uint32_t it = 0;
+        const uint32_t full0 = smem_addr(&sh.tmem_full[0]), empty0 = cluster_addr(smem_addr(&sh.tmem_empty[0]), 0);
+        uint32_t it = 0, group = 0;  // blocks and scale groups so far
         for (int t = first; t < total; t += step) {
-            const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
             uint64_t acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0;
-            for (int b = 0; b < tile.blks; ++b, ++it) {
-                const uint32_t slot = it % kScaleSlots, buf = it & 1;
-                w.wait(smem_addr(&sh.sc_full[slot]), (it / kScaleSlots) & 1);
-                const float sa = sh.sa[slot][row];
-                float s = sa;
-                if constexpr (!B_TILES) s = __fmul_rn(sa, sh.sb[slot][half * 128]);
-                const uint64_t s2 = pack2(s, s);
-                w.wait(smem_addr(&sh.tmem_full[buf]), (it >> 1) & 1);
-                tmem_fence_after();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(lanes + buf * kPairN + c * 32, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if constexpr (B_TILES) {
-                            if (j & 1) continue;
-                            uint64_t s0, s1;  // scales of columns 2j .. 2j + 3
-                            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
-                                         : "=l"(s0), "=l"(s1)
-                                         : "r"(smem_addr(&sh.sb[slot][half * 128 + c * 32 + 2 * j])));
-                            acc[c * 16 + j] = fma2(mul2(pack2(v[2 * j], v[2 * j + 1]), s0), s2, acc[c * 16 + j]);
-                            acc[c * 16 + j + 1] = fma2(mul2(pack2(v[2 * j + 2], v[2 * j + 3]), s1), s2, acc[c * 16 + j + 1]);
-                        } else {
-                            acc[c * 16 + j] = fma2(pack2(v[2 * j], v[2 * j + 1]), s2, acc[c * 16 + j]);
-                        }
+            int left, sub;
+            {
+                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
+                left = tile.blks;
+                sub = tile.blk0 % kScaleBlocks;
+            }
+            float s_next = 0.0f;
+            uint32_t slot = group % kScaleSlots;
+            // scale of the next block (the group is there: its barrier has been waited for)
+            const auto scale = [&]() { return B_TILES ? sh.sc.tile.a[slot][sub][row] : sh.sc.rows[slot][sub][half][row]; };
+            if (left > 0) {
+                w.wait(smem_addr(&sh.sc_full[slot]), (group / kScaleSlots) & 1);
+                s_next = scale();
+            }
+            bool ready = false;
+            while (left > 0) {
+                const uint32_t buf = it & 1, from = lanes + buf * kPairN;
+                const uint64_t s2 = pack2(s_next, s_next);
+                const uint32_t sb = B_TILES ? smem_addr(&sh.sc.tile.b[slot][sub][half * 128]) : 0;
+                // on to the next block's scale
+                const auto advance = [&]() {
+                    ++sub;
+                    if (left == 0 || sub == kScaleBlocks) {  // the group is done with
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
+                        ++group;
+                        sub = 0;
+                        slot = group % kScaleSlots;
+                        if (left > 0) w.wait(smem_addr(&sh.sc_full[slot]), (group / kScaleSlots) & 1);
                     }
-                }
+                    if (left > 0) s_next = scale();
+                };
+                if (!ready) w.wait(full0 + buf * 8, (it >> 1) & 1);
+                __syncwarp();  // lanes may have left the wait apart
+                tmem_fence_after();
+                uint32_t v0[32], v1[32];
+                tmem_ld32(from, v0);
+                ++it;
+                --left;
+                tmem_wait_ld();
+                tmem_ld32(from + 32, v1);
+                scale_add<B_TILES>(acc, v0, s2, sb);
+                tmem_wait_ld();
+                tmem_ld32(from + 64, v0);
+                if (!B_TILES) advance();
+                scale_add<B_TILES>(acc + 16, v1, s2, sb + 128);
+                tmem_wait_ld();
+                tmem_ld32(from + 96, v1);
+                scale_add<B_TILES>(acc + 32, v0, s2, sb + 256);
+                tmem_wait_ld();
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    cluster_arrive(empty0 + buf * 8);
-                    mbar_arrive(&sh.sc_empty[slot]);
-                }
+                if (lane == 0) cluster_arrive<false>(empty0 + buf * 8);  // the buffer has been read
+                ready = left > 0 && Waiter::test(full0 + (it & 1) * 8, (it >> 1) & 1);
+                scale_add<B_TILES>(acc + 48, v1, s2, sb + 384);
+                if (B_TILES) advance();
             }
             // store: this thread's row, 128 columns
-            const int64_t r = tile.row0 + rank * 128 + row, c0 = tile.col0 + half * 128;
-            if (r < tile.row_end && c0 < p.n) {
-                const int64_t at = (RAGGED_K ? (int64_t)tile.group * p.m * p.n : 0) + r * p.n + c0;
-                const int cols = (int)(p.n - c0 < 128 ? p.n - c0 : 128);
-                if (p.out_f32) {
-                    float* d = static_cast<float*>(p.d) + at;
-                    if ((p.n & 3) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 15u) == 0) {
+            const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
+            const int64_t r = tile.row0 + (int)rank * 128 + row, c0 = tile.col0 + half * 128;
+            if (bulk_store && r - lane + 31 < tile.row_end) {
+                store_rows_bulk(p, &map_d, acc, smem_addr(out) + warp * kOutBytes, lane, r - lane, c0,
+                                RAGGED_K ? tile.group : 0);
+            } else if (r < tile.row_end && c0 < p.n) {
+                store_row(p, acc, (RAGGED_K ? (int64_t)tile.group * p.m * p.n : 0) + r * p.n, c0);
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8) {
+            // ---- products: the whole warp of the pair's first CTA walks, one thread issues
+            if (rank == 0) {
+                const uint32_t desc = mma_desc(p.fmt_a, p.fmt_b, false, B_KN, kPairM, kPairN);
+                const uint64_t a0 = tile_desc(smem_addr(tiles)), b0 = tile_desc(smem_addr(tiles) + kTileBytes);
+                uint32_t it = 0, stage = 0, phase = 0;
+                for (int t = first; t < total; t += step) {
+                    const int blks = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t).blks;
+                    for (int b = 0; b < blks; ++b, ++it) {
+                        const uint32_t buf = it & 1, free_bar = smem_addr(&sh.tmem_empty[buf]), free_phase = ((it >> 1) & 1) ^ 1;
+                        const uint64_t at = a0 + stage * (kStageBytes >> 4), bt = b0 + stage * (kStageBytes >> 4);
+                        const bool is_free = it < 2 || Waiter::test(free_bar, free_phase);
+                        // tiles written with plain stores are released to the cluster
+                        if constexpr (TMA && !RAGGED_K) w.wait(smem_addr(&sh.full[stage]), phase);
+                        else w.template wait<true>(smem_addr(&sh.full[stage]), phase);
+                        if (!is_free) w.wait(free_bar, free_phase);
+                        __syncwarp();
+                        tmem_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            if (j * 4 >= cols) continue;
-                            const float2 a = unpack2(acc[2 * j]), b = unpack2(acc[2 * j + 1]);
-                            float4 o = make_float4(a.x, a.y, b.x, b.y);
-                            float4* q = reinterpret_cast<float4*>(d) + j;
-                            if (p.accumulate) {
-                                const float4 old = *q;
-                                o = make_float4(__fadd_rn(old.x, o.x), __fadd_rn(old.y, o.y), __fadd_rn(old.z, o.z),
-                                                __fadd_rn(old.w, o.w));
-                            }
-                            *q = o;
+                            for (int k = 0; k < 4; ++k)
+                                mma_f8<2>(tmem + buf * kPairN, at + k * kStepKMajor,
+                                          bt + k * (B_KN ? kStepMnMajor : kStepKMajor), desc, k > 0);
+                            mma_commit<2>(smem_addr(&sh.tmem_full[buf]));
+                            mma_commit<2>(smem_addr(&sh.empty[stage]));
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 128; ++j) {
-                            if (j >= cols) continue;
-                            const float2 a = unpack2(acc[j >> 1]);
-                            const float o = j & 1 ? a.y : a.x;
-                            d[j] = p.accumulate ? __fadd_rn(d[j], o) : o;
-                        }
-                    }
-                } else {
-                    uint16_t* d = static_cast<uint16_t*>(p.d) + at;
-                    if ((p.n & 7) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 15u) == 0) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (j * 8 >= cols) continue;
-                            uint32_t o[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 a = unpack2(acc[4 * j + i]);
-                                o[i] = f32x2_to_bf16x2(a.x, a.y);
-                            }
-                            reinterpret_cast<uint4*>(d)[j] = make_uint4(o[0], o[1], o[2], o[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 128; ++j) {
-                            if (j >= cols) continue;
-                            const float2 a = unpack2(acc[j >> 1]);
-                            d[j] = (uint16_t)f32x2_to_bf16x2(j & 1 ? a.y : a.x, 0.0f);
+                        __syncwarp();
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1;
                         }
                     }
                 }
             }
-        }
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp < 12) {
+        } else if (warp == 9) {
+            // ---- scales: this CTA's 128 rows and the pair's 256 columns (or their two 128-blocks)
+            const int64_t kb = blocks_of(p.k), nb = blocks_of(p.n);
+            const bool wide_a = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sa) & 15u) == 0;
+            const bool wide_b = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sb) & 15u) == 0;
+            uint32_t group = 0;
+            for (int t = first; t < total; t += step) {
+                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
+                const int last = tile.blk0 + tile.blks;
+                for (int g0 = tile.blk0 / kScaleBlocks * kScaleBlocks; g0 < last; g0 += kScaleBlocks, ++group) {
+                    const int from = max(tile.blk0 - g0, 0), to = min(last - g0, kScaleBlocks);
+                    const uint32_t slot = group % kScaleSlots;
+                    float4 a[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // a row or column that is not there: any scale
+                        const int64_t r = tile.row0 + (int)rank * 128 + i * 32 + lane;
+                        a[i] = load_scales(p.sa + (r < p.m ? r : p.m - 1) * kb, g0, from, to, wide_a);
+                    }
+                    if constexpr (B_TILES) {
+                        const auto put = [&](float* dst, int stride, float4 v) {
+                            dst[0] = v.x;
+                            dst[stride] = v.y;
+                            dst[2 * stride] = v.z;
+                            dst[3 * stride] = v.w;
+                        };
+                        if (group >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (group / kScaleSlots - 1) & 1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) put(&sh.sc.tile.a[slot][0][i * 32 + lane], 128, a[i]);
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int64_t n = tile.col0 + h * 128 + i * 32 + lane;
+                                a[i] = load_scales(p.sb + (n < p.n ? n : p.n - 1) * kb, g0, from, to, wide_b);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) put(&sh.sc.tile.b[slot][0][h * 128 + i * 32 + lane], kPairN, a[i]);
+                        }
+                    } else {
+                        // lanes 4h + j load the scale of block g0 + j, column block h
+                        const int64_t n = tile.col0 / kBlk + ((lane >> 2) & 1), cb = n < nb ? n : nb - 1;
+                        const float* sb = p.sb + (int64_t)tile.group * kb * nb;
+                        const int j = lane & 3;
+                        float c = 0.0f;
+                        if (j >= from && j < to) c = __ldg(sb + (B_KN ? (int64_t)(g0 + j) * nb + cb : cb * kb + g0 + j));
+                        if (group >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (group / kScaleSlots - 1) & 1);
+                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float c0 = __shfl_sync(0xFFFFFFFFu, c, 4 * h), c1 = __shfl_sync(0xFFFFFFFFu, c, 4 * h + 1);
+                            const float c2 = __shfl_sync(0xFFFFFFFFu, c, 4 * h + 2), c3 = __shfl_sync(0xFFFFFFFFu, c, 4 * h + 3);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float* dst = &sh.sc.rows[slot][0][h][i * 32 + lane];
+                                dst[0] = __fmul_rn(a[i].x, c0);
+                                dst[256] = __fmul_rn(a[i].y, c1);
+                                dst[512] = __fmul_rn(a[i].z, c2);
+                                dst[768] = __fmul_rn(a[i].w, c3);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.sc_full[slot]);
+                }
+            }
+        } else {
             // ---- operand tiles: A rows [row0 + 128 rank, ..), B columns [col0 + 128 rank, ..)
-            const int tid = threadIdx.x - 256;
+            const int tid = threadIdx.x - (kThreads - kLoaders);
             const uint32_t base = smem_addr(tiles), full0 = cluster_addr(smem_addr(&sh.full[0]), 0);
-            uint32_t it = 0;
-            if (!TMA || RAGGED_K || tid == 0) {
+            uint32_t it = 0, stage = 0, phase = 0;
+            // with bulk copies alone, one warp is enough
+            if (!TMA || RAGGED_K || warp == 10) {
                 for (int t = first; t < total; t += step) {
                     const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
-                    const int64_t row = tile.row0 + rank * 128, col = tile.col0 + rank * 128;
+                    const int row = tile.row0 + (int)rank * 128, col = tile.col0 + (int)rank * 128;
                     for (int b = 0; b < tile.blks; ++b, ++it) {
-                        const uint32_t stage = it % kStages, a = base + stage * kStageBytes, bt = a + kTileBytes;
-                        const int64_t x = (int64_t)(tile.blk0 + b) * kBlk;
+                        const uint32_t a = base + stage * kStageBytes, bt = a + kTileBytes, bar = full0 + stage * 8;
+                        const int x = (tile.blk0 + b) * kBlk;
                         // a block that a group's end cuts holds other groups' codes too: masked loads
                         const bool cut = RAGGED_K && (x < tile.k_lo || (x + kBlk > tile.k_hi && tile.k_hi < p.k));
-                        if (tid == 0 && it >= kStages) w.wait(smem_addr(&sh.empty[stage]), (it / kStages - 1) & 1);
+                        if (warp == 10 && it >= kStages) w.wait(smem_addr(&sh.empty[stage]), phase ^ 1);
+                        __syncwarp();  // lanes may have left the wait apart
                         if (TMA && !cut) {
-                            if (tid != 0) continue;
-                            cluster_arrive_expect_tx(full0 + stage * 8, kStageBytes);
-                            tma_tile<true>(a, &map_a, (int)x, (int)row, 0, full0 + stage * 8);
-                            if constexpr (B_KN) tma_tile<true>(bt, &map_b, (int)col, (int)x, tile.group, full0 + stage * 8);
-                            else tma_tile<true>(bt, &map_b, (int)x, (int)col, RAGGED_K ? 0 : tile.group, full0 + stage * 8);
-                            continue;
+                            if (warp == 10 && elect_one()) {
+                                cluster_arrive_expect_tx(bar, kStageBytes);
+                                tma_tile<true>(a, &map_a, x, row, 0, bar);
+                                if constexpr (B_KN) tma_tile<true>(bt, &map_b, col, x, tile.group, bar);
+                                else tma_tile<true>(bt, &map_b, x, col, RAGGED_K ? 0 : tile.group, bar);
+                            }
+                        } else {
+                            group_sync(1, kLoaders);  // the stage is free
+                            const TileSource as = {p.a, p.a + p.m * p.k, p.k};
+                            load_tile<kLoaders>(a, as, x, tile.k_lo, tile.k_hi, row, p.m, tid);
+                            const int64_t weight = RAGGED_K ? 0 : (int64_t)tile.group * p.n * p.k;
+                            const TileSource bs = {p.b + weight, p.b + weight + p.n * p.k, B_KN ? p.n : p.k};
+                            if constexpr (B_KN) load_tile<kLoaders>(bt, bs, col, 0, p.n, x, p.k, tid);
+                            else load_tile<kLoaders>(bt, bs, x, tile.k_lo, tile.k_hi, col, p.n, tid);
+                            fence_to_async();
+                            group_sync(1, kLoaders);  // every warp's part is written
+                            if (tid == 0) cluster_arrive<true>(bar);
                         }
                         __syncwarp();
-                        group_sync(1, 128);  // the stage is free
-                        const TileSource as = {p.a, p.a + p.m * p.k, p.k};
-                        load_tile(a, as, x, tile.k_lo, tile.k_hi, row, p.m, tid);
-                        const int64_t weight = RAGGED_K ? 0 : (int64_t)tile.group * p.n * p.k;
-                        const TileSource bs = {p.b + weight, p.b + weight + p.n * p.k, B_KN ? p.n : p.k};
-                        if constexpr (B_KN) load_tile(bt, bs, col, 0, p.n, x, p.k, tid);
-                        else load_tile(bt, bs, x, tile.k_lo, tile.k_hi, col, p.n, tid);
-                        fence_to_async();
-                        group_sync(1, 128);  // every warp's part is written
-                        if (tid == 0) cluster_arrive(full0 + stage * 8);
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
                     }
                 }
                 // the last fills have been read before the CTA ends
@@ -255,94 +484,13 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                     for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
                         w.wait(smem_addr(&sh.empty[i % kStages]), (i / kStages) & 1);
             }
-        } else if (warp == 12) {
-            // ---- products, by one thread of the pair's first CTA
-            if (rank == 0 && lane == 0) {
-                const uint32_t desc = mma_desc(p.fmt_a, p.fmt_b, false, B_KN, kPairM, kPairN);
-                const uint64_t a0 = tile_desc(smem_addr(tiles)), b0 = tile_desc(smem_addr(tiles) + kTileBytes);
-                uint32_t it = 0;
-                for (int t = first; t < total; t += step) {
-                    const int blks = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t).blks;
-                    for (int b = 0; b < blks; ++b, ++it) {
-                        const uint32_t stage = it % kStages, buf = it & 1;
-                        if (it >= 2) w.wait(smem_addr(&sh.tmem_empty[buf]), ((it >> 1) - 1) & 1);
-                        w.wait(smem_addr(&sh.full[stage]), (it / kStages) & 1);
-                        tmem_fence_after();
-                        const uint64_t at = a0 + stage * (kStageBytes >> 4), bt = b0 + stage * (kStageBytes >> 4);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f8<2>(tmem + buf * kPairN, at + k * kStepKMajor, bt + k * (B_KN ? kStepMnMajor : kStepKMajor),
-                                      desc, k > 0);
-                        mma_commit<2>(smem_addr(&sh.empty[stage]));
-                        mma_commit<2>(smem_addr(&sh.tmem_full[buf]));
-                    }
-                }
-            }
-        } else if (warp == 13) {
-            // ---- row scales: this CTA's 128 rows
-            const int64_t kb = blocks_of(p.k);
-            uint32_t it = 0;
-            for (int t = first; t < total; t += step) {
-                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
-                const float* sa[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t r = tile.row0 + rank * 128 + i * 32 + lane;
-                    sa[i] = p.sa + (r < p.m ? r : p.m - 1) * kb + tile.blk0;  // a row that is not there: any scale
-                }
-                for (int b = 0; b < tile.blks; ++b, ++it) {
-                    const uint32_t slot = it % kScaleSlots;
-                    if (it >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (it / kScaleSlots - 1) & 1);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) copy4_async(smem_addr(&sh.sa[slot][i * 32 + lane]), sa[i] + b);
-                    copies_arrive(smem_addr(&sh.sc_full[slot]));
-                }
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-        } else if (warp == 14) {
-            // ---- column scales: the pair's 256 columns, or their two 128-blocks
-            const int64_t kb = blocks_of(p.k), nb = blocks_of(p.n);
-            uint32_t it = 0;
-            for (int t = first; t < total; t += step) {
-                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
-                const float* sb[B_TILES ? 8 : 1];
-                if constexpr (B_TILES) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t c = tile.col0 + i * 32 + lane;
-                        sb[i] = p.sb + (c < p.n ? c : p.n - 1) * kb + tile.blk0;
-                    }
-                } else {
-                    const int64_t c = tile.col0 / kBlk + (lane & 1), cb = c < nb ? c : nb - 1;
-                    sb[0] = p.sb + (int64_t)tile.group * kb * nb + (B_KN ? cb : cb * kb);
-                }
-                const int64_t next_b = B_KN ? nb : 1;
-                for (int b = 0; b < tile.blks; ++b, ++it) {
-                    const uint32_t slot = it % kScaleSlots;
-                    if (it >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (it / kScaleSlots - 1) & 1);
-                    if constexpr (B_TILES) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) copy4_async(smem_addr(&sh.sb[slot][i * 32 + lane]), sb[i] + b);
-                    } else if (lane < 2) {
-                        copy4_async(smem_addr(&sh.sb[slot][lane * 128]), sb[0] + b * next_b);
-                    }
-                    copies_arrive(smem_addr(&sh.sc_full[slot]));
-                }
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
     }
     tmem_fence_before();
     cluster_sync();
     tmem_fence_after();
-    if (warp == 12) tmem_free<2>(tmem, 512);
-}
-
-template <int FORM, bool TMA>
-fp8_status_t launch_pair(const char* fn, const GemmProblem& p, const CUtensorMap& a, const CUtensorMap& b, int pairs,
-                         cudaStream_t st) {
-    return launch_smem(fn, gemm_pair_kernel<FORM, TMA>, dim3(2 * pairs), dim3(kThreads), kSmemBytes, st, p, a, b);
+    if (warp == 8) tmem_free<2>(tmem, 512);
 }
 
 }  // namespace
@@ -352,18 +500,22 @@ fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st
     const int64_t inner_b = p.b_kn ? p.n : p.k, rows_b = p.b_kn ? p.k : p.n;
     // the bulk copies need 16-byte aligned bases and row strides
     const bool tma = aligned16(p.a) && aligned16(p.b) && p.k % 16 == 0 && inner_b % 16 == 0;
-    CUtensorMap a = {}, b = {};
-    if (tma) {
-        fp8_status_t s = encode_tile_map_u8(&a, p.a, p.k, p.m, 1);
-        if (s == FP8_OK) s = encode_tile_map_u8(&b, p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups);
-        if (s != FP8_OK) return s;
-    }
+    const bool bulk = aligned16(p.d) && p.n % (p.out_f32 ? 4 : 8) == 0 && !p.accumulate;
+    CUtensorMap a = {}, b = {}, d = {};
+    fp8_status_t s = FP8_OK;
+    if (tma) s = encode_tile_map_u8(&a, p.a, p.k, p.m, 1);
+    if (tma && s == FP8_OK) s = encode_tile_map_u8(&b, p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups);
+    if (bulk && s == FP8_OK) s = encode_out_map(&d, p.d, p.out_f32, p.n, p.m, p.b_tiles ? p.groups : 1);
+    if (s != FP8_OK) return s;
     const int64_t tiles_n = (p.n + kPairN - 1) / kPairN, tiles_m = (p.m + kPairM - 1) / kPairM;
     const int64_t most = p.b_tiles ? tiles_m * tiles_n * p.groups : (tiles_m + p.groups - 1) * tiles_n;
     const int sms = sm_count() / 2, pairs = (int)(most < sms ? most : sms);
-    if (form == 0) return tma ? launch_pair<0, true>(fn, p, a, b, pairs, st) : launch_pair<0, false>(fn, p, a, b, pairs, st);
-    if (form == 1) return tma ? launch_pair<1, true>(fn, p, a, b, pairs, st) : launch_pair<1, false>(fn, p, a, b, pairs, st);
-    return tma ? launch_pair<2, true>(fn, p, a, b, pairs, st) : launch_pair<2, false>(fn, p, a, b, pairs, st);
+    const auto go = [&](auto kernel) {
+        return launch_smem(fn, kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, st, p, a, b, d, bulk);
+    };
+    if (form == 0) return tma ? go(gemm_pair_kernel<0, true>) : go(gemm_pair_kernel<0, false>);
+    if (form == 1) return tma ? go(gemm_pair_kernel<1, true>) : go(gemm_pair_kernel<1, false>);
+    return tma ? go(gemm_pair_kernel<2, true>) : go(gemm_pair_kernel<2, false>);
 }
 
 fp8_status_t gemm_pair_wait_timeouts(unsigned long long* count) {

@@ -104,6 +104,22 @@ fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inne
     return FP8_OK;
 }
 
+fp8_status_t encode_out_map(CUtensorMap* map, void* base, bool f32, int64_t cols, int64_t rows, int64_t groups) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const fp8_status_t s = tile_map_encoder(&encode);
+    if (s != FP8_OK) return s;
+    const cuuint64_t row_bytes = (cuuint64_t)cols * (f32 ? 4 : 2);
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)groups};
+    const cuuint64_t strides[2] = {row_bytes, row_bytes * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
+    const cuuint32_t elem_strides[3] = {1, 1, 1};
+    const CUresult r = encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims,
+                              strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FP8_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return FP8_OK;
+}
+
 Workspace* stream_workspace(cudaStream_t stream, fp8_status_t* st) {
     *st = FP8_OK;
     int dev = 0;
