@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = 384, kLoaders = 64;
 constexpr int kPairM = 256, kPairN = 256;  // outputs of a pair
 constexpr int kStages = 5;                 // operand ring: A and B tile, 32 KB per CTA and stage
-constexpr int kScaleBlocks = 4;            // blocks whose scales are gathered together
+constexpr int kScaleBlocks = 4;            // blocks of a tile whose scales are gathered together
 constexpr int kScaleSlots = 3;             // such groups in the scale ring
 constexpr int kRaster = 8;                 // tiles along m that are walked before the next tile along n
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
@@ -38,10 +38,10 @@ constexpr uint32_t kOutBytes = 32 * 128;   // one warp's staging: 32 rows of 128
 
 struct Shared {
     union {
-        alignas(16) float rows[kScaleSlots][kScaleBlocks][2][128];  // 128 x 128 blocks: row scale x column block scale
+        float4 rows[kScaleSlots][2][128];  // 128 x 128 blocks: per column half and row, row scale x column block scale
         struct {
-            alignas(16) float a[kScaleSlots][kScaleBlocks][128];    // 1 x 128 tiles: rows
-            alignas(16) float b[kScaleSlots][kScaleBlocks][kPairN]; // and columns
+            float4 a[kScaleSlots][128];                              // 1 x 128 tiles: per row,
+            alignas(16) float b[kScaleSlots][kScaleBlocks][kPairN];  // and per block and column
         } tile;
     } sc;
     uint64_t full[kStages], empty[kStages];
@@ -185,23 +185,23 @@ __device__ __forceinline__ void store_rows_bulk(const GemmProblem& p, const CUte
     }
 }
 
-// Scales of blocks g0 .. g0 + 3 of one row of scales: those in [from, to), as
-// one 16-byte load where rows are multiples of it.
-__device__ __forceinline__ float4 load_scales(const float* row, int g0, int from, int to, bool wide) {
-    if (wide) return __ldg(reinterpret_cast<const float4*>(row + g0));
+// The first `to` of four scales; one 16-byte load where they are aligned to it
+// (and the row holds all four).
+__device__ __forceinline__ float4 load_scales(const float* at, int to, bool wide) {
+    if (wide) return __ldg(reinterpret_cast<const float4*>(at));
     float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (from <= 0 && to > 0) r.x = __ldg(row + g0);
-    if (from <= 1 && to > 1) r.y = __ldg(row + g0 + 1);
-    if (from <= 2 && to > 2) r.z = __ldg(row + g0 + 2);
-    if (from <= 3 && to > 3) r.w = __ldg(row + g0 + 3);
+    if (to > 0) r.x = __ldg(at);
+    if (to > 1) r.y = __ldg(at + 1);
+    if (to > 2) r.z = __ldg(at + 2);
+    if (to > 3) r.w = __ldg(at + 3);
     return r;
 }
 
-// acc += s * P for 32 columns.
-template <bool B_TILES>
-__device__ __forceinline__ void scale_add(uint64_t* acc, const uint32_t (&v)[32], uint64_t s2, uint32_t sb) {
+// acc += s * P for one piece of columns.
+template <bool B_TILES, int COLS>
+__device__ __forceinline__ void scale_add(uint64_t* acc, const uint32_t (&v)[COLS], uint64_t s2, uint32_t sb) {
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
+    for (int j = 0; j < COLS / 2; j += 2) {
         uint64_t x = pack2(v[2 * j], v[2 * j + 1]), y = pack2(v[2 * j + 2], v[2 * j + 3]);
         if constexpr (B_TILES) {
             uint64_t s0, s1;  // scales of columns 2j .. 2j + 3
@@ -257,74 +257,77 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
     Waiter w;
 
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
         const uint32_t full0 = smem_addr(&sh.tmem_full[0]), empty0 = cluster_addr(smem_addr(&sh.tmem_empty[0]), 0);
         uint32_t it = 0, group = 0;  // blocks and scale groups so far
         for (int t = first; t < total; t += step) {
+            const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
             uint64_t acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0;
-            int left, sub;
-            {
-                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
-                left = tile.blks;
-                sub = tile.blk0 % kScaleBlocks;
-            }
-            float s_next = 0.0f;
-            uint32_t slot = group % kScaleSlots;
-            // scale of the next block (the group is there: its barrier has been waited for)
-            const auto scale = [&]() { return B_TILES ? sh.sc.tile.a[slot][sub][row] : sh.sc.rows[slot][sub][half][row]; };
-            if (left > 0) {
+            float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s4_next = s4;
+            uint32_t slot = 0;
+            // this row's scales of the next group of blocks; they live in registers from here on
+            const auto fetch = [&]() {
+                slot = group % kScaleSlots;
                 w.wait(smem_addr(&sh.sc_full[slot]), (group / kScaleSlots) & 1);
-                s_next = scale();
-            }
+                __syncwarp();
+                if constexpr (B_TILES) {
+                    s4_next = sh.sc.tile.a[slot][row];
+                } else {
+                    s4_next = sh.sc.rows[slot][half][row];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
+                }
+                ++group;
+            };
+            if (!B_TILES && tile.blks > 0) fetch();
             bool ready = false;
-            while (left > 0) {
+            for (int b = 0; b < tile.blks; ++b) {
                 const uint32_t buf = it & 1, from = lanes + buf * kPairN;
-                const uint64_t s2 = pack2(s_next, s_next);
-                const uint32_t sb = B_TILES ? smem_addr(&sh.sc.tile.b[slot][sub][half * 128]) : 0;
-                // on to the next block's scale
-                const auto advance = [&]() {
-                    ++sub;
-                    if (left == 0 || sub == kScaleBlocks) {  // the group is done with
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
-                        ++group;
-                        sub = 0;
-                        slot = group % kScaleSlots;
-                        if (left > 0) w.wait(smem_addr(&sh.sc_full[slot]), (group / kScaleSlots) & 1);
+                if (b % kScaleBlocks == 0) {
+                    if constexpr (B_TILES) {
+                        if (b > 0) {  // every lane is done with the last group's column scales
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
+                        }
+                        fetch();
                     }
-                    if (left > 0) s_next = scale();
-                };
+                    s4 = s4_next;
+                } else {
+                    s4.x = s4.y;
+                    s4.y = s4.z;
+                    s4.z = s4.w;
+                }
+                const uint64_t s2 = pack2(s4.x, s4.x);
+                const uint32_t sb = B_TILES ? smem_addr(&sh.sc.tile.b[slot][b % kScaleBlocks][half * 128]) : 0;
                 if (!ready) w.wait(full0 + buf * 8, (it >> 1) & 1);
                 __syncwarp();  // lanes may have left the wait apart
                 tmem_fence_after();
-                uint32_t v0[32], v1[32];
-                tmem_ld32(from, v0);
                 ++it;
-                --left;
-                tmem_wait_ld();
-                tmem_ld32(from + 32, v1);
-                scale_add<B_TILES>(acc, v0, s2, sb);
-                tmem_wait_ld();
-                tmem_ld32(from + 64, v0);
-                if (!B_TILES) advance();
-                scale_add<B_TILES>(acc + 16, v1, s2, sb + 128);
-                tmem_wait_ld();
-                tmem_ld32(from + 96, v1);
-                scale_add<B_TILES>(acc + 32, v0, s2, sb + 256);
-                tmem_wait_ld();
-                tmem_fence_before();
+                constexpr int kPiece = B_TILES ? 16 : 32;  // (the column scales take registers too)
+                uint32_t v[kPiece];
+#pragma unroll
+                for (int c = 0; c < 128 / kPiece; ++c) {
+                    tmem_ld(from + c * kPiece, v);
+                    tmem_wait_ld();
+                    if (c == 128 / kPiece - 1) {  // the buffer has been read
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) cluster_arrive<false>(empty0 + buf * 8);
+                        ready = b + 1 < tile.blks && Waiter::test(full0 + (it & 1) * 8, (it >> 1) & 1);
+                    }
+                    scale_add<B_TILES>(acc + c * kPiece / 2, v, s2, sb + c * kPiece * 4);
+                    if (c == 1 && !B_TILES && b % kScaleBlocks == 2 && b + 2 < tile.blks) fetch();
+                }
+            }
+            if (B_TILES && tile.blks > 0) {
                 __syncwarp();
-                if (lane == 0) cluster_arrive<false>(empty0 + buf * 8);  // the buffer has been read
-                ready = left > 0 && Waiter::test(full0 + (it & 1) * 8, (it >> 1) & 1);
-                scale_add<B_TILES>(acc + 48, v1, s2, sb + 384);
-                if (B_TILES) advance();
+                if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
             }
             // store: this thread's row, 128 columns
-            const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
             const int64_t r = tile.row0 + (int)rank * 128 + row, c0 = tile.col0 + half * 128;
             if (bulk_store && r - lane + 31 < tile.row_end) {
                 store_rows_bulk(p, &map_d, acc, smem_addr(out) + warp * kOutBytes, lane, r - lane, c0,
@@ -336,7 +339,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8) {
             // ---- products: the whole warp of the pair's first CTA walks, one thread issues
             if (rank == 0) {
@@ -379,35 +382,35 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             uint32_t group = 0;
             for (int t = first; t < total; t += step) {
                 const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
-                const int last = tile.blk0 + tile.blks;
-                for (int g0 = tile.blk0 / kScaleBlocks * kScaleBlocks; g0 < last; g0 += kScaleBlocks, ++group) {
-                    const int from = max(tile.blk0 - g0, 0), to = min(last - g0, kScaleBlocks);
+                for (int done = 0; done < tile.blks; done += kScaleBlocks, ++group) {
+                    const int g0 = tile.blk0 + done, to = min(tile.blks - done, kScaleBlocks);
+                    const bool whole = g0 % kScaleBlocks == 0;  // an aligned piece of a row of scales
                     const uint32_t slot = group % kScaleSlots;
                     float4 a[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // a row or column that is not there: any scale
                         const int64_t r = tile.row0 + (int)rank * 128 + i * 32 + lane;
-                        a[i] = load_scales(p.sa + (r < p.m ? r : p.m - 1) * kb, g0, from, to, wide_a);
+                        a[i] = load_scales(p.sa + (r < p.m ? r : p.m - 1) * kb + g0, to, wide_a && whole);
                     }
                     if constexpr (B_TILES) {
-                        const auto put = [&](float* dst, int stride, float4 v) {
-                            dst[0] = v.x;
-                            dst[stride] = v.y;
-                            dst[2 * stride] = v.z;
-                            dst[3 * stride] = v.w;
-                        };
                         if (group >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (group / kScaleSlots - 1) & 1);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) put(&sh.sc.tile.a[slot][0][i * 32 + lane], 128, a[i]);
+                        for (int i = 0; i < 4; ++i) sh.sc.tile.a[slot][i * 32 + lane] = a[i];
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const int64_t n = tile.col0 + h * 128 + i * 32 + lane;
-                                a[i] = load_scales(p.sb + (n < p.n ? n : p.n - 1) * kb, g0, from, to, wide_b);
+                                a[i] = load_scales(p.sb + (n < p.n ? n : p.n - 1) * kb + g0, to, wide_b && whole);
                             }
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) put(&sh.sc.tile.b[slot][0][h * 128 + i * 32 + lane], kPairN, a[i]);
+                            for (int i = 0; i < 4; ++i) {
+                                float* dst = &sh.sc.tile.b[slot][0][h * 128 + i * 32 + lane];
+                                dst[0] = a[i].x;
+                                dst[kPairN] = a[i].y;
+                                dst[2 * kPairN] = a[i].z;
+                                dst[3 * kPairN] = a[i].w;
+                            }
                         }
                     } else {
                         // lanes 4h + j load the scale of block g0 + j, column block h
@@ -415,7 +418,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                         const float* sb = p.sb + (int64_t)tile.group * kb * nb;
                         const int j = lane & 3;
                         float c = 0.0f;
-                        if (j >= from && j < to) c = __ldg(sb + (B_KN ? (int64_t)(g0 + j) * nb + cb : cb * kb + g0 + j));
+                        if (j < to) c = __ldg(sb + (B_KN ? (int64_t)(g0 + j) * nb + cb : cb * kb + g0 + j));
                         if (group >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (group / kScaleSlots - 1) & 1);
                         __syncwarp();
 #pragma unroll
@@ -423,13 +426,9 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                             const float c0 = __shfl_sync(0xFFFFFFFFu, c, 4 * h), c1 = __shfl_sync(0xFFFFFFFFu, c, 4 * h + 1);
                             const float c2 = __shfl_sync(0xFFFFFFFFu, c, 4 * h + 2), c3 = __shfl_sync(0xFFFFFFFFu, c, 4 * h + 3);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float* dst = &sh.sc.rows[slot][0][h][i * 32 + lane];
-                                dst[0] = __fmul_rn(a[i].x, c0);
-                                dst[256] = __fmul_rn(a[i].y, c1);
-                                dst[512] = __fmul_rn(a[i].z, c2);
-                                dst[768] = __fmul_rn(a[i].w, c3);
-                            }
+                            for (int i = 0; i < 4; ++i)
+                                sh.sc.rows[slot][h][i * 32 + lane] = make_float4(__fmul_rn(a[i].x, c0), __fmul_rn(a[i].y, c1),
+                                                                                 __fmul_rn(a[i].z, c2), __fmul_rn(a[i].w, c3));
                         }
                     }
                     __syncwarp();
