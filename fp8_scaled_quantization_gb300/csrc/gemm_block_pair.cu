@@ -40,8 +40,8 @@ struct Shared {
     union {
         float4 rows[kScaleSlots][2][128];  // 128 x 128 blocks: per column half and row, row scale x column block scale
         struct {
-            float4 a[kScaleSlots][128];                              // 1 x 128 tiles: per row,
-            alignas(16) float b[kScaleSlots][kScaleBlocks][kPairN];  // and per block and column
+            float a[kScaleSlots][kScaleBlocks][128];    // 1 x 128 tiles: per block and row,
+            alignas(8) float b[kScaleSlots][kScaleBlocks][kPairN];  // and per block and column
         } tile;
     } sc;
     uint64_t full[kStages], empty[kStages];
@@ -84,55 +84,50 @@ __device__ __forceinline__ Tile locate(const GemmProblem& p, const GroupTable& g
     return r;
 }
 
-// 128 columns of one row of D from column c0 on, by plain stores (and, when
+// Which of a warp's 32 x 128 outputs the pair acc[q] of a lane holds: columns
+// col, col + 1 of row `row`.  TILES: the 16x256b order of TMEM, in which a lane
+// has 4 rows and 32 columns; else lane = row and the 128 columns in order.
+template <bool TILES>
+__device__ __forceinline__ int row_of(int q, int lane) {
+    return TILES ? (q >> 4 & 1) * 16 + (q & 1) * 8 + (lane >> 2) : lane;
+}
+template <bool TILES>
+__device__ __forceinline__ int col_of(int q, int lane) {
+    return TILES ? (q >> 5) * 64 + (q >> 1 & 7) * 8 + 2 * (lane & 3) : 2 * q;
+}
+
+// A warp's 32 x 128 outputs from (row0, c0) on, by plain stores (and, when
 // accumulating, loads): rows that a group's end cuts, unaligned outputs.
-__device__ __forceinline__ void store_row(const GemmProblem& p, const uint64_t (&acc)[64], int64_t row_at, int64_t c0) {
-    const int cols = (int)(p.n - c0 < 128 ? p.n - c0 : 128);
-    if (p.out_f32) {
-        float* d = static_cast<float*>(p.d) + row_at + c0;
-        if ((p.n & 3) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 15u) == 0) {
+template <bool TILES>
+__device__ __forceinline__ void store_direct(const GemmProblem& p, const uint64_t (&acc)[64], int lane, int64_t base,
+                                             int64_t row0, int64_t row_end, int64_t c0) {
+    const bool pairs = (p.n & 1) == 0 && (reinterpret_cast<uintptr_t>(p.d) & (p.out_f32 ? 7u : 3u)) == 0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                if (j * 4 >= cols) continue;
-                const float2 a = unpack2(acc[2 * j]), b = unpack2(acc[2 * j + 1]);
-                float4 o = make_float4(a.x, a.y, b.x, b.y);
-                float4* q = reinterpret_cast<float4*>(d) + j;
+    for (int q = 0; q < 64; ++q) {
+        const int64_t r = row0 + row_of<TILES>(q, lane), c = c0 + col_of<TILES>(q, lane);
+        if (r >= row_end || c >= p.n) continue;
+        const int64_t at = base + r * p.n + c;
+        float2 v = unpack2(acc[q]);
+        if (p.out_f32) {
+            float* d = static_cast<float*>(p.d) + at;
+            if (pairs) {
                 if (p.accumulate) {
-                    const float4 old = *q;
-                    o = make_float4(__fadd_rn(old.x, o.x), __fadd_rn(old.y, o.y), __fadd_rn(old.z, o.z),
-                                    __fadd_rn(old.w, o.w));
+                    const float2 old = *reinterpret_cast<const float2*>(d);
+                    v = make_float2(__fadd_rn(old.x, v.x), __fadd_rn(old.y, v.y));
                 }
-                *q = o;
+                *reinterpret_cast<float2*>(d) = v;
+            } else {
+                d[0] = p.accumulate ? __fadd_rn(d[0], v.x) : v.x;
+                if (c + 1 < p.n) d[1] = p.accumulate ? __fadd_rn(d[1], v.y) : v.y;
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < 128; ++j) {
-                if (j >= cols) continue;
-                const float2 a = unpack2(acc[j >> 1]);
-                const float o = j & 1 ? a.y : a.x;
-                d[j] = p.accumulate ? __fadd_rn(d[j], o) : o;
-            }
-        }
-    } else {
-        uint16_t* d = static_cast<uint16_t*>(p.d) + row_at + c0;
-        if ((p.n & 7) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 15u) == 0) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if (j * 8 >= cols) continue;
-                uint32_t o[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 a = unpack2(acc[4 * j + i]);
-                    o[i] = f32x2_to_bf16x2(a.x, a.y);
-                }
-                reinterpret_cast<uint4*>(d)[j] = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 128; ++j) {
-                if (j >= cols) continue;
-                const float2 a = unpack2(acc[j >> 1]);
-                d[j] = (uint16_t)f32x2_to_bf16x2(j & 1 ? a.y : a.x, 0.0f);
+            uint16_t* d = static_cast<uint16_t*>(p.d) + at;
+            const uint32_t o = f32x2_to_bf16x2(v.x, v.y);
+            if (pairs) {
+                *reinterpret_cast<uint32_t*>(d) = o;
+            } else {
+                d[0] = (uint16_t)o;
+                if (c + 1 < p.n) d[1] = (uint16_t)(o >> 16);
             }
         }
     }
@@ -140,11 +135,11 @@ __device__ __forceinline__ void store_row(const GemmProblem& p, const uint64_t (
 
 // The same for a warp whose 32 rows are all in the group: staged in shared
 // memory 128 bytes of each row at a time (16-byte pieces swizzled, so that the
-// stores spread over all banks) and written by the bulk-copy engine, which
+// stores spread over the banks) and written by the bulk-copy engine, which
 // drops what lies outside D.
-__device__ __forceinline__ void store_rows_bulk(const GemmProblem& p, const CUtensorMap* map, const uint64_t (&acc)[64],
-                                                uint32_t stage, int lane, int64_t row, int64_t c0, int z) {
-    constexpr int kRowPairs = 64;
+template <bool TILES>
+__device__ __forceinline__ void store_bulk(const GemmProblem& p, const CUtensorMap* map, const uint64_t (&acc)[64],
+                                           uint32_t stage, int lane, int64_t row0, int64_t c0, int z) {
 #pragma unroll
     for (int part = 0; part < 4; ++part) {
         if (part >= 2 && !p.out_f32) break;
@@ -152,33 +147,56 @@ __device__ __forceinline__ void store_rows_bulk(const GemmProblem& p, const CUte
         if (x >= p.n) break;
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the staging is free
         __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t o[4];
+        if constexpr (TILES) {
             if (p.out_f32) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 a = unpack2(acc[(part * 16 + 2 * j + i) % kRowPairs]);
-                    o[2 * i] = __float_as_uint(a.x);
-                    o[2 * i + 1] = __float_as_uint(a.y);
+                for (int i = 0; i < 16; ++i) {  // 4 column blocks of 8, 4 rows
+                    const int q = (part >> 1) * 32 + (i >> 1 & 1) * 16 + ((part & 1) * 4 + (i >> 2)) * 2 + (i & 1);
+                    const int r = row_of<true>(q, lane), at = (col_of<true>(q, lane) & 31) * 4;
+                    asm volatile("st.shared.b64 [%0], %1;" ::"r"(stage + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15)),
+                                 "l"(acc[q])
+                                 : "memory");
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 a = unpack2(acc[(part * 32 + 4 * j + i) % kRowPairs]);
-                    o[i] = f32x2_to_bf16x2(a.x, a.y);
+                for (int i = 0; i < 32; ++i) {  // 8 column blocks of 8, 4 rows
+                    const int q = (part & 1) * 32 + i;
+                    const int r = row_of<true>(q, lane), at = (col_of<true>(q, lane) & 63) * 2;
+                    const float2 v = unpack2(acc[q]);
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15)),
+                                 "r"(f32x2_to_bf16x2(v.x, v.y))
+                                 : "memory");
                 }
             }
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((j ^ (lane & 7)) << 4)),
-                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                         : "memory");
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t o[4];
+                if (p.out_f32) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 a = unpack2(acc[part * 16 + 2 * j + i]);
+                        o[2 * i] = __float_as_uint(a.x);
+                        o[2 * i + 1] = __float_as_uint(a.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 a = unpack2(acc[(part & 1) * 32 + 4 * j + i]);
+                        o[i] = f32x2_to_bf16x2(a.x, a.y);
+                    }
+                }
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                             : "memory");
+            }
         }
         fence_to_async();
         __syncwarp();
         if (lane == 0) {
             asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                              reinterpret_cast<uint64_t>(map)),
-                         "r"((int)x), "r"((int)row), "r"(z), "r"(stage)
+                         "r"((int)x), "r"((int)row0), "r"(z), "r"(stage)
                          : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
@@ -195,23 +213,6 @@ __device__ __forceinline__ float4 load_scales(const float* at, int to, bool wide
     if (to > 2) r.z = __ldg(at + 2);
     if (to > 3) r.w = __ldg(at + 3);
     return r;
-}
-
-// acc += s * P for one piece of columns.
-template <bool B_TILES, int COLS>
-__device__ __forceinline__ void scale_add(uint64_t* acc, const uint32_t (&v)[COLS], uint64_t s2, uint32_t sb) {
-#pragma unroll
-    for (int j = 0; j < COLS / 2; j += 2) {
-        uint64_t x = pack2(v[2 * j], v[2 * j + 1]), y = pack2(v[2 * j + 2], v[2 * j + 3]);
-        if constexpr (B_TILES) {
-            uint64_t s0, s1;  // scales of columns 2j .. 2j + 3
-            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(s0), "=l"(s1) : "r"(sb + 8 * j));
-            x = mul2(x, s0);
-            y = mul2(y, s1);
-        }
-        acc[j] = fma2(x, s2, acc[j]);
-        acc[j + 1] = fma2(y, s2, acc[j + 1]);
-    }
 }
 
 // FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: both
@@ -269,71 +270,92 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             for (int i = 0; i < 64; ++i) acc[i] = 0;
             float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s4_next = s4;
             uint32_t slot = 0;
-            // this row's scales of the next group of blocks; they live in registers from here on
+            // the next group of scales is there; 128 x 128 blocks: this row's four live in registers from here on
             const auto fetch = [&]() {
                 slot = group % kScaleSlots;
                 w.wait(smem_addr(&sh.sc_full[slot]), (group / kScaleSlots) & 1);
                 __syncwarp();
-                if constexpr (B_TILES) {
-                    s4_next = sh.sc.tile.a[slot][row];
-                } else {
+                if constexpr (!B_TILES) {
                     s4_next = sh.sc.rows[slot][half][row];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
                 }
                 ++group;
             };
+            const auto release = [&]() {  // 1 x 128 tiles: every lane has read the group
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
+            };
             if (!B_TILES && tile.blks > 0) fetch();
             bool ready = false;
             for (int b = 0; b < tile.blks; ++b) {
                 const uint32_t buf = it & 1, from = lanes + buf * kPairN;
-                if (b % kScaleBlocks == 0) {
-                    if constexpr (B_TILES) {
-                        if (b > 0) {  // every lane is done with the last group's column scales
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
-                        }
-                        fetch();
-                    }
-                    s4 = s4_next;
-                } else {
-                    s4.x = s4.y;
-                    s4.y = s4.z;
-                    s4.z = s4.w;
+                const int sub = b % kScaleBlocks;
+                if (B_TILES && sub == 0) fetch();
+                if (!B_TILES) {
+                    s4 = sub == 0 ? s4_next : make_float4(s4.y, s4.z, s4.w, 0.0f);
                 }
-                const uint64_t s2 = pack2(s4.x, s4.x);
-                const uint32_t sb = B_TILES ? smem_addr(&sh.sc.tile.b[slot][b % kScaleBlocks][half * 128]) : 0;
                 if (!ready) w.wait(full0 + buf * 8, (it >> 1) & 1);
                 __syncwarp();  // lanes may have left the wait apart
                 tmem_fence_after();
                 ++it;
-                constexpr int kPiece = B_TILES ? 16 : 32;  // (the column scales take registers too)
-                uint32_t v[kPiece];
+                const auto read = [&]() {  // the buffer has been read
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) cluster_arrive<false>(empty0 + buf * 8);
+                    ready = b + 1 < tile.blks && Waiter::test(full0 + (it & 1) * 8, (it >> 1) & 1);
+                };
+                uint32_t v[32];
+                if constexpr (B_TILES) {
+                    uint64_t sr[4];  // this lane's four rows
 #pragma unroll
-                for (int c = 0; c < 128 / kPiece; ++c) {
-                    tmem_ld(from + c * kPiece, v);
-                    tmem_wait_ld();
-                    if (c == 128 / kPiece - 1) {  // the buffer has been read
-                        tmem_fence_before();
-                        __syncwarp();
-                        if (lane == 0) cluster_arrive<false>(empty0 + buf * 8);
-                        ready = b + 1 < tile.blks && Waiter::test(full0 + (it & 1) * 8, (it >> 1) & 1);
+                    for (int i = 0; i < 4; ++i) {
+                        const float f = sh.sc.tile.a[slot][sub][(warp & 3) * 32 + i * 8 + (lane >> 2)];
+                        sr[i] = pack2(f, f);
                     }
-                    scale_add<B_TILES>(acc + c * kPiece / 2, v, s2, sb + c * kPiece * 4);
-                    if (c == 1 && !B_TILES && b % kScaleBlocks == 2 && b + 2 < tile.blks) fetch();
+                    const float2* const sb = reinterpret_cast<const float2*>(&sh.sc.tile.b[slot][sub][half * 128]) + (lane & 3);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint64_t sc[8];  // and eight of its column pairs
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 f = sb[h * 32 + i * 4];
+                            sc[i] = pack2(f.x, f.y);
+                        }
+#pragma unroll
+                        for (int rh = 0; rh < 2; ++rh) {
+                            tmem_ld_16x64(from + ((uint32_t)(rh * 16) << 16) + h * 64, v);
+                            tmem_wait_ld();
+                            if (h + rh == 2) read();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                uint64_t* const at = acc + h * 32 + rh * 16 + i * 2;
+                                at[0] = fma2(mul2(pack2(v[4 * i], v[4 * i + 1]), sc[i]), sr[rh * 2], at[0]);
+                                at[1] = fma2(mul2(pack2(v[4 * i + 2], v[4 * i + 3]), sc[i]), sr[rh * 2 + 1], at[1]);
+                            }
+                        }
+                    }
+                    if (sub == kScaleBlocks - 1 || b == tile.blks - 1) release();
+                } else {
+                    const uint64_t s2 = pack2(s4.x, s4.x);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_ld_32x32(from + c * 32, v);
+                        tmem_wait_ld();
+                        if (c == 3) read();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            acc[c * 16 + j] = fma2(pack2(v[2 * j], v[2 * j + 1]), s2, acc[c * 16 + j]);
+                        if (c == 1 && sub == 2 && b + 2 < tile.blks) fetch();
+                    }
                 }
             }
-            if (B_TILES && tile.blks > 0) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
-            }
-            // store: this thread's row, 128 columns
-            const int64_t r = tile.row0 + (int)rank * 128 + row, c0 = tile.col0 + half * 128;
-            if (bulk_store && r - lane + 31 < tile.row_end) {
-                store_rows_bulk(p, &map_d, acc, smem_addr(out) + warp * kOutBytes, lane, r - lane, c0,
-                                RAGGED_K ? tile.group : 0);
-            } else if (r < tile.row_end && c0 < p.n) {
-                store_row(p, acc, (RAGGED_K ? (int64_t)tile.group * p.m * p.n : 0) + r * p.n, c0);
+            // store: this warp's 32 rows, 128 columns
+            const int64_t r0 = tile.row0 + (int)rank * 128 + (warp & 3) * 32, c0 = tile.col0 + half * 128;
+            if (bulk_store && r0 + 31 < tile.row_end) {
+                store_bulk<B_TILES>(p, &map_d, acc, smem_addr(out) + warp * kOutBytes, lane, r0, c0, RAGGED_K ? tile.group : 0);
+            } else {
+                store_direct<B_TILES>(p, acc, lane, RAGGED_K ? (int64_t)tile.group * p.m * p.n : 0, r0, tile.row_end, c0);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -395,7 +417,13 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                     if constexpr (B_TILES) {
                         if (group >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (group / kScaleSlots - 1) & 1);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sh.sc.tile.a[slot][i * 32 + lane] = a[i];
+                        for (int i = 0; i < 4; ++i) {
+                            float* dst = &sh.sc.tile.a[slot][0][i * 32 + lane];
+                            dst[0] = a[i].x;
+                            dst[128] = a[i].y;
+                            dst[256] = a[i].z;
+                            dst[384] = a[i].w;
+                        }
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
 #pragma unroll
