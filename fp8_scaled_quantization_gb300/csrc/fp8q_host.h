@@ -31,10 +31,12 @@ int sm_count();
 fp8_status_t encode_tile_map_u16(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows,
                                  int box_cols);
 
-// Tensor map of `groups` row-major [rows, inner] matrices of bytes, one after
-// another (16-byte aligned base, inner a multiple of 16), read as 128 x 128
-// tiles in the 128-byte swizzle of the tensor core's operands.
-fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups);
+// Tensor map of `groups` row-major [rows, inner] matrices of bytes, `stride`
+// bytes from row to row and rows * stride from matrix to matrix (16-byte
+// aligned base, stride a multiple of 16), read as 128 x 128 tiles in the
+// 128-byte swizzle of the tensor core's operands.
+fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t stride, int64_t rows,
+                                int64_t groups);
 
 // Tensor map of `groups` row-major [rows, cols] outputs, one after another
 // (16-byte aligned base and rows), written as 32 rows of 128 bytes in the same
@@ -50,6 +52,12 @@ fp8_status_t gemm_pair_wait_timeouts(unsigned long long* count);
 // Workspace of (current device, stream) for per-CTA partials; nullptr on
 // failure (the error message is set).
 Workspace* stream_workspace(cudaStream_t stream, fp8_status_t* st);
+
+// At least `bytes` bytes of scratch of (current device, stream), 256-byte
+// aligned, kept for later calls on the stream; a larger request allocates anew
+// and leaves the smaller one to those who captured its address.  nullptr on
+// failure (the error message is set).
+void* stream_scratch(cudaStream_t stream, size_t bytes, fp8_status_t* st);
 
 // Launch `kernel` on `st` with `smem` bytes of dynamic shared memory and
 // programmatic stream serialization allowed (the kernel starts with

@@ -245,57 +245,6 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, i
             : "memory");
 }
 
-// The generic form of the same load, by THREADS threads (t: 0 ..) with plain
-// loads and shared stores: bytes of rows below `row_hi` and columns in
-// [x_lo, x_hi), zero elsewhere.  `base` .. `base_end` are the matrix's own
-// bytes: nothing outside is read.  Any alignment.
-struct TileSource {
-    const uint8_t* base;
-    const uint8_t* base_end;
-    int64_t stride;  // bytes from row to row
-};
-
-__device__ __forceinline__ uint4 load_piece(const TileSource& s, int64_t at, int lo, int hi) {
-    const uint8_t* p = s.base + at;
-    if (lo == 0 && hi == 16) {
-        const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3u);
-        if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
-        const uint8_t* w = p - off;
-        if (w >= s.base && w + 16 + (off ? 4 : 0) <= s.base_end) {
-            uint32_t v[5];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint32_t*>(w) + i);
-            v[4] = off ? __ldg(reinterpret_cast<const uint32_t*>(w) + 4) : 0u;
-            const uint32_t sh = off * 8;
-            return make_uint4(__funnelshift_r(v[0], v[1], sh), __funnelshift_r(v[1], v[2], sh),
-                              __funnelshift_r(v[2], v[3], sh), __funnelshift_r(v[3], v[4], sh));
-        }
-    }
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i >= lo && i < hi) v[i >> 2] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
-    return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-template <int THREADS>
-__device__ __forceinline__ void load_tile(uint32_t dst, const TileSource& s, int64_t x0, int64_t x_lo, int64_t x_hi,
-                                          int64_t row0, int64_t row_hi, int t) {
-    static_assert(THREADS % 8 == 0, "a thread keeps its piece");
-    const int piece = t & 7;
-    const int64_t x = x0 + piece * 16;
-    const int lo = x_lo > x ? (int)(x_lo - x < 16 ? x_lo - x : 16) : 0;
-    const int hi = x_hi < x + 16 ? (int)(x_hi > x ? x_hi - x : 0) : 16;
-#pragma unroll 4
-    for (int r = t >> 3; r < 128; r += THREADS / 8) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (row0 + r < row_hi && lo < hi) v = load_piece(s, (row0 + r) * s.stride + x, lo, hi);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + r * 128 + ((piece ^ (r & 7)) << 4)),
-                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
-    }
-}
-
 // Shared-memory writes of this thread become visible to the tensor core.
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

@@ -1,5 +1,5 @@
 // gemm_block.cu -- block-scaled FP8 products: the C entry points, their checks,
-// and the guarded kernel that takes every shape and alignment.
+// and the copy that aligns odd operands.
 //
 // "Megatron FP8" §6 (forward, dgrad and wgrad GEMMs over FP8 operands), "Low
 // Precision Training and Rollout" (128x128 weight blocks), "[Pytorch][Common]
@@ -11,119 +11,39 @@
 namespace fp8q {
 namespace {
 
-// ------------------------------------------------------------ guarded kernel
-//
-// One 64 x 64 tile of D per CTA and step; 256 threads of 4 x 4 outputs each,
-// operands decoded to fp32 in shared memory 32 contraction steps at a time.
-// Every 128 steps the block's partial sum is multiplied by the block's scales
-// and added, so partial sums and totals are both fp32.  Loads are single bytes
-// behind bounds checks: any size and alignment.
-constexpr int kTile = 64, kStep = 32, kThreads = 256;
+// Rows of `inner` bytes copied to rows of `stride` bytes (a multiple of 16, the
+// rest zeros), one 16-byte piece per lane and step.  Sources start anywhere: a
+// piece is cut out of the aligned 4-byte words around it, or put together from
+// single bytes at the array's two ends, so that nothing outside is read.
+constexpr int kPackThreads = 256;
 
-__device__ __forceinline__ float decode(int fmt, uint32_t code) {
-    const uint32_t h = fmt == kE4M3 ? fp8x2_to_f16x2<kE4M3>(code) : fp8x2_to_f16x2<kE5M2>(code);
-    return f16_lo_to_f32(h);
-}
-
-template <bool RAGGED_K>
-__global__ void __launch_bounds__(kThreads) gemm_guarded_kernel(const __grid_constant__ GemmProblem p) {
-    __shared__ GroupTable groups;
-    __shared__ float as[kStep][kTile + 1], bs[kStep][kTile + 1];
+__global__ void __launch_bounds__(kPackThreads)
+align_rows_kernel(const uint8_t* __restrict__ src, int64_t rows, int64_t inner, uint8_t* __restrict__ dst, int64_t stride) {
     pdl_begin();
-    const int tiles_m = (int)((p.m + kTile - 1) / kTile), tiles_n = (int)((p.n + kTile - 1) / kTile);
-    const int count = RAGGED_K ? p.groups : p.groups + 1;
-    const int total = build_groups(&groups, p.ends, p.groups, RAGGED_K ? p.k : p.m, kTile, RAGGED_K ? p.m : 0, tiles_n);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t kb_all = blocks_of(p.k), nb_all = blocks_of(p.n);
-    (void)tiles_m;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        const int e = find_group(&groups, count, t);
-        const int local = t - groups.tile[e];
-        const int begin = e > 0 ? groups.end[e - 1] : 0, end = groups.end[e];
-        const int64_t row0 = (RAGGED_K ? 0 : begin) + (int64_t)(local / tiles_n) * kTile;
-        const int64_t row_end = RAGGED_K ? p.m : end;
-        const int64_t col0 = (int64_t)(local % tiles_n) * kTile;
-        const int64_t k_lo = RAGGED_K ? begin : 0, k_hi = RAGGED_K ? end : (e < p.groups ? p.k : 0);
-        const uint8_t* b = p.b + (RAGGED_K ? 0 : (int64_t)e * p.n * p.k);
-        const float* sb = p.sb + (RAGGED_K ? 0 : (int64_t)e * (p.b_tiles ? p.n : nb_all) * kb_all);
-        float acc[4][4] = {};
-        for (int64_t blk = k_lo / kBlk; blk * kBlk < k_hi; ++blk) {
-            float part[4][4] = {};
-            for (int64_t k0 = blk * kBlk; k0 < (blk + 1) * kBlk && k0 < k_hi; k0 += kStep) {
-                __syncthreads();
-                for (int i = threadIdx.x; i < kStep * kTile; i += kThreads) {
-                    {
-                        const int kk = i % kStep, r = i / kStep;
-                        const int64_t k = k0 + kk, row = row0 + r;
-                        const bool in = row < row_end && k >= k_lo && k < k_hi;
-                        as[kk][r] = in ? decode(p.fmt_a, p.a[row * p.k + k]) : 0.0f;
-                    }
-                    if (p.b_kn) {
-                        const int kk = i / kTile, c = i % kTile;
-                        const int64_t k = k0 + kk, col = col0 + c;
-                        bs[kk][c] = col < p.n && k < k_hi ? decode(p.fmt_b, b[k * p.n + col]) : 0.0f;
-                    } else {
-                        const int kk = i % kStep, c = i / kStep;
-                        const int64_t k = k0 + kk, col = col0 + c;
-                        const bool in = col < p.n && k >= k_lo && k < k_hi;
-                        bs[kk][c] = in ? decode(p.fmt_b, b[col * p.k + k]) : 0.0f;
-                    }
-                }
-                __syncthreads();
-#pragma unroll 8
-                for (int kk = 0; kk < kStep; ++kk) {
-                    float av[4], bv[4];
+    const uint8_t* const end = src + rows * inner;
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * (kPackThreads / 32);
+    for (int64_t r = (int64_t)blockIdx.x * (kPackThreads / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
+#pragma unroll 4
+        for (int64_t x = lane * 16; x < stride; x += 512) {
+            const uint8_t* p = src + r * inner + x;
+            const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3u);
+            const uint8_t* w = p - off;
+            uint32_t v[5] = {0u, 0u, 0u, 0u, 0u};
+            if (x + 16 <= inner && w >= src && w + 20 <= end) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) av[i] = as[kk][ty + 16 * i];
+                for (int i = 0; i < 5; ++i) v[i] = __ldg(reinterpret_cast<const uint32_t*>(w) + i);
+                const uint32_t sh = off * 8;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) bv[j] = bs[kk][tx + 16 * j];
+                for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], sh);
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) part[i][j] = __fmaf_rn(av[i], bv[j], part[i][j]);
-                }
+                for (int i = 0; i < 16; ++i)
+                    if (x + i < inner) v[i >> 2] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t row = row0 + ty + 16 * i;
-                const float sa = row < row_end ? p.sa[row * kb_all + blk] : 0.0f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t col = col0 + tx + 16 * j;
-                    if (row >= row_end || col >= p.n) continue;
-                    const float s = p.b_tiles ? sb[col * kb_all + blk]
-                                    : p.b_kn  ? sb[blk * nb_all + col / kBlk]
-                                              : sb[col / kBlk * kb_all + blk];
-                    acc[i][j] = __fmaf_rn(part[i][j], __fmul_rn(sa, s), acc[i][j]);
-                }
-            }
-        }
-        const int64_t d0 = RAGGED_K ? (int64_t)e * p.m * p.n : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t row = row0 + ty + 16 * i, col = col0 + tx + 16 * j;
-                if (row >= row_end || col >= p.n) continue;
-                const int64_t at = d0 + row * p.n + col;
-                if (p.out_f32) {
-                    float* d = static_cast<float*>(p.d) + at;
-                    *d = p.accumulate ? __fadd_rn(*d, acc[i][j]) : acc[i][j];
-                } else {
-                    static_cast<uint16_t*>(p.d)[at] = (uint16_t)f32x2_to_bf16x2(acc[i][j], 0.0f);
-                }
-            }
+            stg_stream(dst + r * stride + x, make_uint4(v[0], v[1], v[2], v[3]));
         }
     }
-}
-
-fp8_status_t run_guarded(const char* fn, const GemmProblem& p, bool ragged_k, cudaStream_t st) {
-    const int64_t tiles_n = (p.n + kTile - 1) / kTile;
-    const int64_t tiles_m = ragged_k ? (p.m + kTile - 1) / kTile * p.groups : (p.m + kTile - 1) / kTile + p.groups;
-    const int64_t tiles = tiles_m * tiles_n, most = (int64_t)sm_count() * 6;
-    const dim3 grid((unsigned)(tiles < most ? tiles : most)), block(kThreads);
-    return ragged_k ? launch(fn, gemm_guarded_kernel<true>, grid, block, st, p)
-                    : launch(fn, gemm_guarded_kernel<false>, grid, block, st, p);
 }
 
 fp8_status_t check(const char* fn, const GemmProblem& p, int layout, int b_block_rows, int out_dtype) {
@@ -137,7 +57,7 @@ fp8_status_t check(const char* fn, const GemmProblem& p, int layout, int b_block
         return fail(FP8_ERR_UNSUPPORTED, "%s: 1x128 tiles of B run along the contraction: B must be [n, k]", fn);
     if (p.accumulate && out_dtype != FP8_DT_FP32)
         return fail(FP8_ERR_UNSUPPORTED, "%s: accumulate needs an fp32 output", fn);
-    constexpr int64_t kMost = (1ll << 31) - 256;
+    constexpr int64_t kMost = (1ll << 31) - 256, kTile = 64;
     if (p.m > kMost || p.n > kMost || p.k > kMost)
         return fail(FP8_ERR_UNSUPPORTED, "%s: sizes must be below 2^31 - 256", fn);
     // tiles are numbered with 32 bits
@@ -167,6 +87,40 @@ fp8_status_t check_groups(const char* fn, int groups, const int64_t* ends) {
 }
 
 }  // namespace
+
+fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, const Operand& b, CUtensorMap* map_b,
+                          cudaStream_t st) {
+    const Operand* const in[2] = {&a, &b};
+    CUtensorMap* const map[2] = {map_a, map_b};
+    size_t need[2];
+    for (int i = 0; i < 2; ++i) {
+        const bool fits = aligned16(in[i]->codes) && in[i]->inner % 16 == 0;
+        need[i] = fits ? 0 : (size_t)((in[i]->inner + 15) / 16 * 16) * (size_t)(in[i]->rows * in[i]->groups);
+    }
+    fp8_status_t s = FP8_OK;
+    uint8_t* scratch = nullptr;
+    if (need[0] + need[1] > 0) {
+        scratch = static_cast<uint8_t*>(stream_scratch(st, need[0] + need[1], &s));
+        if (scratch == nullptr) return s;
+    }
+    for (int i = 0; i < 2; ++i) {
+        const Operand& o = *in[i];
+        const int64_t stride = (o.inner + 15) / 16 * 16, rows = o.rows * o.groups;
+        const uint8_t* base = o.codes;
+        if (need[i] > 0) {
+            const int64_t ctas = (rows + kPackThreads / 32 - 1) / (kPackThreads / 32), most = (int64_t)sm_count() * 16;
+            s = launch(fn, align_rows_kernel, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kPackThreads), st, o.codes,
+                       rows, o.inner, scratch, stride);
+            if (s != FP8_OK) return s;
+            base = scratch;
+            scratch += need[i];
+        }
+        s = encode_tile_map_u8(map[i], base, o.inner, stride, o.rows, o.groups);
+        if (s != FP8_OK) return s;
+    }
+    return FP8_OK;
+}
+
 }  // namespace fp8q
 
 using namespace fp8q;
@@ -180,7 +134,7 @@ extern "C" fp8_status_t fp8_gemm_block(const uint8_t* a, fp8_format_t fmt_a, con
                            b_layout == FP8_B_KN, b_block_rows == 1, out_dtype == FP8_DT_FP32, accumulate != 0};
     const fp8_status_t s = check(fn, p, b_layout, b_block_rows, out_dtype);
     if (s != FP8_OK || m == 0 || n == 0 || (k == 0 && p.accumulate)) return s;
-    return p.k > 0 ? run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream)) : run_guarded(fn, p, false, static_cast<cudaStream_t>(stream));
+    return run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" fp8_status_t fp8_gemm_block_grouped(int groups, const int64_t* group_ends, const uint8_t* a,
@@ -195,7 +149,7 @@ extern "C" fp8_status_t fp8_gemm_block_grouped(int groups, const int64_t* group_
                            b_layout == FP8_B_KN, false, out_dtype == FP8_DT_FP32, false};
     s = check(fn, p, b_layout, kBlk, out_dtype);
     if (s != FP8_OK || rows == 0 || n == 0) return s;
-    return p.k > 0 ? run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream)) : run_guarded(fn, p, false, static_cast<cudaStream_t>(stream));
+    return run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" fp8_status_t fp8_gemm_block_grouped_wgrad(int groups, const int64_t* group_ends, const uint8_t* a,
@@ -210,5 +164,5 @@ extern "C" fp8_status_t fp8_gemm_block_grouped_wgrad(int groups, const int64_t* 
                            false, true, out_dtype == FP8_DT_FP32, accumulate != 0};
     s = check(fn, p, FP8_B_NK, 1, out_dtype);
     if (s != FP8_OK || m == 0 || n == 0 || (rows == 0 && p.accumulate)) return s;
-    return p.k > 0 ? run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream)) : run_guarded(fn, p, true, static_cast<cudaStream_t>(stream));
+    return run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream));
 }

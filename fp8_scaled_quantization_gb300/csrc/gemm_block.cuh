@@ -35,6 +35,18 @@ struct GemmProblem {
     bool accumulate; // D += (fp32 only)
 };
 
+// One operand as stored: `groups` row-major [rows, inner] matrices of codes.
+struct Operand {
+    const uint8_t* codes;
+    int64_t inner, rows, groups;
+};
+
+// Tensor maps of the operands of one product.  The bulk copies need 16-byte
+// aligned rows: an operand whose base or row length is not is first copied
+// into the stream's scratch with its rows a multiple of 16 apart.
+fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, const Operand& b, CUtensorMap* map_b,
+                          cudaStream_t st);
+
 // gemm_block_pair.cu: 256 x 256 outputs per CTA pair.
 fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st);
 

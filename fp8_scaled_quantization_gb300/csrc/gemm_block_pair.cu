@@ -10,9 +10,8 @@
 //
 // Roles per CTA of 384 threads: warps 0-7 scale and add, then store; warp 8 of
 // the pair's first CTA issues the products for both; warp 9 gathers the scales;
-// warps 10 and 11 fill the ring of operand tiles (one thread issuing bulk
-// copies, or both warps with plain loads where sizes or addresses are not
-// multiples of 16, or where a ragged group's end cuts a block).
+// warp 10 fills the ring of operand tiles by bulk copies; warp 11 zeroes the
+// steps of other groups in blocks that a ragged group's end cuts.
 //
 // What bounds it: a warp's arithmetic takes 146 of the 512 cycles that the
 // tensor core needs for a block, and two warps share a scheduler, so the
@@ -27,7 +26,7 @@
 namespace fp8q {
 namespace {
 
-constexpr int kThreads = 384, kLoaders = 64;
+constexpr int kThreads = 384;
 constexpr int kPairM = 256, kPairN = 256;  // outputs of a pair
 constexpr int kStages = 5;                 // operand ring: A and B tile, 32 KB per CTA and stage
 constexpr int kScaleBlocks = 4;            // blocks of a tile whose scales are gathered together
@@ -44,7 +43,7 @@ struct Shared {
             alignas(8) float b[kScaleSlots][kScaleBlocks][kPairN];  // and per block and column
         } tile;
     } sc;
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages], empty[kStages], landed[kStages];
     uint64_t tmem_full[2], tmem_empty[2];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint32_t tmem;
@@ -82,6 +81,42 @@ __device__ __forceinline__ Tile locate(const GemmProblem& p, const GroupTable& g
     r.blk0 = r.k_hi > r.k_lo ? r.k_lo / kBlk : 0;
     r.blks = r.k_hi > r.k_lo ? (r.k_hi + kBlk - 1) / kBlk - r.blk0 : 0;
     return r;
+}
+
+// Whether the block at step x holds steps of other groups (beyond the last step
+// the bulk copy fills with zeros itself).
+__device__ __forceinline__ bool is_cut(const Tile& t, int x, int k) {
+    return x < t.k_lo || (x + kBlk > t.k_hi && t.k_hi < k);
+}
+
+// Zeroes the bytes outside [lo, hi) of every row of a K-major tile, by one warp.
+__device__ __forceinline__ void mask_tile(uint32_t tile, int lo, int hi, int lane) {
+    const int piece = lane & 7, from = max(lo - piece * 16, 0), to = min(hi - piece * 16, 16);
+    if (from <= 0 && to >= 16) return;
+    uint32_t keep[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        keep[w] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * w + i >= from && 4 * w + i < to) keep[w] |= 0xFFu << (8 * i);
+    }
+    const bool some = (keep[0] | keep[1] | keep[2] | keep[3]) != 0;
+#pragma unroll 4
+    for (int r = lane >> 3; r < 128; r += 4) {
+        const uint32_t at = tile + r * 128 + ((piece ^ (r & 7)) << 4);
+        uint32_t v[4] = {0u, 0u, 0u, 0u};
+        if (some) {
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(at)
+                         : "memory");
+#pragma unroll
+            for (int w = 0; w < 4; ++w) v[w] &= keep[w];
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                     : "memory");
+    }
 }
 
 // Which of a warp's 32 x 128 outputs the pair acc[q] of a lane holds: columns
@@ -216,9 +251,8 @@ __device__ __forceinline__ float4 load_scales(const float* at, int to, bool wide
 }
 
 // FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: both
-// operands in 1 x 128 tiles, contraction ragged.  TMA: operand tiles by the
-// bulk-copy engine (except blocks that a group end cuts).
-template <int FORM, bool TMA>
+// operands in 1 x 128 tiles, contraction ragged.
+template <int FORM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ CUtensorMap map_a,
                  const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d, bool bulk_store) {
@@ -234,6 +268,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 2);   // one arrival per CTA of the pair
             mbar_init(&sh.empty[i], 1);  // the products' commit
+            mbar_init(&sh.landed[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.tmem_full[i], 1);
@@ -374,9 +409,8 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                         const uint32_t buf = it & 1, free_bar = smem_addr(&sh.tmem_empty[buf]), free_phase = ((it >> 1) & 1) ^ 1;
                         const uint64_t at = a0 + stage * (kStageBytes >> 4), bt = b0 + stage * (kStageBytes >> 4);
                         const bool is_free = it < 2 || Waiter::test(free_bar, free_phase);
-                        // tiles written with plain stores are released to the cluster
-                        if constexpr (TMA && !RAGGED_K) w.wait(smem_addr(&sh.full[stage]), phase);
-                        else w.template wait<true>(smem_addr(&sh.full[stage]), phase);
+                        // (tiles that were masked with plain stores are released to the cluster)
+                        w.template wait<RAGGED_K>(smem_addr(&sh.full[stage]), phase);
                         if (!is_free) w.wait(free_bar, free_phase);
                         __syncwarp();
                         tmem_fence_after();
@@ -463,53 +497,57 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                     if (lane == 0) mbar_arrive(&sh.sc_full[slot]);
                 }
             }
-        } else {
+        } else if (warp == 10) {
             // ---- operand tiles: A rows [row0 + 128 rank, ..), B columns [col0 + 128 rank, ..)
-            const int tid = threadIdx.x - (kThreads - kLoaders);
             const uint32_t base = smem_addr(tiles), full0 = cluster_addr(smem_addr(&sh.full[0]), 0);
             uint32_t it = 0, stage = 0, phase = 0;
-            // with bulk copies alone, one warp is enough
-            if (!TMA || RAGGED_K || warp == 10) {
-                for (int t = first; t < total; t += step) {
-                    const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
-                    const int row = tile.row0 + (int)rank * 128, col = tile.col0 + (int)rank * 128;
-                    for (int b = 0; b < tile.blks; ++b, ++it) {
-                        const uint32_t a = base + stage * kStageBytes, bt = a + kTileBytes, bar = full0 + stage * 8;
-                        const int x = (tile.blk0 + b) * kBlk;
-                        // a block that a group's end cuts holds other groups' codes too: masked loads
-                        const bool cut = RAGGED_K && (x < tile.k_lo || (x + kBlk > tile.k_hi && tile.k_hi < p.k));
-                        if (warp == 10 && it >= kStages) w.wait(smem_addr(&sh.empty[stage]), phase ^ 1);
-                        __syncwarp();  // lanes may have left the wait apart
-                        if (TMA && !cut) {
-                            if (warp == 10 && elect_one()) {
-                                cluster_arrive_expect_tx(bar, kStageBytes);
-                                tma_tile<true>(a, &map_a, x, row, 0, bar);
-                                if constexpr (B_KN) tma_tile<true>(bt, &map_b, col, x, tile.group, bar);
-                                else tma_tile<true>(bt, &map_b, x, col, RAGGED_K ? 0 : tile.group, bar);
-                            }
-                        } else {
-                            group_sync(1, kLoaders);  // the stage is free
-                            const TileSource as = {p.a, p.a + p.m * p.k, p.k};
-                            load_tile<kLoaders>(a, as, x, tile.k_lo, tile.k_hi, row, p.m, tid);
-                            const int64_t weight = RAGGED_K ? 0 : (int64_t)tile.group * p.n * p.k;
-                            const TileSource bs = {p.b + weight, p.b + weight + p.n * p.k, B_KN ? p.n : p.k};
-                            if constexpr (B_KN) load_tile<kLoaders>(bt, bs, col, 0, p.n, x, p.k, tid);
-                            else load_tile<kLoaders>(bt, bs, x, tile.k_lo, tile.k_hi, col, p.n, tid);
-                            fence_to_async();
-                            group_sync(1, kLoaders);  // every warp's part is written
-                            if (tid == 0) cluster_arrive<true>(bar);
-                        }
-                        __syncwarp();
-                        if (++stage == kStages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+            for (int t = first; t < total; t += step) {
+                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
+                const int row = tile.row0 + (int)rank * 128, col = tile.col0 + (int)rank * 128;
+                for (int b = 0; b < tile.blks; ++b, ++it) {
+                    const uint32_t a = base + stage * kStageBytes, bt = a + kTileBytes;
+                    const int x = (tile.blk0 + b) * kBlk;
+                    if (it >= kStages) w.wait(smem_addr(&sh.empty[stage]), phase ^ 1);
+                    __syncwarp();
+                    if (elect_one()) {
+                        // a block that needs masking lands on this CTA's own barrier first
+                        uint32_t bar = full0 + stage * 8;
+                        if (RAGGED_K && is_cut(tile, x, (int)p.k)) bar = smem_addr(&sh.landed[stage]);
+                        cluster_arrive_expect_tx(bar, kStageBytes);
+                        tma_tile<true>(a, &map_a, x, row, 0, bar);
+                        if constexpr (B_KN) tma_tile<true>(bt, &map_b, col, x, tile.group, bar);
+                        else tma_tile<true>(bt, &map_b, x, col, RAGGED_K ? 0 : tile.group, bar);
+                    }
+                    __syncwarp();
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
                     }
                 }
-                // the last fills have been read before the CTA ends
-                if (tid == 0)
-                    for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-                        w.wait(smem_addr(&sh.empty[i % kStages]), (i / kStages) & 1);
+            }
+            // the last fills have been read before the CTA ends
+            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+                w.wait(smem_addr(&sh.empty[i % kStages]), (i / kStages) & 1);
+        } else if (RAGGED_K) {
+            // ---- masking: steps of other groups become zeros, in both operands (their codes may be NaN)
+            const uint32_t base = smem_addr(tiles), full0 = cluster_addr(smem_addr(&sh.full[0]), 0);
+            uint32_t stage = 0, phases = 0;  // bit s: the phase of landed[s]
+            for (int t = first; t < total; t += step) {
+                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
+                for (int b = 0; b < tile.blks; ++b) {
+                    const int x = (tile.blk0 + b) * kBlk;
+                    if (is_cut(tile, x, (int)p.k)) {
+                        w.wait(smem_addr(&sh.landed[stage]), phases >> stage & 1);
+                        phases ^= 1u << stage;
+                        __syncwarp();
+                        mask_tile(base + stage * kStageBytes, tile.k_lo - x, tile.k_hi - x, lane);
+                        mask_tile(base + stage * kStageBytes + kTileBytes, tile.k_lo - x, tile.k_hi - x, lane);
+                        fence_to_async();
+                        __syncwarp();
+                        if (lane == 0) cluster_arrive<true>(full0 + stage * 8);
+                    }
+                    if (++stage == kStages) stage = 0;
+                }
             }
         }
         __syncwarp();
@@ -523,15 +561,12 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
 }  // namespace
 
 fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st) {
-    const int form = p.b_tiles ? 2 : p.b_kn ? 1 : 0;
     const int64_t inner_b = p.b_kn ? p.n : p.k, rows_b = p.b_kn ? p.k : p.n;
-    // the bulk copies need 16-byte aligned bases and row strides
-    const bool tma = aligned16(p.a) && aligned16(p.b) && p.k % 16 == 0 && inner_b % 16 == 0;
     const bool bulk = aligned16(p.d) && p.n % (p.out_f32 ? 4 : 8) == 0 && !p.accumulate;
+    Operand oa = {p.a, p.k, p.m, 1}, ob = {p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups};
     CUtensorMap a = {}, b = {}, d = {};
     fp8_status_t s = FP8_OK;
-    if (tma) s = encode_tile_map_u8(&a, p.a, p.k, p.m, 1);
-    if (tma && s == FP8_OK) s = encode_tile_map_u8(&b, p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups);
+    if (p.k > 0) s = operand_maps(fn, oa, &a, ob, &b, st);
     if (bulk && s == FP8_OK) s = encode_out_map(&d, p.d, p.out_f32, p.n, p.m, p.b_tiles ? p.groups : 1);
     if (s != FP8_OK) return s;
     const int64_t tiles_n = (p.n + kPairN - 1) / kPairN, tiles_m = (p.m + kPairM - 1) / kPairM;
@@ -540,9 +575,7 @@ fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st
     const auto go = [&](auto kernel) {
         return launch_smem(fn, kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, st, p, a, b, d, bulk);
     };
-    if (form == 0) return tma ? go(gemm_pair_kernel<0, true>) : go(gemm_pair_kernel<0, false>);
-    if (form == 1) return tma ? go(gemm_pair_kernel<1, true>) : go(gemm_pair_kernel<1, false>);
-    return tma ? go(gemm_pair_kernel<2, true>) : go(gemm_pair_kernel<2, false>);
+    return p.b_tiles ? go(gemm_pair_kernel<2>) : p.b_kn ? go(gemm_pair_kernel<1>) : go(gemm_pair_kernel<0>);
 }
 
 fp8_status_t gemm_pair_wait_timeouts(unsigned long long* count) {

@@ -6,6 +6,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include <cudaTypedefs.h>
 
@@ -21,6 +22,11 @@ std::atomic<unsigned long long> g_launches{0};
 std::mutex g_mu;
 std::map<int, int> g_sm_count;                                 // device -> SMs
 std::map<std::pair<int, uintptr_t>, Workspace*> g_workspaces;  // (device, stream) -> ws
+struct Scratch {
+    std::vector<void*> all;  // the last one is in use, the others may be held by captured graphs
+    size_t bytes = 0;
+};
+std::map<std::pair<int, uintptr_t>, Scratch> g_scratch;
 }  // namespace
 
 fp8_status_t fail(fp8_status_t st, const char* fmt, ...) {
@@ -89,12 +95,13 @@ fp8_status_t encode_tile_map_u16(CUtensorMap* map, const void* base, int64_t row
     return FP8_OK;
 }
 
-fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t groups) {
+fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t stride, int64_t rows,
+                                int64_t groups) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     const fp8_status_t s = tile_map_encoder(&encode);
     if (s != FP8_OK) return s;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)groups};
-    const cuuint64_t strides[2] = {(cuuint64_t)inner, (cuuint64_t)inner * (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride, (cuuint64_t)stride * (cuuint64_t)rows};
     const cuuint32_t box[3] = {128, 128, 1};
     const cuuint32_t elem_strides[3] = {1, 1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
@@ -149,6 +156,34 @@ Workspace* stream_workspace(cudaStream_t stream, fp8_status_t* st) {
     return ws;
 }
 
+void* stream_scratch(cudaStream_t stream, size_t bytes, fp8_status_t* st) {
+    *st = FP8_OK;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) {
+        *st = cuda_status(e, "cudaGetDevice");
+        return nullptr;
+    }
+    std::lock_guard<std::mutex> lk(g_mu);
+    Scratch& s = g_scratch[std::make_pair(dev, reinterpret_cast<uintptr_t>(stream))];
+    if (s.bytes >= bytes) return s.all.back();
+    // a quarter more than asked for, so that slowly growing requests do not allocate each time
+    const size_t want = (bytes + bytes / 4 + 255) & ~(size_t)255;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    void* p = nullptr;
+    e = cudaMalloc(&p, want);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) {
+        cudaGetLastError();  // the failed allocation is reported here, not by a later launch
+        *st = cuda_status(e, "cudaMalloc(scratch)");
+        return nullptr;
+    }
+    s.all.push_back(p);
+    s.bytes = want;
+    return p;
+}
+
 }  // namespace fp8q
 
 extern "C" {
@@ -185,17 +220,26 @@ fp8_status_t fp8_release_stream_workspace(void* stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_status(e, "fp8_release_stream_workspace: cudaGetDevice");
-    Workspace* ws = nullptr;
+    std::vector<void*> mine;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        auto it = g_workspaces.find(std::make_pair(dev, reinterpret_cast<uintptr_t>(stream)));
-        if (it == g_workspaces.end()) return FP8_OK;  // nothing was allocated for this stream
-        ws = it->second;
-        g_workspaces.erase(it);
+        const auto key = std::make_pair(dev, reinterpret_cast<uintptr_t>(stream));
+        if (auto it = g_workspaces.find(key); it != g_workspaces.end()) {
+            mine.push_back(it->second);
+            g_workspaces.erase(it);
+        }
+        if (auto it = g_scratch.find(key); it != g_scratch.end()) {
+            mine.insert(mine.end(), it->second.all.begin(), it->second.all.end());
+            g_scratch.erase(it);
+        }
     }
-    // The stream's queued work may still use the workspace.
+    if (mine.empty()) return FP8_OK;  // nothing was allocated for this stream
+    // The stream's queued work may still use the memory.
     e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess) e = cudaFree(ws);
+    for (void* p : mine) {
+        const cudaError_t f = cudaFree(p);
+        if (e == cudaSuccess) e = f;
+    }
     return cuda_status(e, "fp8_release_stream_workspace");
 }
 
