@@ -33,10 +33,10 @@ fp8_status_t encode_tile_map_u16(CUtensorMap* map, const void* base, int64_t row
 
 // Tensor map of `groups` row-major [rows, inner] matrices of bytes, `stride`
 // bytes from row to row and rows * stride from matrix to matrix (16-byte
-// aligned base, stride a multiple of 16), read as 128 x 128 tiles in the
-// 128-byte swizzle of the tensor core's operands.
+// aligned base, stride a multiple of 16), read as tiles of tile_rows x 128
+// bytes in the 128-byte swizzle of the tensor core's operands.
 fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t stride, int64_t rows,
-                                int64_t groups);
+                                int64_t groups, int tile_rows);
 
 // Tensor map of `groups` row-major [rows, cols] outputs, one after another
 // (16-byte aligned base and rows), written as 32 rows of 128 bytes in the same
@@ -48,6 +48,7 @@ fp8_status_t encode_out_map(CUtensorMap* map, void* base, bool f32, int64_t cols
 fp8_status_t block_ct_wait_timeouts(unsigned long long* count);
 
 fp8_status_t gemm_pair_wait_timeouts(unsigned long long* count);
+fp8_status_t gemm_stream_wait_timeouts(unsigned long long* count);
 
 // Workspace of (current device, stream) for per-CTA partials; nullptr on
 // failure (the error message is set).
@@ -98,6 +99,33 @@ fp8_status_t launch(const char* what, void (*kernel)(KArgs...), dim3 grid, dim3 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    if (e != cudaSuccess) return cuda_status(e, what);
+    return after_launch(what);
+}
+
+// launch_smem in clusters of `cluster` CTAs along x.
+template <typename... KArgs, typename... Args>
+fp8_status_t launch_cluster(const char* what, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                            cudaStream_t st, Args... args) {
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return cuda_status(e, what);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
     if (e != cudaSuccess) return cuda_status(e, what);
     return after_launch(what);

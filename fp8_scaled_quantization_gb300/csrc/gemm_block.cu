@@ -5,6 +5,8 @@
 // Precision Training and Rollout" (128x128 weight blocks), "[Pytorch][Common]
 // Hybrid quantization #2817" (1x128 / 128x1 blockwise copies for the backward
 // GEMMs), "Megatron FP8" §21 (experts).
+#include <cstdlib>
+
 #include "fp8q_host.h"
 #include "gemm_block.cuh"
 
@@ -115,11 +117,25 @@ fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, 
             base = scratch;
             scratch += need[i];
         }
-        s = encode_tile_map_u8(map[i], base, o.inner, stride, o.rows, o.groups);
+        s = encode_tile_map_u8(map[i], base, o.inner, stride, o.rows, o.groups, o.tile_rows);
         if (s != FP8_OK) return s;
     }
     return FP8_OK;
 }
+
+namespace {
+// Which kernel: the stream kernel while the tiles of the pair kernel would leave
+// most of the SMs without work or most rows of a tile empty.
+fp8_status_t run_gemm(const char* fn, const GemmProblem& p, cudaStream_t st) {
+    if (p.b_tiles && p.ends != nullptr) return run_gemm_pair(fn, p, st);  // ragged contraction
+    static const char* force = getenv("FP8_FORCE_GEMM");
+    if (force && p.k > 0 && atoi(force) > 0) return run_gemm_stream(fn, p, atoi(force), st);
+    if (force) return run_gemm_pair(fn, p, st);
+    const int64_t rows = p.groups > 1 ? (p.m + p.groups - 1) / p.groups : p.m;
+    if (p.k == 0 || rows > 128) return run_gemm_pair(fn, p, st);
+    return run_gemm_stream(fn, p, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128, st);
+}
+}  // namespace
 
 }  // namespace fp8q
 
@@ -134,7 +150,7 @@ extern "C" fp8_status_t fp8_gemm_block(const uint8_t* a, fp8_format_t fmt_a, con
                            b_layout == FP8_B_KN, b_block_rows == 1, out_dtype == FP8_DT_FP32, accumulate != 0};
     const fp8_status_t s = check(fn, p, b_layout, b_block_rows, out_dtype);
     if (s != FP8_OK || m == 0 || n == 0 || (k == 0 && p.accumulate)) return s;
-    return run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream));
+    return run_gemm(fn, p, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" fp8_status_t fp8_gemm_block_grouped(int groups, const int64_t* group_ends, const uint8_t* a,
@@ -149,7 +165,7 @@ extern "C" fp8_status_t fp8_gemm_block_grouped(int groups, const int64_t* group_
                            b_layout == FP8_B_KN, false, out_dtype == FP8_DT_FP32, false};
     s = check(fn, p, b_layout, kBlk, out_dtype);
     if (s != FP8_OK || rows == 0 || n == 0) return s;
-    return run_gemm_pair(fn, p, static_cast<cudaStream_t>(stream));
+    return run_gemm(fn, p, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" fp8_status_t fp8_gemm_block_grouped_wgrad(int groups, const int64_t* group_ends, const uint8_t* a,

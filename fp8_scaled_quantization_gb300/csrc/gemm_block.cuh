@@ -39,6 +39,7 @@ struct GemmProblem {
 struct Operand {
     const uint8_t* codes;
     int64_t inner, rows, groups;
+    int tile_rows;  // rows of one bulk copy
 };
 
 // Tensor maps of the operands of one product.  The bulk copies need 16-byte
@@ -49,6 +50,22 @@ fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, 
 
 // gemm_block_pair.cu: 256 x 256 outputs per CTA pair.
 fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st);
+
+// gemm_block_stream.cu: 128 columns of D per CTA and `tokens` (16, 32, 64 or 128)
+// rows at a time, k > 0; the contraction is not ragged.
+fp8_status_t run_gemm_stream(const char* fn, const GemmProblem& p, int tokens, cudaStream_t st);
+
+// The first `to` of four scales; one 16-byte load where they are aligned to it
+// (and the row holds all four).
+__device__ __forceinline__ float4 load_scales(const float* at, int to, bool wide) {
+    if (wide) return __ldg(reinterpret_cast<const float4*>(at));
+    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (to > 0) r.x = __ldg(at);
+    if (to > 1) r.y = __ldg(at + 1);
+    if (to > 2) r.z = __ldg(at + 2);
+    if (to > 3) r.w = __ldg(at + 3);
+    return r;
+}
 
 __host__ __device__ inline int64_t blocks_of(int64_t n) { return (n + kBlk - 1) / kBlk; }
 

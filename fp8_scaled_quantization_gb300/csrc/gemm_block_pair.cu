@@ -238,18 +238,6 @@ __device__ __forceinline__ void store_bulk(const GemmProblem& p, const CUtensorM
     }
 }
 
-// The first `to` of four scales; one 16-byte load where they are aligned to it
-// (and the row holds all four).
-__device__ __forceinline__ float4 load_scales(const float* at, int to, bool wide) {
-    if (wide) return __ldg(reinterpret_cast<const float4*>(at));
-    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (to > 0) r.x = __ldg(at);
-    if (to > 1) r.y = __ldg(at + 1);
-    if (to > 2) r.z = __ldg(at + 2);
-    if (to > 3) r.w = __ldg(at + 3);
-    return r;
-}
-
 // FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: both
 // operands in 1 x 128 tiles, contraction ragged.
 template <int FORM>
@@ -563,7 +551,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
 fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st) {
     const int64_t inner_b = p.b_kn ? p.n : p.k, rows_b = p.b_kn ? p.k : p.n;
     const bool bulk = aligned16(p.d) && p.n % (p.out_f32 ? 4 : 8) == 0 && !p.accumulate;
-    Operand oa = {p.a, p.k, p.m, 1}, ob = {p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups};
+    const Operand oa = {p.a, p.k, p.m, 1, 128}, ob = {p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups, 128};
     CUtensorMap a = {}, b = {}, d = {};
     fp8_status_t s = FP8_OK;
     if (p.k > 0) s = operand_maps(fn, oa, &a, ob, &b, st);

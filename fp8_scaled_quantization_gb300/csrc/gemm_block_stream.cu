@@ -1,0 +1,383 @@
+// gemm_block_stream.cu -- block-scaled FP8 products with few rows of A (tokens):
+// each CTA streams 128 rows of the weight past one tile of tokens.
+//
+// With few tokens the product is a read of the weight, so the roles of the
+// operands are exchanged: the weight's 128 rows (columns of D) fill the tensor
+// core's M = 128, the tokens its N = 16 .. 128, and a lane of the scaling warps
+// holds one column of D.  The contraction is split over the CTAs of a cluster
+// until there are enough of them to draw the memory's full rate; they add their
+// partial sums through distributed shared memory, in the order of their ranks,
+// so that results do not depend on timing and no workspace is needed.
+//
+// Roles per CTA of 256 threads: warps 0-3 scale, add, join and store; warp 4
+// fills the ring of operand tiles; warp 5 issues the products; warp 6 gathers
+// the scales.
+#include "fp8q_host.h"
+#include "fp8q_tcgen05.cuh"
+#include "gemm_block.cuh"
+
+namespace fp8q {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 128;        // rows of the weight per CTA
+constexpr int kScaleBlocks = 4;   // blocks of an item whose scales are gathered together
+constexpr int kScaleSlots = 3;
+constexpr int kMostSplit = 8;     // CTAs of a cluster
+
+// Per number of tokens: ring depth and CTAs per SM.  Small tiles run two CTAs
+// per SM with 90 KB of tiles in flight each; large ones need the memory alone.
+template <int TOKENS, bool TILES>
+struct Shape {
+    static constexpr int kStages = (TOKENS == 16 ? 5 : TOKENS == 32 ? 4 : TOKENS == 64 ? 6 : 4) - (TILES ? 1 : 0);
+    static constexpr int kCtas = TOKENS <= 32 ? 2 : 1;
+    static constexpr int kBufs = TOKENS <= 64 ? 4 : 2;        // TMEM buffers
+    static constexpr uint32_t kColumns = TOKENS * kBufs;      // a power of two, 64 .. 256
+    static constexpr uint32_t kStageBytes = kTileBytes + TOKENS * 128;
+};
+
+template <int TOKENS, bool TILES>
+struct Shared {
+    using S = Shape<TOKENS, TILES>;
+    alignas(16) float part[TOKENS][kRows];                           // this CTA's partial sums
+    alignas(16) float token[kScaleSlots][kScaleBlocks][TOKENS];      // per block: token scale (x block scale)
+    alignas(16) float weight[TILES ? kScaleSlots : 1][kScaleBlocks][TILES ? kRows : 1];  // 1 x 128 tiles: the weight rows' scales
+    uint64_t full[S::kStages], empty[S::kStages];
+    uint64_t tmem_full[4], tmem_empty[4];
+    uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
+    uint64_t part_full, part_empty;
+    uint32_t tmem;
+    GroupTable groups;
+};
+
+template <int TOKENS, bool TILES>
+constexpr size_t smem_bytes() {
+    using S = Shape<TOKENS, TILES>;
+    constexpr size_t bytes = 1024 + (size_t)S::kStages * S::kStageBytes + sizeof(Shared<TOKENS, TILES>);
+    static_assert(S::kCtas * (bytes + 1024) <= 228 * 1024, "shared memory of an SM");
+    return bytes;
+}
+
+// One item: a tile of tokens, 128 rows of the weight, this CTA's share of the blocks.
+struct Item {
+    int group;
+    int row0, row_end;  // tokens
+    int col0;           // rows of the weight
+    int blk0, blks;
+};
+
+template <int TOKENS>
+__device__ __forceinline__ Item locate(const GemmProblem& p, const GroupTable& g, int tiles_n, int t, int rank, int split) {
+    Item r;
+    const int e = find_group(&g, p.groups + 1, t);
+    const int local = t - g.tile[e], begin = e > 0 ? g.end[e - 1] : 0, end = g.end[e];
+    const int tiles_m = (end - begin + TOKENS - 1) / TOKENS;
+    // tiles of tokens first: neighbours read the same rows of the weight
+    r.group = e;
+    r.row0 = begin + local % tiles_m * TOKENS;
+    r.row_end = end;
+    r.col0 = local / tiles_m * kRows;
+    const int blks = e < p.groups ? (int)blocks_of(p.k) : 0;
+    r.blk0 = (int)((int64_t)blks * rank / split);
+    r.blks = (int)((int64_t)blks * (rank + 1) / split) - r.blk0;
+    return r;
+}
+
+// acc += s_j * P_j over all tokens: scales s at `token` (shared memory), times
+// the lane's own weight-row scale w2 with 1 x 128 tiles.
+template <int TOKENS, bool B_TILES>
+__device__ __forceinline__ void scale_add(uint64_t* acc, uint32_t from, const float* token, uint64_t w2) {
+    constexpr int kPiece = TOKENS < 32 ? 16 : 32;
+#pragma unroll
+    for (int c = 0; c < TOKENS / kPiece; ++c) {
+        uint32_t v[kPiece];
+        if constexpr (kPiece == 16) tmem_ld_32x16(from, v);
+        else tmem_ld_32x32(from + c * kPiece, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < kPiece / 2; ++j) {
+            const float2 s = *reinterpret_cast<const float2*>(token + c * kPiece + 2 * j);
+            uint64_t x = pack2(v[2 * j], v[2 * j + 1]), s2 = pack2(s.x, s.y);
+            if constexpr (B_TILES) s2 = mul2(s2, w2);
+            acc[c * kPiece / 2 + j] = fma2(x, s2, acc[c * kPiece / 2 + j]);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_out(const GemmProblem& p, int64_t at, float v) {
+    if (p.out_f32) {
+        float* d = static_cast<float*>(p.d) + at;
+        *d = p.accumulate ? __fadd_rn(*d, v) : v;
+    } else {
+        static_cast<uint16_t*>(p.d)[at] = (uint16_t)f32x2_to_bf16x2(v, 0.0f);
+    }
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: B [n,
+// k], 1 x 128 tiles.  The cluster's size is the number of shares.
+template <int FORM, int TOKENS>
+__global__ void __launch_bounds__(kThreads, Shape<TOKENS, FORM == 2>::kCtas)
+gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ CUtensorMap map_a,
+                   const __grid_constant__ CUtensorMap map_b, int split) {
+    constexpr bool B_KN = FORM == 1, B_TILES = FORM == 2;
+    using S = Shape<TOKENS, B_TILES>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* const tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    Shared<TOKENS, B_TILES>& sh = *reinterpret_cast<Shared<TOKENS, B_TILES>*>(tiles + S::kStages * S::kStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = split > 1 ? (int)cluster_rank() : 0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < S::kBufs; ++i) {
+            mbar_init(&sh.tmem_full[i], 1);
+            mbar_init(&sh.tmem_empty[i], 4);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(&sh.sc_full[i], 1);
+            mbar_init(&sh.sc_empty[i], 4);
+        }
+        mbar_init(&sh.part_full, 4 * split);   // four warps of each CTA
+        mbar_init(&sh.part_empty, 4 * split);
+        mbar_init_fence();
+    }
+    if (warp == 5) tmem_alloc<1>(&sh.tmem, S::kColumns);
+    pdl_begin();
+    const int tiles_n = (int)((p.n + kRows - 1) / kRows);
+    const int total = build_groups(&sh.groups, p.ends, p.groups, p.m, TOKENS, 0, tiles_n);
+    tmem_fence_before();
+    if (split > 1) cluster_sync();  // (build_groups has synchronised the CTA)
+    else __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int first = blockIdx.x / split, step = gridDim.x / split;
+    Waiter w;
+
+    if (warp < 4) {
+        const int row = warp * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        uint32_t it = 0, group = 0, items = 0;
+        for (int t = first; t < total; t += step, ++items) {
+            const Item item = locate<TOKENS>(p, sh.groups, tiles_n, t, rank, split);
+            uint64_t acc[TOKENS / 2];
+#pragma unroll
+            for (int i = 0; i < TOKENS / 2; ++i) acc[i] = 0;
+            for (int b = 0; b < item.blks; ++b, ++it) {
+                const uint32_t buf = it % S::kBufs, slot = group % kScaleSlots;
+                const int sub = b % kScaleBlocks;
+                if (sub == 0) w.wait(smem_addr(&sh.sc_full[slot]), (group / kScaleSlots) & 1);
+                w.wait(smem_addr(&sh.tmem_full[buf]), (it / S::kBufs) & 1);
+                __syncwarp();  // lanes may have left the wait apart
+                tmem_fence_after();
+                uint64_t w2 = 0;
+                if constexpr (B_TILES) {
+                    const float f = sh.weight[slot][sub][row];
+                    w2 = pack2(f, f);
+                }
+                scale_add<TOKENS, B_TILES>(acc, lanes + buf * TOKENS, sh.token[slot][sub], w2);
+                tmem_fence_before();
+                __syncwarp();
+                const bool last = sub == kScaleBlocks - 1 || b == item.blks - 1;
+                if (lane == 0) {
+                    mbar_arrive(&sh.tmem_empty[buf]);
+                    if (last) mbar_arrive(&sh.sc_empty[slot]);
+                }
+                if (last) ++group;
+            }
+            const int64_t col = item.col0 + row;
+            const int tokens = min(TOKENS, item.row_end - item.row0);
+            if (split == 1) {
+                if (col < p.n) {
+#pragma unroll
+                    for (int j = 0; j < TOKENS; ++j) {
+                        const float2 v = unpack2(acc[j >> 1]);
+                        if (j < tokens) store_out(p, (int64_t)(item.row0 + j) * p.n + col, j & 1 ? v.y : v.x);
+                    }
+                }
+                continue;
+            }
+            // join: every CTA offers its partial sums and adds its share of the tokens over all of them
+            if (items > 0) w.template wait<true>(smem_addr(&sh.part_empty), (items - 1) & 1);
+#pragma unroll
+            for (int j = 0; j < TOKENS; ++j) {
+                const float2 v = unpack2(acc[j >> 1]);
+                if (j < tokens) sh.part[j][row] = j & 1 ? v.y : v.x;
+            }
+            __syncwarp();
+            if (lane < split) cluster_arrive<true>(cluster_addr(smem_addr(&sh.part_full), lane));
+            w.template wait<true>(smem_addr(&sh.part_full), items & 1);
+            __syncwarp();
+            const int j0 = tokens * rank / split, j1 = tokens * (rank + 1) / split;
+            for (int j = j0; j < j1; ++j) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int r = 0; r < kMostSplit; ++r) {
+                    if (r < split) {
+                        const float v = ld_cluster(cluster_addr(smem_addr(&sh.part[j][row]), r));
+                        sum = r == 0 ? v : __fadd_rn(sum, v);
+                    }
+                }
+                if (col < p.n) store_out(p, (int64_t)(item.row0 + j) * p.n + col, sum);
+            }
+            __syncwarp();
+            if (lane < split) cluster_arrive<true>(cluster_addr(smem_addr(&sh.part_empty), lane));
+        }
+    } else if (warp == 4) {
+        // ---- operand tiles
+        const uint32_t base = smem_addr(tiles);
+        uint32_t it = 0, stage = 0, phase = 0;
+        for (int t = first; t < total; t += step) {
+            const Item item = locate<TOKENS>(p, sh.groups, tiles_n, t, rank, split);
+            for (int b = 0; b < item.blks; ++b, ++it) {
+                const uint32_t wt = base + stage * S::kStageBytes, xt = wt + kTileBytes, bar = smem_addr(&sh.full[stage]);
+                const int x = (item.blk0 + b) * kBlk;
+                if (it >= S::kStages) w.wait(smem_addr(&sh.empty[stage]), phase ^ 1);
+                __syncwarp();
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sh.full[stage], S::kStageBytes);
+                    const int matrix = B_TILES ? 0 : item.group;
+                    if constexpr (B_KN) tma_tile<false>(wt, &map_b, item.col0, x, matrix, bar);
+                    else tma_tile<false>(wt, &map_b, x, item.col0, matrix, bar);
+                    tma_tile<false>(xt, &map_a, x, item.row0, 0, bar);
+                }
+                __syncwarp();
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // the last fills have been read before the CTA ends
+        for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
+            w.wait(smem_addr(&sh.empty[i % S::kStages]), (i / S::kStages) & 1);
+    } else if (warp == 5) {
+        // ---- products: weight rows are M, tokens N
+        const uint32_t desc = mma_desc(p.fmt_b, p.fmt_a, B_KN, false, kRows, TOKENS);
+        const uint64_t w0 = tile_desc(smem_addr(tiles)), x0 = tile_desc(smem_addr(tiles) + kTileBytes);
+        uint32_t it = 0, stage = 0, phase = 0;
+        for (int t = first; t < total; t += step) {
+            const int blks = locate<TOKENS>(p, sh.groups, tiles_n, t, rank, split).blks;
+            for (int b = 0; b < blks; ++b, ++it) {
+                const uint32_t buf = it % S::kBufs;
+                const uint64_t wt = w0 + stage * (S::kStageBytes >> 4), xt = x0 + stage * (S::kStageBytes >> 4);
+                if (it >= S::kBufs) w.wait(smem_addr(&sh.tmem_empty[buf]), (it / S::kBufs - 1) & 1);
+                w.wait(smem_addr(&sh.full[stage]), phase);
+                __syncwarp();
+                tmem_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f8<1>(tmem + buf * TOKENS, wt + k * (B_KN ? kStepMnMajor : kStepKMajor), xt + k * kStepKMajor, desc,
+                                  k > 0);
+                    mma_commit<1>(smem_addr(&sh.tmem_full[buf]));
+                    mma_commit<1>(smem_addr(&sh.empty[stage]));
+                }
+                __syncwarp();
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+    } else if (warp == 6) {
+        // ---- scales
+        const int64_t kb = blocks_of(p.k), nb = blocks_of(p.n);
+        const bool wide_a = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sa) & 15u) == 0;
+        const bool wide_b = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sb) & 15u) == 0;
+        uint32_t group = 0;
+        for (int t = first; t < total; t += step) {
+            const Item item = locate<TOKENS>(p, sh.groups, tiles_n, t, rank, split);
+            for (int done = 0; done < item.blks; done += kScaleBlocks, ++group) {
+                const int g0 = item.blk0 + done, to = min(item.blks - done, kScaleBlocks);
+                const bool whole = g0 % kScaleBlocks == 0;  // an aligned piece of a row of scales
+                const uint32_t slot = group % kScaleSlots;
+                float c[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+                if constexpr (!B_TILES) {
+                    const int64_t cb = item.col0 / kBlk;
+                    const float* sb = p.sb + (int64_t)item.group * kb * nb;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < to) c[i] = __ldg(sb + (B_KN ? (int64_t)(g0 + i) * nb + cb : cb * kb + g0 + i));
+                }
+                if (group >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (group / kScaleSlots - 1) & 1);
+                __syncwarp();
+#pragma unroll
+                for (int j = lane; j < TOKENS; j += 32) {  // a token or row that is not there: any scale
+                    const int64_t r = item.row0 + j;
+                    const float4 a = load_scales(p.sa + (r < p.m ? r : p.m - 1) * kb + g0, to, wide_a && whole);
+                    sh.token[slot][0][j] = __fmul_rn(a.x, c[0]);
+                    sh.token[slot][1][j] = __fmul_rn(a.y, c[1]);
+                    sh.token[slot][2][j] = __fmul_rn(a.z, c[2]);
+                    sh.token[slot][3][j] = __fmul_rn(a.w, c[3]);
+                }
+                if constexpr (B_TILES) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t n = item.col0 + i * 32 + lane;
+                        const float4 b = load_scales(p.sb + (n < p.n ? n : p.n - 1) * kb + g0, to, wide_b && whole);
+                        sh.weight[slot][0][i * 32 + lane] = b.x;
+                        sh.weight[slot][1][i * 32 + lane] = b.y;
+                        sh.weight[slot][2][i * 32 + lane] = b.z;
+                        sh.weight[slot][3][i * 32 + lane] = b.w;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.sc_full[slot]);
+            }
+        }
+    }
+    __syncwarp();
+    tmem_fence_before();
+    if (split > 1) cluster_sync();  // no CTA leaves while another reads its partial sums
+    else __syncthreads();
+    tmem_fence_after();
+    if (warp == 5) tmem_free<1>(tmem, S::kColumns);
+}
+
+template <int TOKENS>
+fp8_status_t run(const char* fn, const GemmProblem& p, const CUtensorMap& a, const CUtensorMap& b, cudaStream_t st) {
+    const int64_t tiles_n = (p.n + kRows - 1) / kRows, tiles_m = (p.m + TOKENS - 1) / TOKENS;
+    const int64_t busy = p.groups < p.m ? p.groups : p.m;  // groups with rows, at most
+    const int64_t items = (tiles_m + busy - 1) * tiles_n, slots = (int64_t)sm_count() * Shape<TOKENS, false>::kCtas;
+    // shares of the contraction: as many as fill the SMs, each at least two blocks long
+    const int64_t kb = blocks_of(p.k);
+    int split = 1;
+    while (split < kMostSplit && items * (split + 1) <= slots && kb >= 2 * (split + 1)) ++split;
+    const int64_t most = slots / split, clusters = items + 1 < most ? items + 1 : most;
+    const auto go = [&](auto kernel, size_t smem) {
+        return launch_cluster(fn, kernel, dim3((unsigned)(clusters * split)), dim3(kThreads), smem, split, st, p, a, b, split);
+    };
+    return p.b_tiles ? go(gemm_stream_kernel<2, TOKENS>, smem_bytes<TOKENS, true>())
+           : p.b_kn  ? go(gemm_stream_kernel<1, TOKENS>, smem_bytes<TOKENS, false>())
+                     : go(gemm_stream_kernel<0, TOKENS>, smem_bytes<TOKENS, false>());
+}
+
+}  // namespace
+
+fp8_status_t run_gemm_stream(const char* fn, const GemmProblem& p, int tokens, cudaStream_t st) {
+    const Operand oa = {p.a, p.k, p.m, 1, tokens}, ob = {p.b, p.b_kn ? p.n : p.k, p.b_kn ? p.k : p.n, p.groups, 128};
+    CUtensorMap a = {}, b = {};
+    const fp8_status_t s = operand_maps(fn, oa, &a, ob, &b, st);
+    if (s != FP8_OK) return s;
+    switch (tokens) {
+        case 16: return run<16>(fn, p, a, b, st);
+        case 32: return run<32>(fn, p, a, b, st);
+        case 64: return run<64>(fn, p, a, b, st);
+        default: return run<128>(fn, p, a, b, st);
+    }
+}
+
+fp8_status_t gemm_stream_wait_timeouts(unsigned long long* count) {
+    return cuda_status(cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof *count), "fp8_wait_timeouts");
+}
+
+}  // namespace fp8q

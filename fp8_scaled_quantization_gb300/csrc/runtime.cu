@@ -96,13 +96,13 @@ fp8_status_t encode_tile_map_u16(CUtensorMap* map, const void* base, int64_t row
 }
 
 fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inner, int64_t stride, int64_t rows,
-                                int64_t groups) {
+                                int64_t groups, int tile_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     const fp8_status_t s = tile_map_encoder(&encode);
     if (s != FP8_OK) return s;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)groups};
     const cuuint64_t strides[2] = {(cuuint64_t)stride, (cuuint64_t)stride * (cuuint64_t)rows};
-    const cuuint32_t box[3] = {128, 128, 1};
+    const cuuint32_t box[3] = {128, (cuuint32_t)tile_rows, 1};
     const cuuint32_t elem_strides[3] = {1, 1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
                               elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -208,10 +208,11 @@ fp8_status_t fp8_wait_timeouts(unsigned long long* count) {
     using namespace fp8q;
     if (count == nullptr) return fail(FP8_ERR_INVALID_ARG, "fp8_wait_timeouts: count is NULL");
     fp8_status_t st = cuda_status(cudaDeviceSynchronize(), "fp8_wait_timeouts");
-    unsigned long long pair = 0;
+    unsigned long long pair = 0, stream = 0;
     if (st == FP8_OK) st = block_ct_wait_timeouts(count);
     if (st == FP8_OK) st = gemm_pair_wait_timeouts(&pair);
-    if (st == FP8_OK) *count += pair;
+    if (st == FP8_OK) st = gemm_stream_wait_timeouts(&stream);
+    if (st == FP8_OK) *count += pair + stream;
     return st;
 }
 
