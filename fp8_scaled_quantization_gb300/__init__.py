@@ -125,8 +125,14 @@ def _u64(t, name: str) -> int | None:
     return _p(t)
 
 
+# The current stream's handle without building a Stream object (3 us per call), where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device()) or None
         return torch.cuda.current_stream().cuda_stream or None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream or None
@@ -345,17 +351,25 @@ def fp8_quantize_current(x, fmt, q_out, margin=0, amax_out=None, scale_out=None,
 
 def _operand(q, scale_inv, shape, scale_shape, name):
     """Shape and type checks of one operand of a product."""
-    if not isinstance(q, torch.Tensor) or q.dtype != torch.uint8 or tuple(q.shape) != shape:
+    if q.dtype != torch.uint8 or q.shape != shape:
         raise ValueError(f"{name} must be uint8 {shape}")
-    if not isinstance(scale_inv, torch.Tensor) or scale_inv.dtype != torch.float32 \
-            or tuple(scale_inv.shape) != scale_shape:
+    if scale_inv.dtype != torch.float32 or scale_inv.shape != scale_shape:
         raise ValueError(f"scale_inv_{name} must be float32 {scale_shape}")
 
 
+def _ptrs(*tensors):
+    """Data pointers of contiguous tensors on the current CUDA device (one look at the device for all)."""
+    here = torch.cuda.current_device() if tensors[0].is_cuda else None
+    for t in tensors:
+        if t.get_device() != here or not t.is_contiguous():
+            _p(t)  # says what is wrong with it
+    return [t.data_ptr() or None for t in tensors]
+
+
 def _ends(group_ends):
-    if not isinstance(group_ends, torch.Tensor) or group_ends.dtype != torch.int64 or group_ends.dim() != 1:
+    if group_ends.dtype != torch.int64 or group_ends.dim() != 1:
         raise ValueError("group_ends must be a 1-D int64 tensor")
-    return int(group_ends.shape[0])
+    return group_ends.shape[0]
 
 
 def fp8_gemm_block(a, scale_inv_a, b, scale_inv_b, d, fmt_a=E4M3, fmt_b=E4M3, b_layout=B_NK, b_block_rows=128,
@@ -364,16 +378,17 @@ def fp8_gemm_block(a, scale_inv_a, b, scale_inv_b, d, fmt_a=E4M3, fmt_b=E4M3, b_
     b [n, k] (B_NK) or [k, n] (B_KN) codes with 128 x 128 factors (or, with b_block_rows=1
     and B_NK, 1 x 128 factors).  d is bfloat16 or float32; accumulate adds to a float32 d."""
     m, k = _rows_cols(a)
-    n = int(d.shape[1]) if d.dim() == 2 else -1
-    if tuple(d.shape) != (m, n):
+    if d.dim() != 2 or d.shape[0] != m:
         raise ValueError(f"d must be [{m}, n]")
+    n = d.shape[1]
     kb = -(-k // 128)
     rows_b = n if b_block_rows == 1 else -(-n // 128)
     shape, scales = ((k, n), (kb, rows_b)) if b_layout == B_KN else ((n, k), (rows_b, kb))
     _operand(a, scale_inv_a, (m, k), (m, kb), "a")
     _operand(b, scale_inv_b, shape, scales, "b")
-    _check(library().fp8_gemm_block(_p(a), fmt_a, _p(scale_inv_a), _p(b), fmt_b, _p(scale_inv_b), b_layout, b_block_rows,
-                                    m, n, k, _p(d), _dt(d), int(accumulate), _stream(stream)))
+    pa, psa, pb, psb, pd = _ptrs(a, scale_inv_a, b, scale_inv_b, d)
+    _check(library().fp8_gemm_block(pa, fmt_a, psa, pb, fmt_b, psb, b_layout, b_block_rows, m, n, k, pd, _dt(d),
+                                    int(accumulate), _stream(stream)))
 
 
 def fp8_gemm_block_grouped(a, scale_inv_a, b, scale_inv_b, group_ends, d, fmt_a=E4M3, fmt_b=E4M3, b_layout=B_NK,
@@ -383,15 +398,16 @@ def fp8_gemm_block_grouped(a, scale_inv_a, b, scale_inv_b, group_ends, d, fmt_a=
     rows after the last end become zeros.  group_ends: int64 on the device."""
     rows, k = _rows_cols(a)
     groups = _ends(group_ends)
-    n = int(d.shape[1]) if d.dim() == 2 else -1
-    if tuple(d.shape) != (rows, n):
+    if d.dim() != 2 or d.shape[0] != rows:
         raise ValueError(f"d must be [{rows}, n]")
+    n = d.shape[1]
     kb, nb = -(-k // 128), -(-n // 128)
     shape, scales = ((groups, k, n), (groups, kb, nb)) if b_layout == B_KN else ((groups, n, k), (groups, nb, kb))
     _operand(a, scale_inv_a, (rows, k), (rows, kb), "a")
     _operand(b, scale_inv_b, shape, scales, "b")
-    _check(library().fp8_gemm_block_grouped(groups, _p(group_ends), _p(a), fmt_a, _p(scale_inv_a), _p(b), fmt_b,
-                                            _p(scale_inv_b), b_layout, rows, n, k, _p(d), _dt(d), _stream(stream)))
+    ends, pa, psa, pb, psb, pd = _ptrs(group_ends, a, scale_inv_a, b, scale_inv_b, d)
+    _check(library().fp8_gemm_block_grouped(groups, ends, pa, fmt_a, psa, pb, fmt_b, psb, b_layout, rows, n, k, pd,
+                                            _dt(d), _stream(stream)))
 
 
 def fp8_gemm_block_grouped_wgrad(a, scale_inv_a, b, scale_inv_b, group_ends, d, fmt_a=E4M3, fmt_b=E4M3,
@@ -401,14 +417,14 @@ def fp8_gemm_block_grouped_wgrad(a, scale_inv_a, b, scale_inv_b, group_ends, d, 
     m, rows = _rows_cols(a)
     n, _ = _rows_cols(b)
     groups = _ends(group_ends)
-    if tuple(d.shape) != (groups, m, n):
+    if d.shape != (groups, m, n):
         raise ValueError(f"d must be [{groups}, {m}, {n}]")
     rb = -(-rows // 128)
     _operand(a, scale_inv_a, (m, rows), (m, rb), "a")
     _operand(b, scale_inv_b, (n, rows), (n, rb), "b")
-    _check(library().fp8_gemm_block_grouped_wgrad(groups, _p(group_ends), _p(a), fmt_a, _p(scale_inv_a), _p(b), fmt_b,
-                                                  _p(scale_inv_b), m, n, rows, _p(d), _dt(d), int(accumulate),
-                                                  _stream(stream)))
+    ends, pa, psa, pb, psb, pd = _ptrs(group_ends, a, scale_inv_a, b, scale_inv_b, d)
+    _check(library().fp8_gemm_block_grouped_wgrad(groups, ends, pa, fmt_a, psa, pb, fmt_b, psb, m, n, rows, pd, _dt(d),
+                                                  int(accumulate), _stream(stream)))
 
 
 _GRAD_DTYPES = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}
@@ -416,19 +432,15 @@ _GRAD_DTYPES = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}
 
 def _grad_table(tensors, name):
     """Host arrays (pointers, dtypes) of a list of contiguous BF16 / fp32 tensors on the current device."""
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("tensors passed to the FP8 library must live on a CUDA device")
-        if not t.is_contiguous():
-            raise ValueError("tensors passed to the FP8 library must be contiguous")
-    here = torch.cuda.current_device()
-    if any(t.get_device() != here for t in tensors):
-        raise ValueError(f"every tensor must be on the current CUDA device cuda:{here}")
+    here = torch.cuda.current_device() if tensors[0].is_cuda else None
+    if set(map(torch.Tensor.get_device, tensors)) != {here} or not all(map(torch.Tensor.is_contiguous, tensors)):
+        for t in tensors:
+            _p(t)  # says what is wrong with the first one
     try:
         dtypes = array("i", [_GRAD_DTYPES[t.dtype] for t in tensors])
     except KeyError as e:
         raise TypeError(f"{name} must be bfloat16 or float32 tensors, got {e.args[0]}") from None
-    return array("Q", [t.data_ptr() for t in tensors]), dtypes
+    return array("Q", map(torch.Tensor.data_ptr, tensors)), dtypes
 
 
 def _at(a):
@@ -440,7 +452,7 @@ def fp8_grad_norm_grouped(xs, norm_out, stream=None):
     if not xs:
         raise ValueError("xs must be a non-empty list of tensors")
     ptrs, dtypes = _grad_table(xs, "xs")
-    ns = array("q", [t.numel() for t in xs])
+    ns = array("q", map(torch.Tensor.numel, xs))
     _check(library().fp8_grad_norm_grouped(len(xs), _at(ptrs), _at(ns), _at(dtypes), _f32(norm_out, "norm_out"),
                                            _stream(stream)))
 
@@ -450,8 +462,8 @@ def fp8_grad_clip_grouped(xs, max_norm, norm_out=None, ys=None, coef_out=None, e
     without ys.  A norm that is NaN or Inf leaves the values as they are."""
     if not xs or (ys is not None and len(ys) != len(xs)):
         raise ValueError("xs must be a non-empty list of tensors, and ys as long as xs")
-    ns = array("q", [t.numel() for t in xs])
-    if ys is not None and any(y.numel() != n for y, n in zip(ys, ns)):
+    ns = array("q", map(torch.Tensor.numel, xs))
+    if ys is not None and array("q", map(torch.Tensor.numel, ys)) != ns:
         raise ValueError("each y must have as many elements as its x")
     ptrs, dtypes = _grad_table(xs, "xs")
     outs, out_dtypes = _grad_table(ys, "ys") if ys is not None else (None, None)

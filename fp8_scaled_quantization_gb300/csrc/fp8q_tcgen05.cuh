@@ -50,6 +50,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// The same where only the meeting counts: the last one before the CTAs end.
+// (A release would wait for the outputs' stores, about a microsecond.)
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
 // Address in the cluster's shared window of the same variable in CTA `rank`.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -234,6 +239,11 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t addr, uint32_t (&r)[32]) 
 }
 
 // ---------------------------------------------------------------- tile loads
+
+// Fetches a tensor map ahead of its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 
 // One 128 x 128-byte tile at byte x, row y of matrix z by the bulk-copy engine;
 // x a multiple of 16; what lies outside reads as zero.  PAIR: `bar` may be the

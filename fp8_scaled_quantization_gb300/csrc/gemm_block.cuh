@@ -74,9 +74,12 @@ __host__ __device__ inline int64_t blocks_of(int64_t n) { return (n + kBlk - 1) 
 // ragged, a last group (index `groups`, without a contraction) holds the rows
 // after the last end, whose outputs are zeros.
 struct GroupTable {
-    int end[kMaxGroups + 1];
-    int tile[kMaxGroups + 2];
+    int* end;   // groups + 1 entries
+    int* tile;  // groups + 2 entries
+
+    __device__ __forceinline__ GroupTable(int* words, int groups) : end(words), tile(words + groups + 1) {}
 };
+__host__ __device__ constexpr size_t group_table_bytes(int groups) { return (size_t)(2 * groups + 3) * sizeof(int); }
 
 // Every thread of the CTA calls this (it synchronises the CTA).  Group ends
 // come from device memory and are never trusted: each is clamped to [0, limit]
@@ -86,13 +89,23 @@ struct GroupTable {
 //               output rows instead (RAGGED_K)
 //   tiles_n     tiles along n
 // Returns the number of tiles in all.
-__device__ __forceinline__ int build_groups(GroupTable* t, const int64_t* ends, int groups, int64_t limit,
+__device__ __forceinline__ int build_groups(const GroupTable& t, const int64_t* ends, int groups, int64_t limit,
                                             int tile_rows, int64_t fixed_rows, int tiles_n) {
     const int total = fixed_rows > 0 ? groups : groups + 1;
+    if (ends == nullptr) {  // one group, known on the host
+        if (threadIdx.x == 0) {
+            const int64_t rows = fixed_rows > 0 ? fixed_rows : limit;
+            t.end[0] = t.end[1] = (int)limit;
+            t.tile[0] = 0;
+            t.tile[1] = t.tile[2] = (int)((rows + tile_rows - 1) / tile_rows) * tiles_n;
+        }
+        __syncthreads();
+        return t.tile[1];
+    }
     for (int e = threadIdx.x; e < total; e += blockDim.x) {
-        int64_t v = e < groups && ends != nullptr ? ends[e] : limit;
+        int64_t v = e < groups ? ends[e] : limit;
         v = v < 0 ? 0 : (v > limit ? limit : v);
-        t->end[e] = (int)v;
+        t.end[e] = (int)v;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -100,7 +113,7 @@ __device__ __forceinline__ int build_groups(GroupTable* t, const int64_t* ends, 
         const int lane = threadIdx.x, per = (total + 31) / 32;
         const int lo = min(lane * per, total), hi = min(lo + per, total);
         int mx = 0;
-        for (int e = lo; e < hi; ++e) mx = max(mx, t->end[e]);
+        for (int e = lo; e < hi; ++e) mx = max(mx, t.end[e]);
         int before = mx;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -111,9 +124,9 @@ __device__ __forceinline__ int build_groups(GroupTable* t, const int64_t* ends, 
         if (lane == 0) before = 0;
         int run = before, sum = 0;
         for (int e = lo; e < hi; ++e) {
-            const int end = max(run, t->end[e]);
+            const int end = max(run, t.end[e]);
             const int64_t rows = fixed_rows > 0 ? fixed_rows : end - run;
-            t->end[e] = end;
+            t.end[e] = end;
             run = end;
             sum += (int)((rows + tile_rows - 1) / tile_rows) * tiles_n;
         }
@@ -126,25 +139,25 @@ __device__ __forceinline__ int build_groups(GroupTable* t, const int64_t* ends, 
         pre -= sum;
         run = before;
         for (int e = lo; e < hi; ++e) {
-            const int end = t->end[e];
+            const int end = t.end[e];
             const int64_t rows = fixed_rows > 0 ? fixed_rows : end - run;
             run = end;
-            t->tile[e] = pre;
+            t.tile[e] = pre;
             pre += (int)((rows + tile_rows - 1) / tile_rows) * tiles_n;
         }
-        if (lane == 31) t->tile[total] = pre;
+        if (lane == 31) t.tile[total] = pre;
     }
     __syncthreads();
-    return t->tile[total];
+    return t.tile[total];
 }
 
 // Group of tile `i`: the last one that begins at or before it (groups without
 // tiles share their begin with the next one).
-__device__ __forceinline__ int find_group(const GroupTable* t, int total, int i) {
+__device__ __forceinline__ int find_group(const GroupTable& t, int total, int i) {
     int lo = 0, hi = total - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (t->tile[mid] <= i) lo = mid;
+        if (t.tile[mid] <= i) lo = mid;
         else hi = mid - 1;
     }
     return lo;

@@ -47,7 +47,7 @@ struct Shared {
     uint64_t tmem_full[2], tmem_empty[2];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint32_t tmem;
-    GroupTable groups;
+    int groups[2 * kMaxGroups + 3];
 };
 constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 8 * kOutBytes + sizeof(Shared);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
@@ -64,7 +64,7 @@ struct Tile {
 template <bool RAGGED_K>
 __device__ __forceinline__ Tile locate(const GemmProblem& p, const GroupTable& g, int count, int tiles_n, int t) {
     Tile r;
-    const int e = find_group(&g, count, t);
+    const int e = find_group(g, count, t);
     const int local = t - g.tile[e], begin = e > 0 ? g.end[e - 1] : 0, end = g.end[e];
     const int m = (int)p.m, k = (int)p.k, rows = RAGGED_K ? m : end - begin;
     const int tiles_m = (rows + kPairM - 1) / kPairM;
@@ -269,10 +269,15 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
         mbar_init_fence();
     }
     if (warp == 8) tmem_alloc<2>(&sh.tmem, 512);
+    if (threadIdx.x == 320) {
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
+    }
     pdl_begin();
     const int tiles_n = (int)((p.n + kPairN - 1) / kPairN);
     const int count = RAGGED_K ? p.groups : p.groups + 1;
-    const int total = build_groups(&sh.groups, p.ends, p.groups, RAGGED_K ? p.k : p.m, kPairM, RAGGED_K ? p.m : 0, tiles_n);
+    const GroupTable groups(sh.groups, p.groups);
+    const int total = build_groups(groups, p.ends, p.groups, RAGGED_K ? p.k : p.m, kPairM, RAGGED_K ? p.m : 0, tiles_n);
     tmem_fence_before();
     cluster_sync();
     tmem_fence_after();
@@ -287,7 +292,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
         const uint32_t full0 = smem_addr(&sh.tmem_full[0]), empty0 = cluster_addr(smem_addr(&sh.tmem_empty[0]), 0);
         uint32_t it = 0, group = 0;  // blocks and scale groups so far
         for (int t = first; t < total; t += step) {
-            const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
+            const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
             uint64_t acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0;
@@ -391,16 +396,26 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                 const uint32_t desc = mma_desc(p.fmt_a, p.fmt_b, false, B_KN, kPairM, kPairN);
                 const uint64_t a0 = tile_desc(smem_addr(tiles)), b0 = tile_desc(smem_addr(tiles) + kTileBytes);
                 uint32_t it = 0, stage = 0, phase = 0;
+                bool ready = false;  // the next block's tiles and buffer, asked for while this block's products are issued
                 for (int t = first; t < total; t += step) {
-                    const int blks = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t).blks;
+                    const int blks = locate<RAGGED_K>(p, groups, count, tiles_n, t).blks;
                     for (int b = 0; b < blks; ++b, ++it) {
-                        const uint32_t buf = it & 1, free_bar = smem_addr(&sh.tmem_empty[buf]), free_phase = ((it >> 1) & 1) ^ 1;
-                        const uint64_t at = a0 + stage * (kStageBytes >> 4), bt = b0 + stage * (kStageBytes >> 4);
-                        const bool is_free = it < 2 || Waiter::test(free_bar, free_phase);
-                        // (tiles that were masked with plain stores are released to the cluster)
-                        w.template wait<RAGGED_K>(smem_addr(&sh.full[stage]), phase);
-                        if (!is_free) w.wait(free_bar, free_phase);
+                        const uint32_t buf = it & 1;
+                        if (!ready) {
+                            // (tiles that were masked with plain stores are released to the cluster)
+                            w.template wait<RAGGED_K>(smem_addr(&sh.full[stage]), phase);
+                            if (it >= 2) w.wait(smem_addr(&sh.tmem_empty[buf]), ((it >> 1) - 1) & 1);
+                        }
                         __syncwarp();
+                        const uint64_t at = a0 + stage * (kStageBytes >> 4), bt = b0 + stage * (kStageBytes >> 4);
+                        const uint32_t now = stage;
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                        const uint32_t next = it + 1;
+                        const bool free = next < 2 || Waiter::test(smem_addr(&sh.tmem_empty[next & 1]), ((next >> 1) - 1) & 1);
+                        const bool filled = !RAGGED_K && Waiter::test(smem_addr(&sh.full[stage]), phase);
                         tmem_fence_after();
                         if (elect_one()) {
 #pragma unroll
@@ -408,13 +423,9 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                                 mma_f8<2>(tmem + buf * kPairN, at + k * kStepKMajor,
                                           bt + k * (B_KN ? kStepMnMajor : kStepKMajor), desc, k > 0);
                             mma_commit<2>(smem_addr(&sh.tmem_full[buf]));
-                            mma_commit<2>(smem_addr(&sh.empty[stage]));
+                            mma_commit<2>(smem_addr(&sh.empty[now]));
                         }
-                        __syncwarp();
-                        if (++stage == kStages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+                        ready = __all_sync(0xFFFFFFFFu, free && filled);
                     }
                 }
             }
@@ -425,7 +436,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             const bool wide_b = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sb) & 15u) == 0;
             uint32_t group = 0;
             for (int t = first; t < total; t += step) {
-                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
+                const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
                 for (int done = 0; done < tile.blks; done += kScaleBlocks, ++group) {
                     const int g0 = tile.blk0 + done, to = min(tile.blks - done, kScaleBlocks);
                     const bool whole = g0 % kScaleBlocks == 0;  // an aligned piece of a row of scales
@@ -490,7 +501,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             const uint32_t base = smem_addr(tiles), full0 = cluster_addr(smem_addr(&sh.full[0]), 0);
             uint32_t it = 0, stage = 0, phase = 0;
             for (int t = first; t < total; t += step) {
-                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
+                const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
                 const int row = tile.row0 + (int)rank * 128, col = tile.col0 + (int)rank * 128;
                 for (int b = 0; b < tile.blks; ++b, ++it) {
                     const uint32_t a = base + stage * kStageBytes, bt = a + kTileBytes;
@@ -521,7 +532,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             const uint32_t base = smem_addr(tiles), full0 = cluster_addr(smem_addr(&sh.full[0]), 0);
             uint32_t stage = 0, phases = 0;  // bit s: the phase of landed[s]
             for (int t = first; t < total; t += step) {
-                const Tile tile = locate<RAGGED_K>(p, sh.groups, count, tiles_n, t);
+                const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
                 for (int b = 0; b < tile.blks; ++b) {
                     const int x = (tile.blk0 + b) * kBlk;
                     if (is_cut(tile, x, (int)p.k)) {
@@ -541,7 +552,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
         __syncwarp();
     }
     tmem_fence_before();
-    cluster_sync();
+    cluster_meet();
     tmem_fence_after();
     if (warp == 8) tmem_free<2>(tmem, 512);
 }

@@ -9,9 +9,9 @@
 // partial sums through distributed shared memory, in the order of their ranks,
 // so that results do not depend on timing and no workspace is needed.
 //
-// Roles per CTA of 256 threads: warps 0-3 scale, add, join and store; warp 4
-// fills the ring of operand tiles; warp 5 issues the products; warp 6 gathers
-// the scales.
+// Roles per CTA: four warps (eight from 32 tokens on, each pair of them sharing
+// the tokens of 32 columns) scale, add, join and store; then one warp fills the
+// ring of operand tiles and gathers the scales, and one issues the products.
 #include "fp8q_host.h"
 #include "fp8q_tcgen05.cuh"
 #include "gemm_block.cuh"
@@ -19,21 +19,23 @@
 namespace fp8q {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kRows = 128;        // rows of the weight per CTA
 constexpr int kScaleBlocks = 4;   // blocks of an item whose scales are gathered together
 constexpr int kScaleSlots = 3;
 constexpr int kMostSplit = 8;     // CTAs of a cluster
 
-// Per number of tokens: ring depth and CTAs per SM.  Small tiles run two CTAs
-// per SM with 90 KB of tiles in flight each; large ones need the memory alone.
+// Per number of tokens: ring depth and CTAs per SM.  Two CTAs per SM where their
+// tiles fit, so that one's start and end overlap the other's stream.
 template <int TOKENS, bool TILES>
 struct Shape {
-    static constexpr int kStages = (TOKENS == 16 ? 5 : TOKENS == 32 ? 4 : TOKENS == 64 ? 6 : 4) - (TILES ? 1 : 0);
-    static constexpr int kCtas = TOKENS <= 32 ? 2 : 1;
+    static constexpr int kCtas = TOKENS <= 32 || (TOKENS == 64 && !TILES) ? 2 : 1;
+    static constexpr int kStages = TOKENS == 16 ? 5 - TILES : TOKENS == 32 ? 4 - TILES : TOKENS == 64 && !TILES ? 3 : 4;
     static constexpr int kBufs = TOKENS <= 64 ? 4 : 2;        // TMEM buffers
     static constexpr uint32_t kColumns = TOKENS * kBufs;      // a power of two, 64 .. 256
     static constexpr uint32_t kStageBytes = kTileBytes + TOKENS * 128;
+    static constexpr int kScalers = TOKENS == 16 ? 4 : 8;     // warps
+    static constexpr int kMine = TOKENS * 4 / kScalers;       // tokens per scaling warp: 16, 16, 32, 64
+    static constexpr int kThreads = (kScalers + 2) * 32;      // 10 warps leave 96 registers with two CTAs per SM
 };
 
 template <int TOKENS, bool TILES>
@@ -47,15 +49,16 @@ struct Shared {
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint64_t part_full, part_empty;
     uint32_t tmem;
-    GroupTable groups;
+    int groups[1];  // the group table: as long as the launch asks for
 };
 
 template <int TOKENS, bool TILES>
-constexpr size_t smem_bytes() {
+constexpr size_t smem_bytes(int groups) {
     using S = Shape<TOKENS, TILES>;
     constexpr size_t bytes = 1024 + (size_t)S::kStages * S::kStageBytes + sizeof(Shared<TOKENS, TILES>);
-    static_assert(S::kCtas * (bytes + 1024) <= 228 * 1024, "shared memory of an SM");
-    return bytes;
+    static_assert(S::kCtas * (bytes + group_table_bytes(256) + 1024) <= 228 * 1024, "shared memory of an SM");
+    static_assert(bytes + group_table_bytes(kMaxGroups) <= 227 * 1024, "shared memory of a CTA");
+    return bytes + group_table_bytes(groups);
 }
 
 // One item: a tile of tokens, 128 rows of the weight, this CTA's share of the blocks.
@@ -69,7 +72,7 @@ struct Item {
 template <int TOKENS>
 __device__ __forceinline__ Item locate(const GemmProblem& p, const GroupTable& g, int tiles_n, int t, int rank, int split) {
     Item r;
-    const int e = find_group(&g, p.groups + 1, t);
+    const int e = find_group(g, p.groups + 1, t);
     const int local = t - g.tile[e], begin = e > 0 ? g.end[e - 1] : 0, end = g.end[e];
     const int tiles_m = (end - begin + TOKENS - 1) / TOKENS;
     // tiles of tokens first: neighbours read the same rows of the weight
@@ -83,23 +86,28 @@ __device__ __forceinline__ Item locate(const GemmProblem& p, const GroupTable& g
     return r;
 }
 
-// acc += s_j * P_j over all tokens: scales s at `token` (shared memory), times
-// the lane's own weight-row scale w2 with 1 x 128 tiles.
-template <int TOKENS, bool B_TILES>
+// acc += s_j * P_j over the warp's tokens: scales s at `token` (shared memory),
+// times the lane's own weight-row scale w2 with 1 x 128 tiles.
+template <int MINE, bool B_TILES>
 __device__ __forceinline__ void scale_add(uint64_t* acc, uint32_t from, const float* token, uint64_t w2) {
-    constexpr int kPiece = TOKENS < 32 ? 16 : 32;
+    constexpr int kPiece = MINE <= 32 ? 16 : 32;
 #pragma unroll
-    for (int c = 0; c < TOKENS / kPiece; ++c) {
+    for (int c = 0; c < MINE / kPiece; ++c) {
         uint32_t v[kPiece];
-        if constexpr (kPiece == 16) tmem_ld_32x16(from, v);
+        if constexpr (kPiece == 16) tmem_ld_32x16(from + c * kPiece, v);
         else tmem_ld_32x32(from + c * kPiece, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < kPiece / 2; ++j) {
-            const float2 s = *reinterpret_cast<const float2*>(token + c * kPiece + 2 * j);
-            uint64_t x = pack2(v[2 * j], v[2 * j + 1]), s2 = pack2(s.x, s.y);
-            if constexpr (B_TILES) s2 = mul2(s2, w2);
-            acc[c * kPiece / 2 + j] = fma2(x, s2, acc[c * kPiece / 2 + j]);
+        for (int j = 0; j < kPiece / 2; j += 2) {
+            const float4 s = *reinterpret_cast<const float4*>(token + c * kPiece + 2 * j);
+            uint64_t s0 = pack2(s.x, s.y), s1 = pack2(s.z, s.w);
+            if constexpr (B_TILES) {
+                s0 = mul2(s0, w2);
+                s1 = mul2(s1, w2);
+            }
+            uint64_t* const at = acc + c * kPiece / 2 + j;
+            at[0] = fma2(pack2(v[2 * j], v[2 * j + 1]), s0, at[0]);
+            at[1] = fma2(pack2(v[2 * j + 2], v[2 * j + 3]), s1, at[1]);
         }
     }
 }
@@ -122,7 +130,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 // FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: B [n,
 // k], 1 x 128 tiles.  The cluster's size is the number of shares.
 template <int FORM, int TOKENS>
-__global__ void __launch_bounds__(kThreads, Shape<TOKENS, FORM == 2>::kCtas)
+__global__ void __launch_bounds__(Shape<TOKENS, FORM == 2>::kThreads, Shape<TOKENS, FORM == 2>::kCtas)
 gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ CUtensorMap map_a,
                    const __grid_constant__ CUtensorMap map_b, int split) {
     constexpr bool B_KN = FORM == 1, B_TILES = FORM == 2;
@@ -140,37 +148,50 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
         }
         for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(&sh.tmem_full[i], 1);
-            mbar_init(&sh.tmem_empty[i], 4);
+            mbar_init(&sh.tmem_empty[i], S::kScalers);
         }
         for (int i = 0; i < kScaleSlots; ++i) {
             mbar_init(&sh.sc_full[i], 1);
-            mbar_init(&sh.sc_empty[i], 4);
+            mbar_init(&sh.sc_empty[i], S::kScalers);
         }
-        mbar_init(&sh.part_full, 4 * split);   // four warps of each CTA
-        mbar_init(&sh.part_empty, 4 * split);
+        mbar_init(&sh.part_full, S::kScalers * split);   // the scaling warps of every CTA
+        mbar_init(&sh.part_empty, S::kScalers * split);
         mbar_init_fence();
     }
-    if (warp == 5) tmem_alloc<1>(&sh.tmem, S::kColumns);
+    constexpr int kLoad = S::kScalers, kProduct = kLoad + 1;  // warps
+    if (threadIdx.x == kLoad * 32) {
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
+    }
+    if (warp == kProduct) {
+        tmem_alloc<1>(&sh.tmem, S::kColumns);
+        tmem_fence_before();
+    }
     pdl_begin();
     const int tiles_n = (int)((p.n + kRows - 1) / kRows);
-    const int total = build_groups(&sh.groups, p.ends, p.groups, p.m, TOKENS, 0, tiles_n);
-    tmem_fence_before();
-    if (split > 1) cluster_sync();  // (build_groups has synchronised the CTA)
-    else __syncthreads();
+    const GroupTable groups(sh.groups, p.groups);
+    const int total = build_groups(groups, p.ends, p.groups, p.m, TOKENS, 0, tiles_n);  // synchronises the CTA
+    // Every CTA's barriers are ready before another one arrives on them; the tile
+    // and scale warps, which do not, go ahead without waiting for that.
+    if (split > 1) {
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        if (warp < S::kScalers) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    }
     tmem_fence_after();
     const uint32_t tmem = sh.tmem;
     const int first = blockIdx.x / split, step = gridDim.x / split;
     Waiter w;
 
-    if (warp < 4) {
-        const int row = warp * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    if (warp < S::kScalers) {
+        constexpr int kMine = S::kMine;
+        const int row = (warp & 3) * 32 + lane, token0 = (warp >> 2) * kMine;  // this lane's column of D, this warp's first token
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + token0;
         uint32_t it = 0, group = 0, items = 0;
         for (int t = first; t < total; t += step, ++items) {
-            const Item item = locate<TOKENS>(p, sh.groups, tiles_n, t, rank, split);
-            uint64_t acc[TOKENS / 2];
+            const Item item = locate<TOKENS>(p, groups, tiles_n, t, rank, split);
+            uint64_t acc[kMine / 2];
 #pragma unroll
-            for (int i = 0; i < TOKENS / 2; ++i) acc[i] = 0;
+            for (int i = 0; i < kMine / 2; ++i) acc[i] = 0;
             for (int b = 0; b < item.blks; ++b, ++it) {
                 const uint32_t buf = it % S::kBufs, slot = group % kScaleSlots;
                 const int sub = b % kScaleBlocks;
@@ -183,7 +204,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
                     const float f = sh.weight[slot][sub][row];
                     w2 = pack2(f, f);
                 }
-                scale_add<TOKENS, B_TILES>(acc, lanes + buf * TOKENS, sh.token[slot][sub], w2);
+                scale_add<kMine, B_TILES>(acc, lanes + buf * TOKENS, &sh.token[slot][sub][token0], w2);
                 tmem_fence_before();
                 __syncwarp();
                 const bool last = sub == kScaleBlocks - 1 || b == item.blks - 1;
@@ -193,50 +214,117 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
                 }
                 if (last) ++group;
             }
+            // The partial sums go to shared memory.  Without shares of the contraction every
+            // lane takes its own back; else each CTA adds its part of the tokens over all
+            // CTAs, the first warp of a column quarter the even ones, the second the odd.
             const int64_t col = item.col0 + row;
             const int tokens = min(TOKENS, item.row_end - item.row0);
+            if (split > 1 && items > 0) {
+                w.template wait<true>(smem_addr(&sh.part_empty), (items - 1) & 1);
+                __syncwarp();
+            }
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                const float2 v = unpack2(acc[j >> 1]);
+                if (token0 + j < tokens) sh.part[token0 + j][row] = j & 1 ? v.y : v.x;
+            }
             if (split == 1) {
                 if (col < p.n) {
-#pragma unroll
-                    for (int j = 0; j < TOKENS; ++j) {
-                        const float2 v = unpack2(acc[j >> 1]);
-                        if (j < tokens) store_out(p, (int64_t)(item.row0 + j) * p.n + col, j & 1 ? v.y : v.x);
-                    }
+#pragma unroll 4
+                    for (int j = token0; j < min(token0 + kMine, tokens); ++j)
+                        store_out(p, (int64_t)(item.row0 + j) * p.n + col, sh.part[j][row]);
                 }
                 continue;
-            }
-            // join: every CTA offers its partial sums and adds its share of the tokens over all of them
-            if (items > 0) w.template wait<true>(smem_addr(&sh.part_empty), (items - 1) & 1);
-#pragma unroll
-            for (int j = 0; j < TOKENS; ++j) {
-                const float2 v = unpack2(acc[j >> 1]);
-                if (j < tokens) sh.part[j][row] = j & 1 ? v.y : v.x;
             }
             __syncwarp();
             if (lane < split) cluster_arrive<true>(cluster_addr(smem_addr(&sh.part_full), lane));
             w.template wait<true>(smem_addr(&sh.part_full), items & 1);
             __syncwarp();
             const int j0 = tokens * rank / split, j1 = tokens * (rank + 1) / split;
-            for (int j = j0; j < j1; ++j) {
-                float sum = 0.0f;
+            for (int j = j0 + (warp >> 2); j < j1; j += S::kScalers / 4) {
+                float v[kMostSplit];
 #pragma unroll
-                for (int r = 0; r < kMostSplit; ++r) {
-                    if (r < split) {
-                        const float v = ld_cluster(cluster_addr(smem_addr(&sh.part[j][row]), r));
-                        sum = r == 0 ? v : __fadd_rn(sum, v);
-                    }
-                }
+                for (int r = 0; r < kMostSplit; ++r)
+                    v[r] = r < split ? ld_cluster(cluster_addr(smem_addr(&sh.part[j][row]), r)) : 0.0f;
+                float sum = v[0];
+#pragma unroll
+                for (int r = 1; r < kMostSplit; ++r)
+                    if (r < split) sum = __fadd_rn(sum, v[r]);
                 if (col < p.n) store_out(p, (int64_t)(item.row0 + j) * p.n + col, sum);
             }
             __syncwarp();
-            if (lane < split) cluster_arrive<true>(cluster_addr(smem_addr(&sh.part_empty), lane));
+            // (nothing overwrites the last item's sums)
+            if (lane < split && t + step < total) cluster_arrive<true>(cluster_addr(smem_addr(&sh.part_empty), lane));
         }
-    } else if (warp == 4) {
-        // ---- operand tiles
+    } else if (warp == kLoad) {
+        // ---- operand tiles, and scales: those of the next group of blocks are loaded into
+        // registers while the copies of this group's tiles are issued
+        const int64_t kb = blocks_of(p.k), nb = blocks_of(p.n);
+        const bool wide_a = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sa) & 15u) == 0;
+        const bool wide_b = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sb) & 15u) == 0;
+        constexpr int kTokens = (TOKENS + 31) / 32, kWeights = B_TILES ? 4 : 1;
+        float4 ts[kTokens], ws[kWeights];  // this lane's tokens; its weight rows, or the weight's blocks
+        const auto load_group = [&](const Item& item, int done) {
+            const int g0 = item.blk0 + done, to = min(item.blks - done, kScaleBlocks);
+            const bool whole = g0 % kScaleBlocks == 0;  // an aligned piece of a row of scales
+            if constexpr (B_TILES) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // a token or row that is not there: any scale
+                    const int64_t n = item.col0 + i * 32 + lane;
+                    ws[i] = load_scales(p.sb + (n < p.n ? n : p.n - 1) * kb + g0, to, wide_b && whole);
+                }
+            } else {
+                const int64_t cb = item.col0 / kBlk;
+                const float* const sb = p.sb + (int64_t)item.group * kb * nb;
+                if constexpr (B_KN) {
+                    const float* const at = sb + (int64_t)g0 * nb + cb;
+                    ws[0] = make_float4(__ldg(at), to > 1 ? __ldg(at + nb) : 0.0f, to > 2 ? __ldg(at + 2 * nb) : 0.0f,
+                                        to > 3 ? __ldg(at + 3 * nb) : 0.0f);
+                } else {
+                    ws[0] = load_scales(sb + cb * kb + g0, to, wide_b && whole);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kTokens; ++i) {
+                const int64_t r = item.row0 + min(i * 32 + lane, TOKENS - 1);
+                ts[i] = load_scales(p.sa + (r < p.m ? r : p.m - 1) * kb + g0, to, wide_a && whole);
+            }
+        };
+        uint32_t group = 0;
+        const auto publish = [&]() {
+            const uint32_t slot = group % kScaleSlots;
+            if (group >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (group / kScaleSlots - 1) & 1);
+            __syncwarp();
+            const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f), c = B_TILES ? one : ws[0];
+#pragma unroll
+            for (int i = 0; i < kTokens; ++i) {
+                const int j = i * 32 + lane;
+                if (TOKENS % 32 == 0 || j < TOKENS) {
+                    sh.token[slot][0][j] = __fmul_rn(ts[i].x, c.x);
+                    sh.token[slot][1][j] = __fmul_rn(ts[i].y, c.y);
+                    sh.token[slot][2][j] = __fmul_rn(ts[i].z, c.z);
+                    sh.token[slot][3][j] = __fmul_rn(ts[i].w, c.w);
+                }
+            }
+            if constexpr (B_TILES) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sh.weight[slot][0][i * 32 + lane] = ws[i].x;
+                    sh.weight[slot][1][i * 32 + lane] = ws[i].y;
+                    sh.weight[slot][2][i * 32 + lane] = ws[i].z;
+                    sh.weight[slot][3][i * 32 + lane] = ws[i].w;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.sc_full[slot]);
+            ++group;
+        };
         const uint32_t base = smem_addr(tiles);
         uint32_t it = 0, stage = 0, phase = 0;
+        bool loaded = false;  // the next group's scales are in registers
         for (int t = first; t < total; t += step) {
-            const Item item = locate<TOKENS>(p, sh.groups, tiles_n, t, rank, split);
+            const Item item = locate<TOKENS>(p, groups, tiles_n, t, rank, split);
+            if (!loaded && item.blks > 0) load_group(item, 0);
             for (int b = 0; b < item.blks; ++b, ++it) {
                 const uint32_t wt = base + stage * S::kStageBytes, xt = wt + kTileBytes, bar = smem_addr(&sh.full[stage]);
                 const int x = (item.blk0 + b) * kBlk;
@@ -254,24 +342,48 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
                     stage = 0;
                     phase ^= 1;
                 }
+                // The products of this group's first blocks wait for sums of earlier groups
+                // only, so its scales may follow the copies of its second block (or the last).
+                if (b % kScaleBlocks == 1 || (b % kScaleBlocks == 0 && b == item.blks - 1)) {
+                    publish();
+                    const int next = (b / kScaleBlocks + 1) * kScaleBlocks;
+                    if (next < item.blks) {
+                        load_group(item, next);
+                    } else if (t + step < total) {
+                        const Item after = locate<TOKENS>(p, groups, tiles_n, t + step, rank, split);
+                        loaded = after.blks > 0;
+                        if (loaded) load_group(after, 0);
+                    }
+                }
             }
         }
         // the last fills have been read before the CTA ends
         for (uint32_t i = it > S::kStages ? it - S::kStages : 0; i < it; ++i)
             w.wait(smem_addr(&sh.empty[i % S::kStages]), (i / S::kStages) & 1);
-    } else if (warp == 5) {
+    } else {
         // ---- products: weight rows are M, tokens N
         const uint32_t desc = mma_desc(p.fmt_b, p.fmt_a, B_KN, false, kRows, TOKENS);
         const uint64_t w0 = tile_desc(smem_addr(tiles)), x0 = tile_desc(smem_addr(tiles) + kTileBytes);
         uint32_t it = 0, stage = 0, phase = 0;
+        bool ready = false;  // the next block's tiles and buffer, asked for while this block's products are issued
         for (int t = first; t < total; t += step) {
-            const int blks = locate<TOKENS>(p, sh.groups, tiles_n, t, rank, split).blks;
+            const int blks = locate<TOKENS>(p, groups, tiles_n, t, rank, split).blks;
             for (int b = 0; b < blks; ++b, ++it) {
                 const uint32_t buf = it % S::kBufs;
-                const uint64_t wt = w0 + stage * (S::kStageBytes >> 4), xt = x0 + stage * (S::kStageBytes >> 4);
-                if (it >= S::kBufs) w.wait(smem_addr(&sh.tmem_empty[buf]), (it / S::kBufs - 1) & 1);
-                w.wait(smem_addr(&sh.full[stage]), phase);
+                if (!ready) {
+                    if (it >= S::kBufs) w.wait(smem_addr(&sh.tmem_empty[buf]), (it / S::kBufs - 1) & 1);
+                    w.wait(smem_addr(&sh.full[stage]), phase);
+                }
                 __syncwarp();
+                const uint64_t wt = w0 + stage * (S::kStageBytes >> 4), xt = x0 + stage * (S::kStageBytes >> 4);
+                const uint32_t now = stage;
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+                const uint32_t next = it + 1;
+                const bool free = next < S::kBufs || Waiter::test(smem_addr(&sh.tmem_empty[next % S::kBufs]), (next / S::kBufs - 1) & 1);
+                const bool filled = Waiter::test(smem_addr(&sh.full[stage]), phase);
                 tmem_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -279,86 +391,42 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
                         mma_f8<1>(tmem + buf * TOKENS, wt + k * (B_KN ? kStepMnMajor : kStepKMajor), xt + k * kStepKMajor, desc,
                                   k > 0);
                     mma_commit<1>(smem_addr(&sh.tmem_full[buf]));
-                    mma_commit<1>(smem_addr(&sh.empty[stage]));
+                    mma_commit<1>(smem_addr(&sh.empty[now]));
                 }
-                __syncwarp();
-                if (++stage == S::kStages) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-    } else if (warp == 6) {
-        // ---- scales
-        const int64_t kb = blocks_of(p.k), nb = blocks_of(p.n);
-        const bool wide_a = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sa) & 15u) == 0;
-        const bool wide_b = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sb) & 15u) == 0;
-        uint32_t group = 0;
-        for (int t = first; t < total; t += step) {
-            const Item item = locate<TOKENS>(p, sh.groups, tiles_n, t, rank, split);
-            for (int done = 0; done < item.blks; done += kScaleBlocks, ++group) {
-                const int g0 = item.blk0 + done, to = min(item.blks - done, kScaleBlocks);
-                const bool whole = g0 % kScaleBlocks == 0;  // an aligned piece of a row of scales
-                const uint32_t slot = group % kScaleSlots;
-                float c[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-                if constexpr (!B_TILES) {
-                    const int64_t cb = item.col0 / kBlk;
-                    const float* sb = p.sb + (int64_t)item.group * kb * nb;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < to) c[i] = __ldg(sb + (B_KN ? (int64_t)(g0 + i) * nb + cb : cb * kb + g0 + i));
-                }
-                if (group >= kScaleSlots) w.wait(smem_addr(&sh.sc_empty[slot]), (group / kScaleSlots - 1) & 1);
-                __syncwarp();
-#pragma unroll
-                for (int j = lane; j < TOKENS; j += 32) {  // a token or row that is not there: any scale
-                    const int64_t r = item.row0 + j;
-                    const float4 a = load_scales(p.sa + (r < p.m ? r : p.m - 1) * kb + g0, to, wide_a && whole);
-                    sh.token[slot][0][j] = __fmul_rn(a.x, c[0]);
-                    sh.token[slot][1][j] = __fmul_rn(a.y, c[1]);
-                    sh.token[slot][2][j] = __fmul_rn(a.z, c[2]);
-                    sh.token[slot][3][j] = __fmul_rn(a.w, c[3]);
-                }
-                if constexpr (B_TILES) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int64_t n = item.col0 + i * 32 + lane;
-                        const float4 b = load_scales(p.sb + (n < p.n ? n : p.n - 1) * kb + g0, to, wide_b && whole);
-                        sh.weight[slot][0][i * 32 + lane] = b.x;
-                        sh.weight[slot][1][i * 32 + lane] = b.y;
-                        sh.weight[slot][2][i * 32 + lane] = b.z;
-                        sh.weight[slot][3][i * 32 + lane] = b.w;
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.sc_full[slot]);
+                ready = __all_sync(0xFFFFFFFFu, free && filled);
             }
         }
     }
     __syncwarp();
     tmem_fence_before();
-    if (split > 1) cluster_sync();  // no CTA leaves while another reads its partial sums
-    else __syncthreads();
+    if (split > 1) {  // no CTA leaves while another reads its partial sums
+        if (warp >= S::kScalers) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        cluster_meet();
+    } else {
+        __syncthreads();
+    }
     tmem_fence_after();
-    if (warp == 5) tmem_free<1>(tmem, S::kColumns);
+    if (warp == kProduct) tmem_free<1>(tmem, S::kColumns);
 }
 
 template <int TOKENS>
 fp8_status_t run(const char* fn, const GemmProblem& p, const CUtensorMap& a, const CUtensorMap& b, cudaStream_t st) {
     const int64_t tiles_n = (p.n + kRows - 1) / kRows, tiles_m = (p.m + TOKENS - 1) / TOKENS;
     const int64_t busy = p.groups < p.m ? p.groups : p.m;  // groups with rows, at most
-    const int64_t items = (tiles_m + busy - 1) * tiles_n, slots = (int64_t)sm_count() * Shape<TOKENS, false>::kCtas;
+    const int ctas = p.b_tiles ? Shape<TOKENS, true>::kCtas : Shape<TOKENS, false>::kCtas;  // per SM
+    const int64_t items = (tiles_m + busy - 1) * tiles_n, slots = (int64_t)sm_count() * ctas;
     // shares of the contraction: as many as fill the SMs, each at least two blocks long
     const int64_t kb = blocks_of(p.k);
     int split = 1;
     while (split < kMostSplit && items * (split + 1) <= slots && kb >= 2 * (split + 1)) ++split;
     const int64_t most = slots / split, clusters = items + 1 < most ? items + 1 : most;
     const auto go = [&](auto kernel, size_t smem) {
-        return launch_cluster(fn, kernel, dim3((unsigned)(clusters * split)), dim3(kThreads), smem, split, st, p, a, b, split);
+        return launch_cluster(fn, kernel, dim3((unsigned)(clusters * split)), dim3(Shape<TOKENS, false>::kThreads), smem, split, st,
+                              p, a, b, split);
     };
-    return p.b_tiles ? go(gemm_stream_kernel<2, TOKENS>, smem_bytes<TOKENS, true>())
-           : p.b_kn  ? go(gemm_stream_kernel<1, TOKENS>, smem_bytes<TOKENS, false>())
-                     : go(gemm_stream_kernel<0, TOKENS>, smem_bytes<TOKENS, false>());
+    return p.b_tiles ? go(gemm_stream_kernel<2, TOKENS>, smem_bytes<TOKENS, true>(p.groups))
+           : p.b_kn  ? go(gemm_stream_kernel<1, TOKENS>, smem_bytes<TOKENS, false>(p.groups))
+                     : go(gemm_stream_kernel<0, TOKENS>, smem_bytes<TOKENS, false>(p.groups));
 }
 
 }  // namespace
