@@ -60,6 +60,10 @@ Workspace* stream_workspace(cudaStream_t stream, fp8_status_t* st);
 // failure (the error message is set).
 void* stream_scratch(cudaStream_t stream, size_t bytes, fp8_status_t* st);
 
+// Let `kernel` use `smem` bytes of dynamic shared memory on the current device
+// (asked of the runtime once per kernel, device and size).
+fp8_status_t allow_smem(const char* what, const void* kernel, size_t smem);
+
 // Launch `kernel` on `st` with `smem` bytes of dynamic shared memory and
 // programmatic stream serialization allowed (the kernel starts with
 // pdl_begin()), then check and count the launch.
@@ -67,8 +71,8 @@ template <typename... KArgs, typename... Args>
 fp8_status_t launch_smem(const char* what, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                          cudaStream_t st, Args... args) {
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return cuda_status(e, what);
+        const fp8_status_t s = allow_smem(what, reinterpret_cast<const void*>(kernel), smem);
+        if (s != FP8_OK) return s;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -109,8 +113,8 @@ template <typename... KArgs, typename... Args>
 fp8_status_t launch_cluster(const char* what, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
                             cudaStream_t st, Args... args) {
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return cuda_status(e, what);
+        const fp8_status_t s = allow_smem(what, reinterpret_cast<const void*>(kernel), smem);
+        if (s != FP8_OK) return s;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;

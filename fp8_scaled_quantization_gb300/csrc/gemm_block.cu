@@ -5,7 +5,7 @@
 // Precision Training and Rollout" (128x128 weight blocks), "[Pytorch][Common]
 // Hybrid quantization #2817" (1x128 / 128x1 blockwise copies for the backward
 // GEMMs), "Megatron FP8" §21 (experts).
-#include <cstdlib>
+#include <cmath>
 
 #include "fp8q_host.h"
 #include "gemm_block.cuh"
@@ -124,16 +124,52 @@ fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, 
 }
 
 namespace {
-// Which kernel: the stream kernel while the tiles of the pair kernel would leave
-// most of the SMs without work or most rows of a tile empty.
+// Which kernel, by estimated times in microseconds from what both measured on
+// GB300 (one call, in a CUDA graph, cold weights; [m, n, k] bf16 out):
+//   [1, 7168, 18432]   stream/16 24   pair 68      [48, 14336, 4096]  stream/32 18  stream/64 19  pair 22
+//   [64, 7168, 7168]   stream/64 17   pair 30      [256, 4096, 4096]  stream/32 17  stream/128 20 pair 20
+//   [256, 7168, 7168]  pair 31  stream/128 32      [512, 1024, 4096]  stream/64 12  pair 19
+//   [256, 256, 16384] in 1 x 128 tiles  stream/16 11  pair 96
+//   [512, 7168, 7168] in 1 x 128 tiles  pair 47  stream/128 70
+// A pair of CTAs takes 0.5 (1 x 128 tiles: 0.73) per 128-block of a 256 x 256
+// tile, whatever part of the tile is used.  A CTA of the stream kernel takes
+// 0.28 / 0.39 / 0.59 / 0.48 per block with 16 / 32 / 64 / 128 tokens (two
+// CTAs per SM up to 64).  Neither is faster than the operands come from memory,
+// where the stream kernel reaches 6.5 TB/s and the pair kernel 4.5 (96 rows over
+// 64 experts, 2048 x 7168 each: stream/16 99, stream/32 107, pair 137).
+struct Choice {
+    int tokens;  // 0: the pair kernel
+    double us;
+};
+
+Choice choose(const GemmProblem& p) {
+    const int64_t kb = blocks_of(p.k), sms = sm_count();
+    const double busy = (double)(p.groups < p.m ? p.groups : p.m);
+    const auto tiles = [&](int rows) {  // along m: the groups' last tiles are half full on average
+        return p.groups > 1 ? (double)p.m / rows + 0.5 * busy : (double)((p.m + rows - 1) / rows);
+    };
+    const auto most = [](double a, double b) { return a > b ? a : b; };
+    const double memory = (busy * (double)p.n * (double)p.k + (double)p.m * (double)(p.k + 2 * p.n)) / 6.5e6;
+    const double pair = ceil(tiles(256) * (double)((p.n + 255) / 256) / (double)(sms / 2)) * (double)kb * (p.b_tiles ? 0.73 : 0.5);
+    Choice best = {0, 4.0 + most(pair, memory * 6.5 / 4.5)};
+    constexpr double kBlock[4] = {0.28, 0.39, 0.59, 0.48}, kJoin[4] = {1.2, 2.5, 5.0, 8.0};
+    for (int i = 0; i < 4; ++i) {
+        const int tokens = 16 << i;
+        const double items = tiles(tokens) * (double)((p.n + 127) / 128), slots = (double)sms * (tokens <= 64 ? 2 : 1);
+        double split = slots / items;
+        split = split < 1 ? 1 : split > 8 ? 8 : (double)(int)split;
+        if (split > kb / 2) split = kb > 2 ? (double)(kb / 2) : 1;
+        const double compute = ceil(items * split / slots) * ceil((double)kb / split) * kBlock[i];
+        const double us = 5.0 + (split > 1 ? kJoin[i] : 0.0) + most(compute, memory);
+        if (us < best.us) best = {tokens, us};
+    }
+    return best;
+}
+
 fp8_status_t run_gemm(const char* fn, const GemmProblem& p, cudaStream_t st) {
-    if (p.b_tiles && p.ends != nullptr) return run_gemm_pair(fn, p, st);  // ragged contraction
-    static const char* force = getenv("FP8_FORCE_GEMM");
-    if (force && p.k > 0 && atoi(force) > 0) return run_gemm_stream(fn, p, atoi(force), st);
-    if (force) return run_gemm_pair(fn, p, st);
-    const int64_t rows = p.groups > 1 ? (p.m + p.groups - 1) / p.groups : p.m;
-    if (p.k == 0 || rows > 128) return run_gemm_pair(fn, p, st);
-    return run_gemm_stream(fn, p, rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128, st);
+    if (p.k == 0 || (p.b_tiles && p.ends != nullptr)) return run_gemm_pair(fn, p, st);  // nothing to sum; ragged contraction
+    const int tokens = choose(p).tokens;
+    return tokens > 0 ? run_gemm_stream(fn, p, tokens, st) : run_gemm_pair(fn, p, st);
 }
 }  // namespace
 

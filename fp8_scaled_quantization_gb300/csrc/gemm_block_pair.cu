@@ -396,26 +396,16 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                 const uint32_t desc = mma_desc(p.fmt_a, p.fmt_b, false, B_KN, kPairM, kPairN);
                 const uint64_t a0 = tile_desc(smem_addr(tiles)), b0 = tile_desc(smem_addr(tiles) + kTileBytes);
                 uint32_t it = 0, stage = 0, phase = 0;
-                bool ready = false;  // the next block's tiles and buffer, asked for while this block's products are issued
                 for (int t = first; t < total; t += step) {
                     const int blks = locate<RAGGED_K>(p, groups, count, tiles_n, t).blks;
                     for (int b = 0; b < blks; ++b, ++it) {
-                        const uint32_t buf = it & 1;
-                        if (!ready) {
-                            // (tiles that were masked with plain stores are released to the cluster)
-                            w.template wait<RAGGED_K>(smem_addr(&sh.full[stage]), phase);
-                            if (it >= 2) w.wait(smem_addr(&sh.tmem_empty[buf]), ((it >> 1) - 1) & 1);
-                        }
-                        __syncwarp();
+                        const uint32_t buf = it & 1, free_bar = smem_addr(&sh.tmem_empty[buf]), free_phase = ((it >> 1) & 1) ^ 1;
                         const uint64_t at = a0 + stage * (kStageBytes >> 4), bt = b0 + stage * (kStageBytes >> 4);
-                        const uint32_t now = stage;
-                        if (++stage == kStages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
-                        const uint32_t next = it + 1;
-                        const bool free = next < 2 || Waiter::test(smem_addr(&sh.tmem_empty[next & 1]), ((next >> 1) - 1) & 1);
-                        const bool filled = !RAGGED_K && Waiter::test(smem_addr(&sh.full[stage]), phase);
+                        const bool is_free = it < 2 || Waiter::test(free_bar, free_phase);
+                        // (tiles that were masked with plain stores are released to the cluster)
+                        w.template wait<RAGGED_K>(smem_addr(&sh.full[stage]), phase);
+                        if (!is_free) w.wait(free_bar, free_phase);
+                        __syncwarp();
                         tmem_fence_after();
                         if (elect_one()) {
 #pragma unroll
@@ -423,9 +413,13 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                                 mma_f8<2>(tmem + buf * kPairN, at + k * kStepKMajor,
                                           bt + k * (B_KN ? kStepMnMajor : kStepKMajor), desc, k > 0);
                             mma_commit<2>(smem_addr(&sh.tmem_full[buf]));
-                            mma_commit<2>(smem_addr(&sh.empty[now]));
+                            mma_commit<2>(smem_addr(&sh.empty[stage]));
                         }
-                        ready = __all_sync(0xFFFFFFFFu, free && filled);
+                        __syncwarp();
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
                     }
                 }
             }

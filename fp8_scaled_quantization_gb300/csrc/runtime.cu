@@ -49,6 +49,20 @@ fp8_status_t after_launch(const char* kernel) {
     return FP8_OK;
 }
 
+fp8_status_t allow_smem(const char* what, const void* kernel, size_t smem) {
+    static std::map<std::pair<const void*, int>, size_t> allowed;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_status(e, what);
+    std::lock_guard<std::mutex> lk(g_mu);
+    size_t& had = allowed[std::make_pair(kernel, dev)];
+    if (had >= smem) return FP8_OK;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_status(e, what);
+    had = smem;
+    return FP8_OK;
+}
+
 int sm_count() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;

@@ -13,6 +13,9 @@ call into the CUDA library.
                      scale), or fp8_quantize -> fp8_update_scale_delayed
   BlockScaling       "Low Precision Training and Rollout": fp8_quantize_block
                      128 x 128 (weight) and 1 x 128 (activation)
+  BlockLinearStep    "Low Precision Training and Rollout" / "Megatron FP8" §6, §21: one training step of
+                     a layer (or of an MoE layer's experts) in block-scaled FP8 -- quantize, the
+                     forward product, both gradients, and the clipped weight gradient
   GradientQDQ        E5M2 current scaling then fp8_dequantize back to BF16, per tensor or
                      with one grouped amax + scale call over all tensors (§21)
 """
@@ -22,9 +25,11 @@ from dataclasses import dataclass, field
 
 import torch
 
-from . import (AMAX_MAX, E4M3, E5M2, fp8_amax, fp8_amax_grouped, fp8_dequantize, fp8_quantize, fp8_quantize_block,
+from . import (AMAX_MAX, B_KN, E4M3, E5M2, fp8_amax, fp8_amax_grouped, fp8_dequantize, fp8_quantize, fp8_quantize_block,
                fp8_quantize_cast_transpose, fp8_quantize_current, fp8_quantize_delayed, fp8_quantize_grouped,
                fp8_update_scale_delayed)
+from . import (fp8_gemm_block, fp8_gemm_block_grouped, fp8_gemm_block_grouped_wgrad, fp8_grad_clip_grouped,
+               fp8_quantize_block_cast_transpose)
 
 
 def _f32(dev, n=1, fill=None):
@@ -185,6 +190,82 @@ class BlockScaling:
         b = KernelBytes()
         b.add("block128x128", self.w.numel() * (esize(self.w) + 1) + self.si_w.numel() * 4)
         b.add("block1x128", self.a.numel() * (esize(self.a) + 1) + self.si_a.numel() * 4)
+        return b
+
+
+class BlockLinearStep:
+    """One training step of a linear layer in block-scaled FP8, master weights and
+    activations in BF16:
+      quantize   x (1 x 128 tiles and the columnwise copy), weight (128 x 128 blocks)
+      y          = x weight^T
+      quantize   dy (both directions)
+      dx         = dy weight, from the same weight codes
+      dweight    = dy^T x in fp32, from the two columnwise copies
+      clip       dweight to `max_norm`, in place
+    weight [out, in] is one layer; weight [experts, out, in] with group_ends (int64
+    [experts], device: rows of x and dy sorted by expert) is an MoE layer's experts.
+    out must be a multiple of 128 with experts, so that no block spans two of them."""
+
+    def __init__(self, x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, group_ends: torch.Tensor = None,
+                 fmt: int = E4M3, grad_fmt: int = E4M3, max_norm: float = 1.0):
+        if (weight.dim() == 3) != (group_ends is not None):
+            raise ValueError("weight [experts, out, in] goes with group_ends, weight [out, in] without")
+        out, inn = weight.shape[-2:]
+        if weight.dim() == 3 and out % 128:
+            raise ValueError("out must be a multiple of 128 with experts")
+        self.x, self.weight, self.dy, self.ends = x, weight, dy, group_ends
+        self.fmt, self.grad_fmt, self.max_norm = fmt, grad_fmt, max_norm
+        dev, rows = x.device, x.shape[0]
+
+        def both(c):  # rowwise and columnwise codes with their factors
+            return [torch.empty((rows, c), dtype=torch.uint8, device=dev), _f32(dev, rows * -(-c // 128)).view(rows, -1),
+                    torch.empty((c, rows), dtype=torch.uint8, device=dev), _f32(dev, c * -(-rows // 128)).view(c, -1)]
+
+        self.qx, self.qdy = both(inn), both(out)
+        self.qw = torch.empty(weight.shape, dtype=torch.uint8, device=dev)
+        blocks = (*weight.shape[:-2], -(-out // 128), -(-inn // 128))
+        self.sw = torch.empty(blocks, dtype=torch.float32, device=dev)
+        self.y = torch.empty((rows, out), dtype=torch.bfloat16, device=dev)
+        self.dx = torch.empty((rows, inn), dtype=torch.bfloat16, device=dev)
+        self.dweight = torch.empty(weight.shape, dtype=torch.float32, device=dev)
+        self.norm = _f32(dev)
+
+    def _product(self, a, sa, fmt_a, d, layout):
+        if self.ends is None:
+            fp8_gemm_block(a, sa, self.qw, self.sw, d, fmt_a, self.fmt, b_layout=layout)
+        else:
+            fp8_gemm_block_grouped(a, sa, self.qw, self.sw, self.ends, d, fmt_a, self.fmt, b_layout=layout)
+
+    def run(self, timer=None):
+        w2, s2 = self.weight.view(-1, self.weight.shape[-1]), self.sw.view(-1, self.sw.shape[-1])
+        _t(timer, "quantize_weight", lambda: fp8_quantize_block(w2, 128, 128, self.fmt, self.qw.view(w2.shape), s2))
+        _t(timer, "quantize_x", lambda: fp8_quantize_block_cast_transpose(self.x, self.fmt, *self.qx))
+        _t(timer, "forward", lambda: self._product(self.qx[0], self.qx[1], self.fmt, self.y, 0))
+        _t(timer, "quantize_dy", lambda: fp8_quantize_block_cast_transpose(self.dy, self.grad_fmt, *self.qdy))
+        _t(timer, "dgrad", lambda: self._product(self.qdy[0], self.qdy[1], self.grad_fmt, self.dx, B_KN))
+        _t(timer, "wgrad", self._wgrad)
+        _t(timer, "clip", lambda: fp8_grad_clip_grouped([self.dweight], self.max_norm, self.norm))
+
+    def _wgrad(self):
+        a, sa, b, sb = *self.qdy[2:], *self.qx[2:]
+        if self.ends is None:
+            fp8_gemm_block(a, sa, b, sb, self.dweight, self.grad_fmt, self.fmt, b_block_rows=1)
+        else:
+            fp8_gemm_block_grouped_wgrad(a, sa, b, sb, self.ends, self.dweight, self.grad_fmt, self.fmt)
+
+    def bytes(self) -> KernelBytes:
+        b, w = KernelBytes(), self.weight
+        rows, out, inn = self.x.shape[0], *w.shape[-2:]
+        scales = {c: 4 * rows * -(-c // 128) for c in (out, inn)}            # rowwise
+        columns = {c: 4 * c * -(-rows // 128) for c in (out, inn)}           # columnwise
+        codes, blocks = w.numel(), self.sw.numel() * 4
+        b.add("quantize_weight", w.numel() * (esize(w) + 1) + blocks)
+        b.add("quantize_x", rows * inn * (esize(self.x) + 2) + scales[inn] + columns[inn])
+        b.add("forward", rows * inn + scales[inn] + codes + blocks + rows * out * 2)
+        b.add("quantize_dy", rows * out * (esize(self.dy) + 2) + scales[out] + columns[out])
+        b.add("dgrad", rows * out + scales[out] + codes + blocks + rows * inn * 2)
+        b.add("wgrad", rows * (out + inn) + columns[out] + columns[inn] + w.numel() * 4)
+        b.add("clip", w.numel() * 4 * 2)
         return b
 
 

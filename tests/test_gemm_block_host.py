@@ -172,3 +172,21 @@ def test_clip_binding_checks(native_lib):
         fq.fp8_grad_clip_grouped(xs, 1.0, ys=xs[::-1])
     with pytest.raises(ValueError, match="non-empty"):
         fq.fp8_grad_norm_grouped([], torch.zeros(1))
+
+
+# ------------------------------------------------------------ a layer's step
+
+def test_block_linear_step_refuses_and_accounts():
+    from fp8_scaled_quantization_gb300 import pipelines as P
+    meta = torch.device("meta")
+    mk = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=meta)  # noqa: E731
+    with pytest.raises(ValueError, match="group_ends"):
+        P.BlockLinearStep(mk(8, 256), mk(2, 128, 256), mk(8, 128))
+    with pytest.raises(ValueError, match="multiple of 128"):
+        P.BlockLinearStep(mk(8, 256), mk(2, 100, 256), mk(8, 100), torch.empty(2, dtype=torch.int64, device=meta))
+    b = P.BlockLinearStep(mk(512, 256), mk(128, 256), mk(512, 128)).bytes()
+    codes, tokens = 128 * 256, 512
+    assert b.per_kernel["forward"] == (tokens * 256 + 4 * tokens * 2 + codes + 4 * 2 + tokens * 128 * 2, 1)
+    assert b.per_kernel["dgrad"] == (tokens * 128 + 4 * tokens + codes + 4 * 2 + tokens * 256 * 2, 1)
+    assert b.per_kernel["wgrad"] == (tokens * 384 + 4 * 384 * 4 + codes * 4, 1)
+    assert b.per_kernel["clip"] == (codes * 8, 1) and b.launches == 7
