@@ -13,12 +13,16 @@
 // warp 10 fills the ring of operand tiles by bulk copies; warp 11 zeroes the
 // steps of other groups in blocks that a ragged group's end cuts.
 //
-// What bounds it: a warp's arithmetic takes 146 of the 512 cycles that the
-// tensor core needs for a block, and two warps share a scheduler, so the
-// latencies between (a barrier's answer 150-180 cycles, a load of TMEM, shared
-// memory, a local-memory spill 300) decide.  Hence: barriers are asked one step
-// early, TMEM is read one piece ahead, the scales lie ready as one word per row
-// and block, and nothing may spill.
+// What bounds it: the scaling warps.  A block takes the tensor core 512 cycles
+// and the warps about 890 (1 x 128 tiles: 1340): the arithmetic of a scheduler's
+// two warps is 292, and the way of each warp through a block -- the barrier's
+// answer 190 cycles, four reads of TMEM with their arithmetic 100 each, the
+// arrival, the loop -- hides behind the other's in part only.  A third warp per
+// scheduler or reads further ahead do not fit the registers: any spill costs
+// more (a load from local memory takes 300 cycles with shared memory this full).
+// Measured: 8192^3 418 us, 2630 TFLOP/s; 16384 x 18432 x 7168 in one call 1.6
+// ms; products alone, without scaling, would take 266 us.  The SM clock falls
+// from 2070 to about 1850 MHz meanwhile (power).
 #include "fp8q_host.h"
 #include "fp8q_tcgen05.cuh"
 #include "gemm_block.cuh"
@@ -28,14 +32,24 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kPairM = 256, kPairN = 256;  // outputs of a pair
-constexpr int kStages = 5;                 // operand ring: A and B tile, 32 KB per CTA and stage
 constexpr int kScaleBlocks = 4;            // blocks of a tile whose scales are gathered together
 constexpr int kScaleSlots = 3;             // such groups in the scale ring
 constexpr int kRaster = 8;                 // tiles along m that are walked before the next tile along n
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
-constexpr uint32_t kOutBytes = 32 * 128;   // one warp's staging: 32 rows of 128 bytes
+constexpr uint32_t kOutBytes = 32 * 128;   // one staging buffer of a warp: 32 rows of 128 bytes
 
+// Operand ring (A and B tile, 32 KB per CTA and stage) and staging buffers per
+// warp.  With 128 x 128 blocks two buffers gain 2% and the fifth stage nothing;
+// with ragged contractions, whose cut blocks stay longer in the ring, the fifth
+// stage is worth 4%.
+template <bool TILES>
+struct Ring {
+    static constexpr int kStages = TILES ? 5 : 4, kOuts = TILES ? 1 : 2;
+};
+
+template <bool TILES>
 struct Shared {
+    static constexpr int kStages = Ring<TILES>::kStages;
     union {
         float4 rows[kScaleSlots][2][128];  // 128 x 128 blocks: per column half and row, row scale x column block scale
         struct {
@@ -49,8 +63,13 @@ struct Shared {
     uint32_t tmem;
     int groups[2 * kMaxGroups + 3];
 };
-constexpr size_t kSmemBytes = 1024 + (size_t)kStages * kStageBytes + 8 * kOutBytes + sizeof(Shared);
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+template <bool TILES>
+constexpr size_t smem_bytes() {
+    constexpr size_t bytes =
+        1024 + (size_t)Ring<TILES>::kStages * kStageBytes + 8 * Ring<TILES>::kOuts * kOutBytes + sizeof(Shared<TILES>);
+    static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+    return bytes;
+}
 
 // Where a tile's operands and outputs lie.
 struct Tile {
@@ -174,13 +193,15 @@ __device__ __forceinline__ void store_direct(const GemmProblem& p, const uint64_
 // drops what lies outside D.
 template <bool TILES>
 __device__ __forceinline__ void store_bulk(const GemmProblem& p, const CUtensorMap* map, const uint64_t (&acc)[64],
-                                           uint32_t stage, int lane, int64_t row0, int64_t c0, int z) {
+                                           uint32_t stages, int lane, int64_t row0, int64_t c0, int z) {
 #pragma unroll
     for (int part = 0; part < 4; ++part) {
+        const uint32_t stage = stages + part % Ring<TILES>::kOuts * kOutBytes;
         if (part >= 2 && !p.out_f32) break;
         const int64_t x = c0 + part * (p.out_f32 ? 32 : 64);
         if (x >= p.n) break;
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the staging is free
+        if (lane == 0)  // this buffer has been read
+            asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(Ring<TILES>::kOuts - 1) : "memory");
         __syncwarp();
         if constexpr (TILES) {
             if (p.out_f32) {
@@ -245,10 +266,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ CUtensorMap map_a,
                  const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d, bool bulk_store) {
     constexpr bool RAGGED_K = FORM == 2, B_KN = FORM == 1, B_TILES = FORM == 2;
+    constexpr int kStages = Ring<B_TILES>::kStages, kOuts = Ring<B_TILES>::kOuts;
     extern __shared__ uint8_t raw[];
     uint8_t* const tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* const out = tiles + kStages * kStageBytes;
-    Shared& sh = *reinterpret_cast<Shared*>(out + 8 * kOutBytes);
+    Shared<B_TILES>& sh = *reinterpret_cast<Shared<B_TILES>*>(out + 8 * kOuts * kOutBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
 
@@ -315,7 +337,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                 if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
             };
             if (!B_TILES && tile.blks > 0) fetch();
-            bool ready = false;
+            bool ready = false;  // (asking one block ahead pays with 1 x 128 tiles only)
             for (int b = 0; b < tile.blks; ++b) {
                 const uint32_t buf = it & 1, from = lanes + buf * kPairN;
                 const int sub = b % kScaleBlocks;
@@ -323,7 +345,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                 if (!B_TILES) {
                     s4 = sub == 0 ? s4_next : make_float4(s4.y, s4.z, s4.w, 0.0f);
                 }
-                if (!ready) w.wait(full0 + buf * 8, (it >> 1) & 1);
+                if (!B_TILES || !ready) w.wait(full0 + buf * 8, (it >> 1) & 1);
                 __syncwarp();  // lanes may have left the wait apart
                 tmem_fence_after();
                 ++it;
@@ -331,7 +353,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) cluster_arrive<false>(empty0 + buf * 8);
-                    ready = b + 1 < tile.blks && Waiter::test(full0 + (it & 1) * 8, (it >> 1) & 1);
+                    if (B_TILES) ready = b + 1 < tile.blks && Waiter::test(full0 + (it & 1) * 8, (it >> 1) & 1);
                 };
                 uint32_t v[32];
                 if constexpr (B_TILES) {
@@ -381,7 +403,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             // store: this warp's 32 rows, 128 columns
             const int64_t r0 = tile.row0 + (int)rank * 128 + (warp & 3) * 32, c0 = tile.col0 + half * 128;
             if (bulk_store && r0 + 31 < tile.row_end) {
-                store_bulk<B_TILES>(p, &map_d, acc, smem_addr(out) + warp * kOutBytes, lane, r0, c0, RAGGED_K ? tile.group : 0);
+                store_bulk<B_TILES>(p, &map_d, acc, smem_addr(out) + warp * kOuts * kOutBytes, lane, r0, c0, RAGGED_K ? tile.group : 0);
             } else {
                 store_direct<B_TILES>(p, acc, lane, RAGGED_K ? (int64_t)tile.group * p.m * p.n : 0, r0, tile.row_end, c0);
             }
@@ -565,10 +587,12 @@ fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st
     const int64_t tiles_n = (p.n + kPairN - 1) / kPairN, tiles_m = (p.m + kPairM - 1) / kPairM;
     const int64_t most = p.b_tiles ? tiles_m * tiles_n * p.groups : (tiles_m + p.groups - 1) * tiles_n;
     const int sms = sm_count() / 2, pairs = (int)(most < sms ? most : sms);
-    const auto go = [&](auto kernel) {
-        return launch_smem(fn, kernel, dim3(2 * pairs), dim3(kThreads), kSmemBytes, st, p, a, b, d, bulk);
+    const auto go = [&](auto kernel, size_t smem) {
+        return launch_smem(fn, kernel, dim3(2 * pairs), dim3(kThreads), smem, st, p, a, b, d, bulk);
     };
-    return p.b_tiles ? go(gemm_pair_kernel<2>) : p.b_kn ? go(gemm_pair_kernel<1>) : go(gemm_pair_kernel<0>);
+    return p.b_tiles ? go(gemm_pair_kernel<2>, smem_bytes<true>())
+           : p.b_kn  ? go(gemm_pair_kernel<1>, smem_bytes<false>())
+                     : go(gemm_pair_kernel<0>, smem_bytes<false>());
 }
 
 fp8_status_t gemm_pair_wait_timeouts(unsigned long long* count) {
