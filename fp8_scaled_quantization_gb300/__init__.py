@@ -13,7 +13,8 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
-from array import array
+import struct
+from operator import attrgetter
 
 import torch
 
@@ -140,9 +141,10 @@ def _stream(stream) -> int | None:
 
 
 def _rows_cols(x: torch.Tensor):
-    if x.dim() != 2:
-        raise ValueError(f"expected a 2-D tensor, got shape {tuple(x.shape)}")
-    return int(x.shape[0]), int(x.shape[1])
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"expected a 2-D tensor, got shape {tuple(shape)}")
+    return shape[0], shape[1]
 
 
 def fp8_amax(x, amax_out, fmt=E4M3, margin=0, scale_out=None, scale_inv_out=None, stream=None):
@@ -351,19 +353,21 @@ def fp8_quantize_current(x, fmt, q_out, margin=0, amax_out=None, scale_out=None,
 
 def _operand(q, scale_inv, shape, scale_shape, name):
     """Shape and type checks of one operand of a product."""
-    if q.dtype != torch.uint8 or q.shape != shape:
+    if q.dtype is not torch.uint8 or q.shape != shape:
         raise ValueError(f"{name} must be uint8 {shape}")
-    if scale_inv.dtype != torch.float32 or scale_inv.shape != scale_shape:
+    if scale_inv.dtype is not torch.float32 or scale_inv.shape != scale_shape:
         raise ValueError(f"scale_inv_{name} must be float32 {scale_shape}")
 
 
 def _ptrs(*tensors):
     """Data pointers of contiguous tensors on the current CUDA device (one look at the device for all)."""
     here = torch.cuda.current_device() if tensors[0].is_cuda else None
+    out = []
     for t in tensors:
         if t.get_device() != here or not t.is_contiguous():
             _p(t)  # says what is wrong with it
-    return [t.data_ptr() or None for t in tensors]
+        out.append(t.data_ptr() or None)
+    return out
 
 
 def _ends(group_ends):
@@ -372,23 +376,31 @@ def _ends(group_ends):
     return group_ends.shape[0]
 
 
+def _out(d, rows):
+    """Columns of an output [rows, n]."""
+    shape = d.shape
+    if len(shape) != 2 or shape[0] != rows:
+        raise ValueError(f"d must be [{rows}, n]")
+    return shape[1]
+
+
 def fp8_gemm_block(a, scale_inv_a, b, scale_inv_b, d, fmt_a=E4M3, fmt_b=E4M3, b_layout=B_NK, b_block_rows=128,
                    accumulate=False, stream=None):
     """d[m, n] = the product of block-scaled operands: a [m, k] codes with 1 x 128 factors,
     b [n, k] (B_NK) or [k, n] (B_KN) codes with 128 x 128 factors (or, with b_block_rows=1
     and B_NK, 1 x 128 factors).  d is bfloat16 or float32; accumulate adds to a float32 d."""
     m, k = _rows_cols(a)
-    if d.dim() != 2 or d.shape[0] != m:
-        raise ValueError(f"d must be [{m}, n]")
-    n = d.shape[1]
+    n = _out(d, m)
     kb = -(-k // 128)
     rows_b = n if b_block_rows == 1 else -(-n // 128)
-    shape, scales = ((k, n), (kb, rows_b)) if b_layout == B_KN else ((n, k), (rows_b, kb))
     _operand(a, scale_inv_a, (m, k), (m, kb), "a")
-    _operand(b, scale_inv_b, shape, scales, "b")
+    if b_layout == B_KN:
+        _operand(b, scale_inv_b, (k, n), (kb, rows_b), "b")
+    else:
+        _operand(b, scale_inv_b, (n, k), (rows_b, kb), "b")
     pa, psa, pb, psb, pd = _ptrs(a, scale_inv_a, b, scale_inv_b, d)
     _check(library().fp8_gemm_block(pa, fmt_a, psa, pb, fmt_b, psb, b_layout, b_block_rows, m, n, k, pd, _dt(d),
-                                    int(accumulate), _stream(stream)))
+                                    1 if accumulate else 0, _stream(stream)))
 
 
 def fp8_gemm_block_grouped(a, scale_inv_a, b, scale_inv_b, group_ends, d, fmt_a=E4M3, fmt_b=E4M3, b_layout=B_NK,
@@ -398,9 +410,7 @@ def fp8_gemm_block_grouped(a, scale_inv_a, b, scale_inv_b, group_ends, d, fmt_a=
     rows after the last end become zeros.  group_ends: int64 on the device."""
     rows, k = _rows_cols(a)
     groups = _ends(group_ends)
-    if d.dim() != 2 or d.shape[0] != rows:
-        raise ValueError(f"d must be [{rows}, n]")
-    n = d.shape[1]
+    n = _out(d, rows)
     kb, nb = -(-k // 128), -(-n // 128)
     shape, scales = ((groups, k, n), (groups, kb, nb)) if b_layout == B_KN else ((groups, n, k), (groups, nb, kb))
     _operand(a, scale_inv_a, (rows, k), (rows, kb), "a")
@@ -430,21 +440,25 @@ def fp8_gemm_block_grouped_wgrad(a, scale_inv_a, b, scale_inv_b, group_ends, d, 
 _GRAD_DTYPES = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}
 
 
+_dtype_of = attrgetter("dtype")
+
+
+def _pack(code, values):
+    """Host array of a C type as bytes (a pointer argument takes them as they are)."""
+    return struct.pack(f"{len(values)}{code}", *values)
+
+
 def _grad_table(tensors, name):
     """Host arrays (pointers, dtypes) of a list of contiguous BF16 / fp32 tensors on the current device."""
     here = torch.cuda.current_device() if tensors[0].is_cuda else None
     if set(map(torch.Tensor.get_device, tensors)) != {here} or not all(map(torch.Tensor.is_contiguous, tensors)):
         for t in tensors:
             _p(t)  # says what is wrong with the first one
-    try:
-        dtypes = array("i", [_GRAD_DTYPES[t.dtype] for t in tensors])
-    except KeyError as e:
-        raise TypeError(f"{name} must be bfloat16 or float32 tensors, got {e.args[0]}") from None
-    return array("Q", map(torch.Tensor.data_ptr, tensors)), dtypes
-
-
-def _at(a):
-    return a.buffer_info()[0]
+    kinds = list(map(_dtype_of, tensors))
+    if not set(kinds) <= _GRAD_DTYPES.keys():
+        raise TypeError(f"{name} must be bfloat16 or float32 tensors")
+    dtypes = [_GRAD_DTYPES[kinds[0]]] * len(kinds) if len(set(kinds)) == 1 else [_GRAD_DTYPES[k] for k in kinds]
+    return _pack("Q", list(map(torch.Tensor.data_ptr, tensors))), _pack("i", dtypes)
 
 
 def fp8_grad_norm_grouped(xs, norm_out, stream=None):
@@ -452,8 +466,8 @@ def fp8_grad_norm_grouped(xs, norm_out, stream=None):
     if not xs:
         raise ValueError("xs must be a non-empty list of tensors")
     ptrs, dtypes = _grad_table(xs, "xs")
-    ns = array("q", map(torch.Tensor.numel, xs))
-    _check(library().fp8_grad_norm_grouped(len(xs), _at(ptrs), _at(ns), _at(dtypes), _f32(norm_out, "norm_out"),
+    ns = list(map(torch.Tensor.numel, xs))
+    _check(library().fp8_grad_norm_grouped(len(xs), ptrs, _pack("q", ns), dtypes, _f32(norm_out, "norm_out"),
                                            _stream(stream)))
 
 
@@ -462,11 +476,10 @@ def fp8_grad_clip_grouped(xs, max_norm, norm_out=None, ys=None, coef_out=None, e
     without ys.  A norm that is NaN or Inf leaves the values as they are."""
     if not xs or (ys is not None and len(ys) != len(xs)):
         raise ValueError("xs must be a non-empty list of tensors, and ys as long as xs")
-    ns = array("q", map(torch.Tensor.numel, xs))
-    if ys is not None and array("q", map(torch.Tensor.numel, ys)) != ns:
+    ns = list(map(torch.Tensor.numel, xs))
+    if ys is not None and list(map(torch.Tensor.numel, ys)) != ns:
         raise ValueError("each y must have as many elements as its x")
     ptrs, dtypes = _grad_table(xs, "xs")
     outs, out_dtypes = _grad_table(ys, "ys") if ys is not None else (None, None)
-    _check(library().fp8_grad_clip_grouped(len(xs), _at(ptrs), _at(ns), _at(dtypes), outs and _at(outs),
-                                           out_dtypes and _at(out_dtypes), max_norm, eps, _f32(norm_out, "norm_out"),
-                                           _f32(coef_out, "coef_out"), _stream(stream)))
+    _check(library().fp8_grad_clip_grouped(len(xs), ptrs, _pack("q", ns), dtypes, outs, out_dtypes, max_norm, eps,
+                                           _f32(norm_out, "norm_out"), _f32(coef_out, "coef_out"), _stream(stream)))
