@@ -136,6 +136,21 @@ struct Waiter {
     }
 };
 
+// A role whose wait gave up says so in `flag` (shared memory) of every CTA of its
+// cluster before the CTAs meet for the last time: copies and products may then
+// still be in flight, and the CTAs stay for another millisecond.
+__device__ __forceinline__ void report_dead(uint32_t flag, int ctas) {
+    for (int r = 0; r < ctas; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(flag, r)), "r"(1) : "memory");
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void linger() {
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    for (uint32_t i = 0; i < (1u << 20) && global_ns() - t0 < 1000000ull; ++i) {
+    }
+}
+
 // One thread of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t yes;

@@ -60,7 +60,7 @@ struct Shared {
     uint64_t full[kStages], empty[kStages], landed[kStages];
     uint64_t tmem_full[2], tmem_empty[2];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
-    uint32_t tmem;
+    uint32_t tmem, dead;
     int groups[2 * kMaxGroups + 3];
 };
 template <bool TILES>
@@ -275,6 +275,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
     const uint32_t rank = cluster_rank();
 
     if (threadIdx.x == 0) {
+        sh.dead = 0;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 2);   // one arrival per CTA of the pair
             mbar_init(&sh.empty[i], 1);  // the products' commit
@@ -567,8 +568,13 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
         }
         __syncwarp();
     }
+    if (w.dead) report_dead(smem_addr(&sh.dead), 2);
     tmem_fence_before();
     cluster_meet();
+    if (sh.dead != 0) {
+        linger();
+        cluster_meet();
+    }
     tmem_fence_after();
     if (warp == 8) tmem_free<2>(tmem, 512);
 }

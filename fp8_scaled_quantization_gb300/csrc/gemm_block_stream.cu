@@ -48,7 +48,7 @@ struct Shared {
     uint64_t tmem_full[4], tmem_empty[4];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint64_t part_full, part_empty;
-    uint32_t tmem;
+    uint32_t tmem, dead;
     int groups[1];  // the group table: as long as the launch asks for
 };
 
@@ -142,6 +142,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
     const int rank = split > 1 ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
+        sh.dead = 0;
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
@@ -398,12 +399,18 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
         }
     }
     __syncwarp();
+    if (w.dead) report_dead(smem_addr(&sh.dead), split);
     tmem_fence_before();
     if (split > 1) {  // no CTA leaves while another reads its partial sums
         if (warp >= S::kScalers) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
         cluster_meet();
     } else {
         __syncthreads();
+    }
+    if (sh.dead != 0) {
+        linger();
+        if (split > 1) cluster_meet();
+        else __syncthreads();
     }
     tmem_fence_after();
     if (warp == kProduct) tmem_free<1>(tmem, S::kColumns);

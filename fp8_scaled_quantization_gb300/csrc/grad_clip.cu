@@ -54,8 +54,12 @@ __device__ __forceinline__ float element(const uint8_t* x, bool f32, int64_t i) 
 // whose squares fell below the fp32 range.
 template <bool SCALED>
 __device__ __forceinline__ float squares(const uint8_t* x, bool f32, bool vec, int64_t lo, int64_t hi, float s, uint32_t* any) {
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     uint32_t bits = 0;
+    const auto fold = [&]() {
+        total = __fadd_rn(total, __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3])));
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+    };
     const auto add = [&](float v, int j) {
         if constexpr (SCALED) v = __fmul_rn(v, s);
         acc[j] = __fmaf_rn(v, v, acc[j]);
@@ -88,14 +92,19 @@ __device__ __forceinline__ float squares(const uint8_t* x, bool f32, bool vec, i
                 add(bf16hi(v[k].w), 3);
             }
         }
+        fold();
     }
-    for (int64_t i = last + threadIdx.x; i < hi; i += kThreads) {
-        const float v = element(x, f32, i);
-        bits |= __float_as_uint(v);
-        add(v, 0);
+    for (int64_t i = last + threadIdx.x; i < hi; i += 4 * kThreads) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float v = i + j * kThreads < hi ? element(x, f32, i + j * kThreads) : 0.0f;
+            bits |= __float_as_uint(v);
+            add(v, j);
+        }
     }
     *any = bits & (f32 ? 0x7FFFFFFFu : 0x7FFF7FFFu);
-    return __fadd_rn(__fadd_rn(acc[0], acc[1]), __fadd_rn(acc[2], acc[3]));
+    fold();
+    return total;
 }
 
 __device__ __forceinline__ double block_sum_f64(double v, double* smem) {
@@ -113,7 +122,9 @@ __device__ __forceinline__ double block_sum_f64(double v, double* smem) {
 
 // Pass 1: one CTA per `reps` chunks, one 64-bit partial per CTA.
 //
-// A thread adds its squares in fp32 (four sums of at most 16 * reps values).
+// A thread adds its squares in fp32: four sums of at most 16 values per chunk,
+// and those of its chunks one after another (unaligned tensors: four sums of 16 *
+// reps values).
 // Squares leave the fp32 range for |x| above 2^63 and below 2^-63: where the
 // thread's sum is not below 2^120, or is below 2^-100 with some x nonzero, it
 // reads its elements again scaled by 2^-96 or 2^96, and the power of two is
@@ -348,10 +359,14 @@ fp8_status_t run(const char* fn, const Tensors& g, bool clip, Clip c, cudaStream
     double* parts = reinterpret_cast<double*>(ws->sat);
     c.parts = parts;
     c.coef = ws->scratch;
-    // every tensor rounds its chunk count up: at most total / reps + count partials
+    // About 16 CTAs per SM once there is work for more of them: the 64-bit block sum at
+    // a CTA's end costs as much as a third of a chunk's reads (4 x 67 MB, one chunk per
+    // CTA: 53 us, 5.1 TB/s).  Every tensor rounds its chunk count up, so that there are
+    // at most total / reps + count partials.
     int64_t total = 0, reps = 1;
     for (int i = 0; i < g.count; ++i) total += chunks_of(g, i, 1);
-    if (total > kMaxPartials) reps = (total + (kMaxPartials - g.count) - 1) / (kMaxPartials - g.count);
+    if (total > 16 * sm_count()) reps = total / (16 * sm_count());
+    if (total / reps + g.count > kMaxPartials) reps = (total + (kMaxPartials - g.count) - 1) / (kMaxPartials - g.count);
     if (reps > 0x7FFFFFFF) return fail(FP8_ERR_UNSUPPORTED, "%s: too many elements", fn);
     int done = 0;
     s = for_tables<N>(fn, g, reps, [&](const Table<N>& t, int chunks) {

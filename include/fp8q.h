@@ -13,9 +13,12 @@
  * Memory.   Every tensor and scalar pointer is a DEVICE pointer owned by the
  *           caller (for example a PyTorch allocation).  The library never
  *           frees caller memory and never synchronises the device or a stream.
- *           The one allocation it makes is a 96 KB reduction workspace per
+ *           The allocations it makes are a 96 KB reduction workspace per
  *           (device, stream) pair, created on the first call that needs it
- *           and kept until process exit (see "Workspace" below).
+ *           and kept until process exit (see "Workspace" below), and, for
+ *           products whose operand rows are not multiples of 16 bytes, a
+ *           scratch copy of those operands per (device, stream) (see
+ *           fp8_gemm_block).
  * Streams.  `stream` is a cudaStream_t passed as void*; NULL means the legacy
  *           default stream.  Every call only enqueues work on that stream and
  *           returns; results are ready when the stream reaches them.
@@ -137,9 +140,9 @@ fp8_status_t fp8_wait_timeouts(unsigned long long* count);
  * synchronises with the device. */
 fp8_status_t fp8_test_drop_tile_copy(int tile);
 
-/* Frees the reduction workspace (96 KB) that the calls made on `stream` on the
- * current device, after waiting for the work queued on that stream.  A later
- * reducing call on the stream allocates a new one.  Returns FP8_OK when there
+/* Frees the reduction workspace (96 KB) and the products' scratch that the calls
+ * made on `stream` on the current device, after waiting for the work queued on
+ * that stream.  A later call on the stream that needs one allocates a new one.  Returns FP8_OK when there
  * is none.  Call it before destroying a stream when many short-lived streams
  * are used, and not while the stream is being captured or while a captured
  * graph whose kernels used that workspace may still be launched (its nodes
@@ -478,9 +481,20 @@ fp8_status_t fp8_block128_scales_to_mx(const float* scale_inv, int64_t rows, int
  *                   sum is the product first, then one addition).
  *   Sizes           m, n, k >= 0, each below 2^31 - 256; k == 0 gives zeros
  *                   (or leaves an accumulated D alone).
+ *   Alignment       operands with 16-byte aligned bases and rows that are
+ *                   multiples of 16 bytes are read in place.  Others are first
+ *                   copied, with their rows 16-byte aligned, into scratch of
+ *                   the stream, which grows to the largest such call (about
+ *                   1.25 times its codes) and is kept for later ones;
+ *                   FP8_ERR_CUDA if it cannot be allocated.  D may start
+ *                   anywhere; whole 16-byte rows are written faster.
  * NaN codes and E5M2 infinities follow fp32 arithmetic (the sign and payload
  * of a NaN are not specified).  Results do not depend on the stream, on other
  * calls or on earlier ones: every sum has a fixed order for given sizes.
+ * Two kernels: CTA pairs over 256 x 256 outputs, or, with few rows of A, CTAs
+ * that stream 128 columns' worth of B and split the contraction over a cluster;
+ * which one is chosen by sizes alone.  Their waits are bounded and counted by
+ * fp8_wait_timeouts.  One launch, plus one per operand that is copied.
  *
  * The forward product of a layer with weight W [out, in] and tokens X [t, in]
  * is (A = X, B = W, FP8_B_NK); the input gradient is (A = dY [t, out], B = W,

@@ -388,3 +388,25 @@ def test_products_are_the_gradients_of_the_forward_product():
         e[i, j] = h
         diff = ((gv2 * (xv2 @ (wv + e).T)).sum() - (gv2 * (xv2 @ (wv - e).T)).sum()) / (2 * h)
         assert abs(dw[i, j].double() - diff) <= bound_w[i, j] + 1e-8 * (gv2.abs().T @ xv2.abs())[i, j] * out
+
+
+def test_no_wait_gave_up():
+    """Every product above ended by itself: no bounded wait reached its limit."""
+    assert fq.wait_timeouts() == 0
+
+
+def test_scratch_of_odd_operands_is_kept_and_released():
+    """Odd rows are copied into the stream's scratch: it grows, serves smaller calls, and can be released."""
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        for m, n, k in [(20, 256, 333), (300, 520, 1001), (20, 256, 333)]:
+            ops = operands(m, n, k, "nk", 0, 0, m + k)
+            d = torch.empty((m, n), device=DEV)
+            call(*ops, d, "nk", 0, 0)
+            R.check(d, *want(*ops, "nk", 0, 0))
+        fq.release_stream_workspace(s)
+        ops = operands(40, 130, 77, "kn", 0, 0, 1)
+        d = torch.empty((40, 130), device=DEV)
+        call(*ops, d, "kn", 0, 0)
+        R.check(d, *want(*ops, "kn", 0, 0))
+        fq.release_stream_workspace(s)
