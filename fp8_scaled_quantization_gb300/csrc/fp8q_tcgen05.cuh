@@ -82,7 +82,9 @@ __device__ __forceinline__ void cluster_arrive_expect_tx(uint32_t bar, uint32_t 
 
 // Waits give up after about two seconds; a thread whose wait did so polls each
 // later barrier once only, so that the kernel always ends (its outputs are then
-// incomplete, which fp8_wait_timeouts reports).
+// incomplete, which fp8_wait_timeouts reports).  It issues no further copy or
+// product and arrives on no barrier that copies report to: such a barrier holds
+// 2^20 - 1 bytes, and no arrivals beyond its count while bytes are in flight.
 struct Waiter {
     bool dead = false;
 

@@ -430,7 +430,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                         if (!is_free) w.wait(free_bar, free_phase);
                         __syncwarp();
                         tmem_fence_after();
-                        if (elect_one()) {
+                        if (elect_one() && !w.dead) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 mma_f8<2>(tmem + buf * kPairN, at + k * kStepKMajor,
@@ -525,7 +525,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                     const int x = (tile.blk0 + b) * kBlk;
                     if (it >= kStages) w.wait(smem_addr(&sh.empty[stage]), phase ^ 1);
                     __syncwarp();
-                    if (elect_one()) {
+                    if (elect_one() && !w.dead) {
                         // a block that needs masking lands on this CTA's own barrier first
                         uint32_t bar = full0 + stage * 8;
                         if (RAGGED_K && is_cut(tile, x, (int)p.k)) bar = smem_addr(&sh.landed[stage]);
@@ -560,7 +560,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                         mask_tile(base + stage * kStageBytes + kTileBytes, tile.k_lo - x, tile.k_hi - x, lane);
                         fence_to_async();
                         __syncwarp();
-                        if (lane == 0) cluster_arrive<true>(full0 + stage * 8);
+                        if (lane == 0 && !w.dead) cluster_arrive<true>(full0 + stage * 8);
                     }
                     if (++stage == kStages) stage = 0;
                 }

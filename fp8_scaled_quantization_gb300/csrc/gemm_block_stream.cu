@@ -331,7 +331,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
                 const int x = (item.blk0 + b) * kBlk;
                 if (it >= S::kStages) w.wait(smem_addr(&sh.empty[stage]), phase ^ 1);
                 __syncwarp();
-                if (elect_one()) {
+                if (elect_one() && !w.dead) {
                     mbar_arrive_expect_tx(&sh.full[stage], S::kStageBytes);
                     const int matrix = B_TILES ? 0 : item.group;
                     if constexpr (B_KN) tma_tile<false>(wt, &map_b, item.col0, x, matrix, bar);
@@ -386,7 +386,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
                 const bool free = next < S::kBufs || Waiter::test(smem_addr(&sh.tmem_empty[next % S::kBufs]), (next / S::kBufs - 1) & 1);
                 const bool filled = Waiter::test(smem_addr(&sh.full[stage]), phase);
                 tmem_fence_after();
-                if (elect_one()) {
+                if (elect_one() && !w.dead) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_f8<1>(tmem + buf * TOKENS, wt + k * (B_KN ? kStepMnMajor : kStepKMajor), xt + k * kStepKMajor, desc,
