@@ -4,25 +4,28 @@
 // The scales change every 128 contraction steps, and they are fp32 numbers, so
 // they cannot ride in the tensor core: each block's product P_b is formed in
 // TMEM from zero (four instructions of 32 steps), and eight warps per CTA read
-// it back and add s * P_b to accumulators in registers (one row per lane, 128
-// columns per thread, packed two-lane fused multiply-adds).  Two TMEM buffers
-// of 256 columns let the next block's product run meanwhile.
+// it back and add s * P_b to accumulators in registers (128 outputs per lane).
+// Two TMEM buffers of 256 columns let the next block's product run meanwhile.
 //
 // Roles per CTA of 384 threads: warps 0-7 scale and add, then store; warp 8 of
-// the pair's first CTA issues the products for both; warp 9 gathers the scales;
-// warp 10 fills the ring of operand tiles by bulk copies; warp 11 zeroes the
-// steps of other groups in blocks that a ragged group's end cuts.
+// the pair's first CTA issues the products for both; warp 9 gathers the scales
+// and says where each tile lies; warp 10 fills the ring of operand tiles by bulk
+// copies; warp 11 zeroes the steps of other groups in blocks that a ragged
+// group's end cuts.
 //
-// What bounds it: the scaling warps.  A block takes the tensor core 512 cycles
-// and the warps about 890 (1 x 128 tiles: 1340): the arithmetic of a scheduler's
-// two warps is 292, and the way of each warp through a block -- the barrier's
-// answer 190 cycles, four reads of TMEM with their arithmetic 100 each, the
-// arrival, the loop -- hides behind the other's in part only.  A third warp per
-// scheduler or reads further ahead do not fit the registers: any spill costs
-// more (a load from local memory takes 300 cycles with shared memory this full).
-// Measured: 8192^3 418 us, 2630 TFLOP/s; 16384 x 18432 x 7168 in one call 1.6
-// ms; products alone, without scaling, would take 266 us.  The SM clock falls
-// from 2070 to about 1850 MHz meanwhile (power).
+// What bounds it, per block of 512 tensor-core cycles.  128 x 128 blocks, 800
+// cycles: the way of a TMEM buffer around.  Sixteen warps read it (the reads run
+// one piece ahead of the arithmetic, whose rate sets their time: 480 cycles), they
+// arrive across the pair, the product is issued, takes its 512, and reports back
+// to both CTAs; two buffers share that way, and TMEM has no room for a third
+// (four of half the width run the tensor core at half its rate: 1000 cycles).
+// 1 x 128 tiles, 1330 cycles: the scaling warps themselves, with two operations
+// per element and 1020 cycles without any wait.  A spill in the loop costs more
+// than any of this gains (a load from local memory takes 300 cycles with shared
+// memory this full).  A tile costs another 2500 cycles, mostly to store it.
+// Measured: 4001 x 7168 x 18432 (rows, n, k) 381 us, 2770 TFLOP/s; 16384 x 18432 x
+// 7168 against [k, n] 1.53 ms, 2830; 4096 x 14336 x 8192 in 1 x 128 tiles 535 to
+// 565 us.  The SM clock falls from 2070 to about 1850 MHz meanwhile (power).
 #include "fp8q_host.h"
 #include "fp8q_tcgen05.cuh"
 #include "gemm_block.cuh"
@@ -34,6 +37,9 @@ constexpr int kThreads = 384;
 constexpr int kPairM = 256, kPairN = 256;  // outputs of a pair
 constexpr int kScaleBlocks = 4;            // blocks of a tile whose scales are gathered together
 constexpr int kScaleSlots = 3;             // such groups in the scale ring
+// The scale warp is at most kScaleSlots groups ahead, so it writes a tile's place
+// over that of a tile that every scaling warp has left.
+constexpr int kPlaces = kScaleSlots + 1;
 constexpr int kRaster = 8;                 // tiles along m that are walked before the next tile along n
 constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kOutBytes = 32 * 128;   // one staging buffer of a warp: 32 rows of 128 bytes
@@ -57,6 +63,8 @@ struct Shared {
             alignas(8) float b[kScaleSlots][kScaleBlocks][kPairN];  // and per block and column
         } tile;
     } sc;
+    int4 place[kPlaces];  // of the tiles under way: first row, end of rows, first column, blocks
+    int matrix[kPlaces];  // and group
     uint64_t full[kStages], empty[kStages], landed[kStages];
     uint64_t tmem_full[2], tmem_empty[2];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
@@ -138,7 +146,30 @@ __device__ __forceinline__ void mask_tile(uint32_t tile, int lo, int hi, int lan
     }
 }
 
-// Which of a warp's 32 x 128 outputs the pair acc[q] of a lane holds: columns
+// A lane's 128 sums.  1 x 128 tiles, with two operations per element, keep them
+// as 64 packed pairs (single numbers: 7% slower).  Else they are single numbers,
+// although a packed operation does two: for packed pairs the compiler finds no
+// registers to read the products one piece ahead, and 3 to 4% are lost.
+template <bool TILES>
+struct Sums {
+    float v[128];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) v[i] = 0.0f;
+    }
+    __device__ __forceinline__ float2 pair(int q) const { return make_float2(v[2 * q], v[2 * q + 1]); }
+};
+template <>
+struct Sums<true> {
+    uint64_t v[64];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) v[i] = 0;
+    }
+    __device__ __forceinline__ float2 pair(int q) const { return unpack2(v[q]); }
+};
+
+// Which of a warp's 32 x 128 outputs the pair q of a lane's sums holds: columns
 // col, col + 1 of row `row`.  TILES: the 16x256b order of TMEM, in which a lane
 // has 4 rows and 32 columns; else lane = row and the 128 columns in order.
 template <bool TILES>
@@ -150,112 +181,130 @@ __device__ __forceinline__ int col_of(int q, int lane) {
     return TILES ? (q >> 5) * 64 + (q >> 1 & 7) * 8 + 2 * (lane & 3) : 2 * q;
 }
 
-// A warp's 32 x 128 outputs from (row0, c0) on, by plain stores (and, when
-// accumulating, loads): rows that a group's end cuts, unaligned outputs.
+// 128 bytes of each of a warp's rows, piece `part`, to shared memory.
 template <bool TILES>
-__device__ __forceinline__ void store_direct(const GemmProblem& p, const uint64_t (&acc)[64], int lane, int64_t base,
-                                             int64_t row0, int64_t row_end, int64_t c0) {
-    const bool pairs = (p.n & 1) == 0 && (reinterpret_cast<uintptr_t>(p.d) & (p.out_f32 ? 7u : 3u)) == 0;
+__device__ __forceinline__ void stage_out(bool f32, const Sums<TILES>& acc, int part, uint32_t stage, int lane) {
+    if constexpr (TILES) {
+        if (f32) {
 #pragma unroll
-    for (int q = 0; q < 64; ++q) {
-        const int64_t r = row0 + row_of<TILES>(q, lane), c = c0 + col_of<TILES>(q, lane);
-        if (r >= row_end || c >= p.n) continue;
-        const int64_t at = base + r * p.n + c;
-        float2 v = unpack2(acc[q]);
-        if (p.out_f32) {
-            float* d = static_cast<float*>(p.d) + at;
-            if (pairs) {
-                if (p.accumulate) {
-                    const float2 old = *reinterpret_cast<const float2*>(d);
-                    v = make_float2(__fadd_rn(old.x, v.x), __fadd_rn(old.y, v.y));
-                }
-                *reinterpret_cast<float2*>(d) = v;
-            } else {
-                d[0] = p.accumulate ? __fadd_rn(d[0], v.x) : v.x;
-                if (c + 1 < p.n) d[1] = p.accumulate ? __fadd_rn(d[1], v.y) : v.y;
+            for (int i = 0; i < 16; ++i) {  // 4 column blocks of 8, 4 rows
+                const int q = (part >> 1) * 32 + (i >> 1 & 1) * 16 + ((part & 1) * 4 + (i >> 2)) * 2 + (i & 1);
+                const int r = row_of<true>(q, lane), at = (col_of<true>(q, lane) & 31) * 4;
+                const float2 v = acc.pair(q);
+                asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stage + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15)),
+                             "f"(v.x), "f"(v.y)
+                             : "memory");
             }
         } else {
-            uint16_t* d = static_cast<uint16_t*>(p.d) + at;
-            const uint32_t o = f32x2_to_bf16x2(v.x, v.y);
-            if (pairs) {
-                *reinterpret_cast<uint32_t*>(d) = o;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {  // 8 column blocks of 8, 4 rows
+                const int q = (part & 1) * 32 + i;
+                const int r = row_of<true>(q, lane), at = (col_of<true>(q, lane) & 63) * 2;
+                const float2 v = acc.pair(q);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15)),
+                             "r"(f32x2_to_bf16x2(v.x, v.y))
+                             : "memory");
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t o[4];
+            if (f32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 v = acc.pair(part * 16 + 2 * j + i);
+                    o[2 * i] = __float_as_uint(v.x);
+                    o[2 * i + 1] = __float_as_uint(v.y);
+                }
             } else {
-                d[0] = (uint16_t)o;
-                if (c + 1 < p.n) d[1] = (uint16_t)(o >> 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = acc.pair((part & 1) * 32 + 4 * j + i);
+                    o[i] = f32x2_to_bf16x2(v.x, v.y);
+                }
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((j ^ (lane & 7)) << 4)), "r"(o[0]),
+                         "r"(o[1]), "r"(o[2]), "r"(o[3])
+                         : "memory");
+        }
+    }
+}
+
+// Such a piece (outputs from column x on) from shared memory to D by plain stores
+// and, when accumulating, loads: a row per step.
+__device__ __forceinline__ void copy_out(const GemmProblem& p, uint32_t stage, int lane, int64_t base, int64_t row0,
+                                         int64_t row_end, int64_t x) {
+    const int rows = (int)(row_end - row0 < 32 ? row_end - row0 : 32), mine = p.out_f32 ? 1 : 2;
+    const int64_t c = x + lane * mine;
+    if (c >= p.n) return;
+    const bool both = c + 1 < p.n, pair = (p.n & 1) == 0 && (reinterpret_cast<uintptr_t>(p.d) & 3u) == 0;
+    uint8_t* d = static_cast<uint8_t*>(p.d) + (base + row0 * p.n + c) * (p.out_f32 ? 4 : 2);
+    const int64_t pitch = p.n * (p.out_f32 ? 4 : 2);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8, d += 8 * pitch) {
+        const int to = min(rows - r0, 8);
+        float old[8];
+        if (p.accumulate) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) old[r] = r < to ? *reinterpret_cast<const float*>(d + r * pitch) : 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            if (r >= to) break;
+            uint32_t v;
+            asm volatile("ld.shared.u32 %0, [%1];"
+                         : "=r"(v)
+                         : "r"(stage + (r0 + r) * 128 + (((lane >> 2) ^ r) << 4) + (lane & 3) * 4)
+                         : "memory");
+            if (p.out_f32) {
+                const float f = __uint_as_float(v);
+                *reinterpret_cast<float*>(d + r * pitch) = p.accumulate ? __fadd_rn(old[r], f) : f;
+            } else if (pair) {
+                *reinterpret_cast<uint32_t*>(d + r * pitch) = v;
+            } else {
+                uint16_t* const h = reinterpret_cast<uint16_t*>(d + r * pitch);
+                h[0] = (uint16_t)v;
+                if (both) h[1] = (uint16_t)(v >> 16);
             }
         }
     }
 }
 
-// The same for a warp whose 32 rows are all in the group: staged in shared
-// memory 128 bytes of each row at a time (16-byte pieces swizzled, so that the
-// stores spread over the banks) and written by the bulk-copy engine, which
-// drops what lies outside D.
+// A warp's 32 x 128 outputs from (row0, c0) on: 128 bytes of each row at a time
+// go through shared memory (16-byte pieces swizzled, so that the accesses spread
+// over the banks).  Where all 32 rows are in the group the bulk-copy engine
+// writes them and drops what lies outside D; rows that a group's end cuts,
+// unaligned outputs and sums onto D take plain stores.
 template <bool TILES>
-__device__ __forceinline__ void store_bulk(const GemmProblem& p, const CUtensorMap* map, const uint64_t (&acc)[64],
-                                           uint32_t stages, int lane, int64_t row0, int64_t c0, int z) {
+__device__ __forceinline__ void store_tile(const GemmProblem& p, const CUtensorMap* map, bool bulk, const Sums<TILES>& acc,
+                                           uint32_t stages, int lane, int64_t row0, int64_t row_end, int64_t c0, int matrix) {
+    constexpr int kOuts = Ring<TILES>::kOuts;
 #pragma unroll
     for (int part = 0; part < 4; ++part) {
-        const uint32_t stage = stages + part % Ring<TILES>::kOuts * kOutBytes;
+        const uint32_t stage = stages + part % kOuts * kOutBytes;
         if (part >= 2 && !p.out_f32) break;
         const int64_t x = c0 + part * (p.out_f32 ? 32 : 64);
-        if (x >= p.n) break;
-        if (lane == 0)  // this buffer has been read
-            asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(Ring<TILES>::kOuts - 1) : "memory");
-        __syncwarp();
-        if constexpr (TILES) {
-            if (p.out_f32) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {  // 4 column blocks of 8, 4 rows
-                    const int q = (part >> 1) * 32 + (i >> 1 & 1) * 16 + ((part & 1) * 4 + (i >> 2)) * 2 + (i & 1);
-                    const int r = row_of<true>(q, lane), at = (col_of<true>(q, lane) & 31) * 4;
-                    asm volatile("st.shared.b64 [%0], %1;" ::"r"(stage + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15)),
-                                 "l"(acc[q])
+        if (x < p.n) {
+            if (lane == 0)  // this buffer has been read: every piece commits a group, if an empty one
+                asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOuts - 1) : "memory");
+            __syncwarp();
+            stage_out<TILES>(p.out_f32, acc, part, stage, lane);
+            if (bulk && row0 + 31 < row_end) {
+                fence_to_async();
+                __syncwarp();
+                if (lane == 0)
+                    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                                     reinterpret_cast<uint64_t>(map)),
+                                 "r"((int)x), "r"((int)row0), "r"(matrix), "r"(stage)
                                  : "memory");
-                }
             } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {  // 8 column blocks of 8, 4 rows
-                    const int q = (part & 1) * 32 + i;
-                    const int r = row_of<true>(q, lane), at = (col_of<true>(q, lane) & 63) * 2;
-                    const float2 v = unpack2(acc[q]);
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15)),
-                                 "r"(f32x2_to_bf16x2(v.x, v.y))
-                                 : "memory");
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t o[4];
-                if (p.out_f32) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 a = unpack2(acc[part * 16 + 2 * j + i]);
-                        o[2 * i] = __float_as_uint(a.x);
-                        o[2 * i + 1] = __float_as_uint(a.y);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 a = unpack2(acc[(part & 1) * 32 + 4 * j + i]);
-                        o[i] = f32x2_to_bf16x2(a.x, a.y);
-                    }
-                }
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((j ^ (lane & 7)) << 4)),
-                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                             : "memory");
+                __syncwarp();
+                copy_out(p, stage, lane, (int64_t)matrix * p.m * p.n, row0, row_end, x);
+                __syncwarp();
             }
         }
-        fence_to_async();
-        __syncwarp();
-        if (lane == 0) {
-            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                             reinterpret_cast<uint64_t>(map)),
-                         "r"((int)x), "r"((int)row0), "r"(z), "r"(stage)
-                         : "memory");
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
 }
 
@@ -313,12 +362,10 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
         const int half = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
         const uint32_t full0 = smem_addr(&sh.tmem_full[0]), empty0 = cluster_addr(smem_addr(&sh.tmem_empty[0]), 0);
-        uint32_t it = 0, group = 0;  // blocks and scale groups so far
+        uint32_t it = 0, group = 0, at_place = 0;  // blocks and scale groups so far; this tile's place
         for (int t = first; t < total; t += step) {
-            const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
-            uint64_t acc[64];
-#pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0;
+            Sums<B_TILES> acc;
+            acc.clear();
             float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s4_next = s4;
             uint32_t slot = 0;
             // the next group of scales is there; 128 x 128 blocks: this row's four live in registers from here on
@@ -337,15 +384,15 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.sc_empty[slot]);
             };
-            if (!B_TILES && tile.blks > 0) fetch();
+            fetch();
+            const int blks = sh.place[at_place].w;
+            if (B_TILES && blks == 0) release();
             bool ready = false;  // (asking one block ahead pays with 1 x 128 tiles only)
-            for (int b = 0; b < tile.blks; ++b) {
+            for (int b = 0; b < blks; ++b) {
                 const uint32_t buf = it & 1, from = lanes + buf * kPairN;
                 const int sub = b % kScaleBlocks;
-                if (B_TILES && sub == 0) fetch();
-                if (!B_TILES) {
-                    s4 = sub == 0 ? s4_next : make_float4(s4.y, s4.z, s4.w, 0.0f);
-                }
+                if (B_TILES && b > 0 && sub == 0) fetch();
+                if (!B_TILES) s4 = sub == 0 ? s4_next : make_float4(s4.y, s4.z, s4.w, 0.0f);
                 if (!B_TILES || !ready) w.wait(full0 + buf * 8, (it >> 1) & 1);
                 __syncwarp();  // lanes may have left the wait apart
                 tmem_fence_after();
@@ -354,9 +401,8 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) cluster_arrive<false>(empty0 + buf * 8);
-                    if (B_TILES) ready = b + 1 < tile.blks && Waiter::test(full0 + (it & 1) * 8, (it >> 1) & 1);
+                    if (B_TILES) ready = Waiter::test(full0 + (it & 1) * 8, (it >> 1) & 1);
                 };
-                uint32_t v[32];
                 if constexpr (B_TILES) {
                     uint64_t sr[4];  // this lane's four rows
 #pragma unroll
@@ -375,39 +421,41 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                         }
 #pragma unroll
                         for (int rh = 0; rh < 2; ++rh) {
+                            uint32_t v[32];
                             tmem_ld_16x64(from + ((uint32_t)(rh * 16) << 16) + h * 64, v);
                             tmem_wait_ld();
                             if (h + rh == 2) read();
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                uint64_t* const at = acc + h * 32 + rh * 16 + i * 2;
+                                uint64_t* const at = acc.v + h * 32 + rh * 16 + i * 2;
                                 at[0] = fma2(mul2(pack2(v[4 * i], v[4 * i + 1]), sc[i]), sr[rh * 2], at[0]);
                                 at[1] = fma2(mul2(pack2(v[4 * i + 2], v[4 * i + 3]), sc[i]), sr[rh * 2 + 1], at[1]);
                             }
                         }
                     }
-                    if (sub == kScaleBlocks - 1 || b == tile.blks - 1) release();
+                    if (sub == kScaleBlocks - 1 || b == blks - 1) release();
                 } else {
-                    const uint64_t s2 = pack2(s4.x, s4.x);
+                    uint32_t v[2][16];
+                    tmem_ld_32x16(from, v[0]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld_32x32(from + c * 32, v);
+                    for (int c = 0; c < 8; ++c) {  // reads run one piece ahead
                         tmem_wait_ld();
-                        if (c == 3) read();
+                        if (c < 7) tmem_ld_32x16(from + (c + 1) * 16, v[(c + 1) & 1]);
+                        else read();
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            acc[c * 16 + j] = fma2(pack2(v[2 * j], v[2 * j + 1]), s2, acc[c * 16 + j]);
-                        if (c == 1 && sub == 2 && b + 2 < tile.blks) fetch();
+                            acc.v[c * 16 + j] = __fmaf_rn(__uint_as_float(v[c & 1][j]), s4.x, acc.v[c * 16 + j]);
+                        if (c == 1 && sub == 2 && b + 2 < blks) fetch();
                     }
                 }
             }
             // store: this warp's 32 rows, 128 columns
-            const int64_t r0 = tile.row0 + (int)rank * 128 + (warp & 3) * 32, c0 = tile.col0 + half * 128;
-            if (bulk_store && r0 + 31 < tile.row_end) {
-                store_bulk<B_TILES>(p, &map_d, acc, smem_addr(out) + warp * kOuts * kOutBytes, lane, r0, c0, RAGGED_K ? tile.group : 0);
-            } else {
-                store_direct<B_TILES>(p, acc, lane, RAGGED_K ? (int64_t)tile.group * p.m * p.n : 0, r0, tile.row_end, c0);
-            }
+            const int4 place = sh.place[at_place];
+            const int matrix = RAGGED_K ? sh.matrix[at_place] : 0;
+            at_place = (at_place + 1) % kPlaces;
+            const int64_t r0 = place.x + (int)rank * 128 + (warp & 3) * 32, c0 = place.z + half * 128;
+            store_tile<B_TILES>(p, &map_d, bulk_store, acc, smem_addr(out) + warp * kOuts * kOutBytes, lane, r0, place.y, c0,
+                                matrix);
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
@@ -421,20 +469,20 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                 uint32_t it = 0, stage = 0, phase = 0;
                 for (int t = first; t < total; t += step) {
                     const int blks = locate<RAGGED_K>(p, groups, count, tiles_n, t).blks;
-                    for (int b = 0; b < blks; ++b, ++it) {
-                        const uint32_t buf = it & 1, free_bar = smem_addr(&sh.tmem_empty[buf]), free_phase = ((it >> 1) & 1) ^ 1;
+                    for (int b = 0; b < blks; ++b) {
                         const uint64_t at = a0 + stage * (kStageBytes >> 4), bt = b0 + stage * (kStageBytes >> 4);
-                        const bool is_free = it < 2 || Waiter::test(free_bar, free_phase);
+                        const uint32_t buf = it & 1;
                         // (tiles that were masked with plain stores are released to the cluster)
                         w.template wait<RAGGED_K>(smem_addr(&sh.full[stage]), phase);
-                        if (!is_free) w.wait(free_bar, free_phase);
+                        if (it >= 2) w.wait(smem_addr(&sh.tmem_empty[buf]), ((it >> 1) & 1) ^ 1);
+                        ++it;
                         __syncwarp();
                         tmem_fence_after();
                         if (elect_one() && !w.dead) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_f8<2>(tmem + buf * kPairN, at + k * kStepKMajor,
-                                          bt + k * (B_KN ? kStepMnMajor : kStepKMajor), desc, k > 0);
+                                mma_f8<2>(tmem + buf * kPairN, at + k * kStepKMajor, bt + k * (B_KN ? kStepMnMajor : kStepKMajor),
+                                          desc, k > 0);
                             mma_commit<2>(smem_addr(&sh.tmem_full[buf]));
                             mma_commit<2>(smem_addr(&sh.empty[stage]));
                         }
@@ -451,12 +499,12 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             const int64_t kb = blocks_of(p.k), nb = blocks_of(p.n);
             const bool wide_a = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sa) & 15u) == 0;
             const bool wide_b = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sb) & 15u) == 0;
-            uint32_t group = 0;
+            uint32_t group = 0, at_place = 0;
             for (int t = first; t < total; t += step) {
                 const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
-                for (int done = 0; done < tile.blks; done += kScaleBlocks, ++group) {
+                for (int done = 0; done == 0 || done < tile.blks; done += kScaleBlocks, ++group) {  // (once without blocks, too)
                     const int g0 = tile.blk0 + done, to = min(tile.blks - done, kScaleBlocks);
-                    const bool whole = g0 % kScaleBlocks == 0;  // an aligned piece of a row of scales
+                    const bool whole = to > 0 && g0 % kScaleBlocks == 0;  // an aligned piece of a row of scales
                     const uint32_t slot = group % kScaleSlots;
                     float4 a[4];
 #pragma unroll
@@ -509,9 +557,14 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                                                                                  __fmul_rn(a[i].z, c2), __fmul_rn(a[i].w, c3));
                         }
                     }
+                    if (done == 0 && lane == 0) {
+                        sh.place[at_place] = make_int4(tile.row0, tile.row_end, tile.col0, tile.blks);
+                        sh.matrix[at_place] = tile.group;
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.sc_full[slot]);
                 }
+                at_place = (at_place + 1) % kPlaces;
             }
         } else if (warp == 10) {
             // ---- operand tiles: A rows [row0 + 128 rank, ..), B columns [col0 + 128 rank, ..)
