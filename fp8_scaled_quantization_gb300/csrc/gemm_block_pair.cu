@@ -118,31 +118,33 @@ __device__ __forceinline__ bool is_cut(const Tile& t, int x, int k) {
 
 // Zeroes the bytes outside [lo, hi) of every row of a K-major tile, by one warp.
 __device__ __forceinline__ void mask_tile(uint32_t tile, int lo, int hi, int lane) {
-    const int piece = lane & 7, from = max(lo - piece * 16, 0), to = min(hi - piece * 16, 16);
-    if (from <= 0 && to >= 16) return;
-    uint32_t keep[4];
+#pragma unroll 1
+    for (int piece = 0; piece < 8; ++piece) {
+        const int from = max(lo - piece * 16, 0), to = min(hi - piece * 16, 16);
+        if (from <= 0 && to >= 16) continue;
+        uint32_t keep[4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        keep[w] = 0;
+        for (int w = 0; w < 4; ++w) {
+            keep[w] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * w + i >= from && 4 * w + i < to) keep[w] |= 0xFFu << (8 * i);
+        }
+        const bool some = (keep[0] | keep[1] | keep[2] | keep[3]) != 0;
+        const uint32_t at = tile + lane * 128 + ((piece ^ (lane & 7)) << 4);
+        uint32_t v[4][4] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // rows lane + 32 i
+            if (some)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
+                             : "r"(at + i * 32 * 128)
+                             : "memory");
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (4 * w + i >= from && 4 * w + i < to) keep[w] |= 0xFFu << (8 * i);
-    }
-    const bool some = (keep[0] | keep[1] | keep[2] | keep[3]) != 0;
-#pragma unroll 4
-    for (int r = lane >> 3; r < 128; r += 4) {
-        const uint32_t at = tile + r * 128 + ((piece ^ (r & 7)) << 4);
-        uint32_t v[4] = {0u, 0u, 0u, 0u};
-        if (some) {
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(at)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + i * 32 * 128), "r"(v[i][0] & keep[0]),
+                         "r"(v[i][1] & keep[1]), "r"(v[i][2] & keep[2]), "r"(v[i][3] & keep[3])
                          : "memory");
-#pragma unroll
-            for (int w = 0; w < 4; ++w) v[w] &= keep[w];
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                     : "memory");
     }
 }
 
