@@ -116,34 +116,40 @@ __device__ __forceinline__ bool is_cut(const Tile& t, int x, int k) {
     return x < t.k_lo || (x + kBlk > t.k_hi && t.k_hi < k);
 }
 
-// Zeroes the bytes outside [lo, hi) of every row of a K-major tile, by one warp.
-__device__ __forceinline__ void mask_tile(uint32_t tile, int lo, int hi, int lane) {
+// Zeroes the bytes outside [lo, hi) of every row of the stage's two K-major tiles,
+// by one warp: a 16-byte column of all rows at a time, and only a column that lo or
+// hi divides is read (4 rows of each tile per lane at once, for one latency).
+__device__ __forceinline__ void mask_stage(uint32_t stage, int lo, int hi, int lane) {
 #pragma unroll 1
     for (int piece = 0; piece < 8; ++piece) {
         const int from = max(lo - piece * 16, 0), to = min(hi - piece * 16, 16);
         if (from <= 0 && to >= 16) continue;
-        uint32_t keep[4];
+        const uint32_t at = stage + lane * 128 + ((piece ^ (lane & 7)) << 4);
+        uint32_t v[8][4] = {};
+        if (from < to) {
+            uint32_t keep[4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            keep[w] = 0;
+            for (int w = 0; w < 4; ++w) {
+                keep[w] = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (4 * w + i >= from && 4 * w + i < to) keep[w] |= 0xFFu << (8 * i);
-        }
-        const bool some = (keep[0] | keep[1] | keep[2] | keep[3]) != 0;
-        const uint32_t at = tile + lane * 128 + ((piece ^ (lane & 7)) << 4);
-        uint32_t v[4][4] = {};
+                for (int i = 0; i < 4; ++i)
+                    if (4 * w + i >= from && 4 * w + i < to) keep[w] |= 0xFFu << (8 * i);
+            }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // rows lane + 32 i
-            if (some)
+            for (int i = 0; i < 8; ++i)
                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
                              : "r"(at + i * 32 * 128)
                              : "memory");
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + i * 32 * 128), "r"(v[i][0] & keep[0]),
-                         "r"(v[i][1] & keep[1]), "r"(v[i][2] & keep[2]), "r"(v[i][3] & keep[3])
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v[i][w] &= keep[w];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + i * 32 * 128), "r"(v[i][0]), "r"(v[i][1]),
+                         "r"(v[i][2]), "r"(v[i][3])
                          : "memory");
     }
 }
@@ -611,8 +617,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                         w.wait(smem_addr(&sh.landed[stage]), phases >> stage & 1);
                         phases ^= 1u << stage;
                         __syncwarp();
-                        mask_tile(base + stage * kStageBytes, tile.k_lo - x, tile.k_hi - x, lane);
-                        mask_tile(base + stage * kStageBytes + kTileBytes, tile.k_lo - x, tile.k_hi - x, lane);
+                        mask_stage(base + stage * kStageBytes, tile.k_lo - x, tile.k_hi - x, lane);
                         fence_to_async();
                         __syncwarp();
                         if (lane == 0 && !w.dead) cluster_arrive<true>(full0 + stage * 8);
