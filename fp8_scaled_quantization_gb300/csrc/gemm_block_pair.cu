@@ -45,17 +45,11 @@ constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kOutBytes = 32 * 128;   // one staging buffer of a warp: 32 rows of 128 bytes
 
 // Operand ring (A and B tile, 32 KB per CTA and stage) and staging buffers per
-// warp.  With 128 x 128 blocks two buffers gain 2% and the fifth stage nothing;
-// with ragged contractions, whose cut blocks stay longer in the ring, the fifth
-// stage is worth 4%.
-template <bool TILES>
-struct Ring {
-    static constexpr int kStages = TILES ? 5 : 4, kOuts = TILES ? 1 : 2;
-};
+// warp: the second buffer gains 2%, a fifth stage in its place nothing.
+constexpr int kStages = 4, kOuts = 2;
 
 template <bool TILES>
 struct Shared {
-    static constexpr int kStages = Ring<TILES>::kStages;
     union {
         float4 rows[kScaleSlots][2][128];  // 128 x 128 blocks: per column half and row, row scale x column block scale
         struct {
@@ -74,7 +68,7 @@ struct Shared {
 template <bool TILES>
 constexpr size_t smem_bytes() {
     constexpr size_t bytes =
-        1024 + (size_t)Ring<TILES>::kStages * kStageBytes + 8 * Ring<TILES>::kOuts * kOutBytes + sizeof(Shared<TILES>);
+        1024 + (size_t)kStages * kStageBytes + 8 * kOuts * kOutBytes + sizeof(Shared<TILES>);
     static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
     return bytes;
 }
@@ -287,7 +281,6 @@ __device__ __forceinline__ void copy_out(const GemmProblem& p, uint32_t stage, i
 template <bool TILES>
 __device__ __forceinline__ void store_tile(const GemmProblem& p, const CUtensorMap* map, bool bulk, const Sums<TILES>& acc,
                                            uint32_t stages, int lane, int64_t row0, int64_t row_end, int64_t c0, int matrix) {
-    constexpr int kOuts = Ring<TILES>::kOuts;
 #pragma unroll
     for (int part = 0; part < 4; ++part) {
         const uint32_t stage = stages + part % kOuts * kOutBytes;
@@ -323,7 +316,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ CUtensorMap map_a,
                  const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d, bool bulk_store) {
     constexpr bool RAGGED_K = FORM == 2, B_KN = FORM == 1, B_TILES = FORM == 2;
-    constexpr int kStages = Ring<B_TILES>::kStages, kOuts = Ring<B_TILES>::kOuts;
     extern __shared__ uint8_t raw[];
     uint8_t* const tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* const out = tiles + kStages * kStageBytes;
