@@ -63,6 +63,9 @@ void* stream_scratch(cudaStream_t stream, size_t bytes, fp8_status_t* st);
 // Let `kernel` use `smem` bytes of dynamic shared memory on the current device
 // (asked of the runtime once per kernel, device and size).
 fp8_status_t allow_smem(const char* what, const void* kernel, size_t smem);
+// How many clusters of `cluster` CTAs of this shape the device holds at one time;
+// 0: it does not say.
+int max_clusters(const void* kernel, int threads, size_t smem, int cluster);
 
 // Launch `kernel` on `st` with `smem` bytes of dynamic shared memory and
 // programmatic stream serialization allowed (the kernel starts with

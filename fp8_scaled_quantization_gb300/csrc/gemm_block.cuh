@@ -54,6 +54,13 @@ fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st
 // gemm_block_stream.cu: 128 columns of D per CTA and `tokens` (16, 32, 64 or 128)
 // rows at a time, k > 0; the contraction is not ragged.
 fp8_status_t run_gemm_stream(const char* fn, const GemmProblem& p, int tokens, cudaStream_t st);
+// How it does so: items of `tokens` rows and 128 columns (with ragged rows, at
+// most), CTAs that share an item's contraction, and clusters of them at one time.
+struct StreamPlan {
+    int64_t items;
+    int split, clusters;
+};
+StreamPlan stream_plan(const GemmProblem& p, int tokens);
 
 // The first `to` of four scales; one 16-byte load where they are aligned to it
 // (and the row holds all four).

@@ -12,6 +12,8 @@
 // Roles per CTA: four warps (eight from 32 tokens on, each pair of them sharing
 // the tokens of 32 columns) scale, add, join and store; then one warp fills the
 // ring of operand tiles and gathers the scales, and one issues the products.
+#include <atomic>
+
 #include "fp8q_host.h"
 #include "fp8q_tcgen05.cuh"
 #include "gemm_block.cuh"
@@ -416,20 +418,45 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
     if (warp == kProduct) tmem_free<1>(tmem, S::kColumns);
 }
 
+// How many clusters of `split` CTAs run at one time, one CTA per SM: a cluster
+// lies within one group of SMs, so that these are fewer than the SMs divided (of
+// 152: 23 clusters of 6, 15 of 8).  A grid beyond them runs in two turns: 96 x 2048
+// x 7168 in 48 clusters of 6 on two CTAs per SM takes 17 us, in 32 of 3 11.
+// Asked once, of the kernel of which one CTA fits an SM (of one that allocates
+// TMEM the runtime counts no second CTA, although it runs).
+int clusters_per_turn(int split) {
+    static std::atomic<int> known[kMostSplit + 1];
+    int n = known[split].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    using S = Shape<128, false>;
+    const int most = sm_count() / split;
+    n = max_clusters(reinterpret_cast<const void*>(gemm_stream_kernel<0, 128>), S::kThreads, smem_bytes<128, false>(1), split);
+    n = n <= 0 || n > most ? most : n;
+    known[split].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <int TOKENS>
+StreamPlan plan(const GemmProblem& p) {
+    const int ctas = p.b_tiles ? Shape<TOKENS, true>::kCtas : Shape<TOKENS, false>::kCtas;  // per SM
+    const int64_t tiles_n = (p.n + kRows - 1) / kRows, tiles_m = (p.m + TOKENS - 1) / TOKENS, kb = blocks_of(p.k);
+    const int64_t busy = p.groups < p.m ? p.groups : p.m;  // groups with rows, at most
+    StreamPlan r = {(tiles_m + busy - 1) * tiles_n, 1, ctas * sm_count()};
+    // shares of the contraction: as many as run at one time, each at least two blocks long
+    for (int split = 2; split <= kMostSplit && kb >= 2 * split; ++split) {
+        const int clusters = ctas * clusters_per_turn(split);
+        if (r.items <= clusters) r = {r.items, split, clusters};
+    }
+    return r;
+}
+
 template <int TOKENS>
 fp8_status_t run(const char* fn, const GemmProblem& p, const CUtensorMap& a, const CUtensorMap& b, cudaStream_t st) {
-    const int64_t tiles_n = (p.n + kRows - 1) / kRows, tiles_m = (p.m + TOKENS - 1) / TOKENS;
-    const int64_t busy = p.groups < p.m ? p.groups : p.m;  // groups with rows, at most
-    const int ctas = p.b_tiles ? Shape<TOKENS, true>::kCtas : Shape<TOKENS, false>::kCtas;  // per SM
-    const int64_t items = (tiles_m + busy - 1) * tiles_n, slots = (int64_t)sm_count() * ctas;
-    // shares of the contraction: as many as fill the SMs, each at least two blocks long
-    const int64_t kb = blocks_of(p.k);
-    int split = 1;
-    while (split < kMostSplit && items * (split + 1) <= slots && kb >= 2 * (split + 1)) ++split;
-    const int64_t most = slots / split, clusters = items + 1 < most ? items + 1 : most;
+    const StreamPlan how = plan<TOKENS>(p);
+    const int64_t clusters = how.items + 1 < how.clusters ? how.items + 1 : how.clusters;
     const auto go = [&](auto kernel, size_t smem) {
-        return launch_cluster(fn, kernel, dim3((unsigned)(clusters * split)), dim3(Shape<TOKENS, false>::kThreads), smem, split, st,
-                              p, a, b, split);
+        return launch_cluster(fn, kernel, dim3((unsigned)(clusters * how.split)), dim3(Shape<TOKENS, false>::kThreads), smem,
+                              how.split, st, p, a, b, how.split);
     };
     return p.b_tiles ? go(gemm_stream_kernel<2, TOKENS>, smem_bytes<TOKENS, true>(p.groups))
            : p.b_kn  ? go(gemm_stream_kernel<1, TOKENS>, smem_bytes<TOKENS, false>(p.groups))
@@ -437,6 +464,15 @@ fp8_status_t run(const char* fn, const GemmProblem& p, const CUtensorMap& a, con
 }
 
 }  // namespace
+
+StreamPlan stream_plan(const GemmProblem& p, int tokens) {
+    switch (tokens) {
+        case 16: return plan<16>(p);
+        case 32: return plan<32>(p);
+        case 64: return plan<64>(p);
+        default: return plan<128>(p);
+    }
+}
 
 fp8_status_t run_gemm_stream(const char* fn, const GemmProblem& p, int tokens, cudaStream_t st) {
     const Operand oa = {p.a, p.k, p.m, 1, tokens}, ob = {p.b, p.b_kn ? p.n : p.k, p.b_kn ? p.k : p.n, p.groups, 128};

@@ -63,6 +63,25 @@ fp8_status_t allow_smem(const char* what, const void* kernel, size_t smem) {
     return FP8_OK;
 }
 
+int max_clusters(const void* kernel, int threads, size_t smem, int cluster) {
+    if (smem > 48 * 1024 && allow_smem("max_clusters", kernel, smem) != FP8_OK) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cluster);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
+    (void)cudaGetLastError();
+    return 0;
+}
+
 int sm_count() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
