@@ -156,7 +156,7 @@ Choice choose(const GemmProblem& p) {
     constexpr double kBlock[2][4] = {{0.40, 0.39, 0.66, 0.53}, {0.45, 0.47, 0.40, 0.57}}, kJoin[4] = {1.0, 1.8, 2.2, 4.0};
     for (int i = 0; i < 4; ++i) {
         const int tokens = 16 << i;
-        const StreamPlan plan = stream_plan(p, tokens);
+        const StreamPlan plan = stream_plan(p, tokens, (int)sms);
         const double items = tiles(tokens) * (double)((p.n + 127) / 128);
         const double compute = ceil(items / plan.clusters) * ceil((double)kb / plan.split) * kBlock[p.b_tiles][i];
         const double us = 5.0 + (plan.split > 1 ? kJoin[i] : 0.0) + most(compute, memory);

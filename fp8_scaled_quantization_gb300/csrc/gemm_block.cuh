@@ -60,7 +60,7 @@ struct StreamPlan {
     int64_t items;
     int split, clusters;
 };
-StreamPlan stream_plan(const GemmProblem& p, int tokens);
+StreamPlan stream_plan(const GemmProblem& p, int tokens, int sms);
 
 // The first `to` of four scales; one 16-byte load where they are aligned to it
 // (and the row holds all four).

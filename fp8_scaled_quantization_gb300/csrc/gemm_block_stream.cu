@@ -32,8 +32,8 @@ template <int TOKENS, bool TILES>
 struct Shape {
     static constexpr int kCtas = TOKENS <= 32 || (TOKENS == 64 && !TILES) ? 2 : 1;
     static constexpr int kStages = TOKENS == 16 ? 5 - TILES : TOKENS == 32 ? 4 - TILES : TOKENS == 64 && !TILES ? 3 : 4;
-    static constexpr int kBufs = TOKENS <= 64 ? 4 : 2;        // TMEM buffers
-    static constexpr uint32_t kColumns = TOKENS * kBufs;      // a power of two, 64 .. 256
+    static constexpr int kBufs = 4;                           // TMEM buffers (128 tokens with two: 2% slower)
+    static constexpr uint32_t kColumns = TOKENS * kBufs;      // a power of two, 64 .. 512
     static constexpr uint32_t kStageBytes = kTileBytes + TOKENS * 128;
     static constexpr int kScalers = TOKENS == 16 ? 4 : 8;     // warps
     static constexpr int kMine = TOKENS * 4 / kScalers;       // tokens per scaling warp: 16, 16, 32, 64
@@ -47,7 +47,7 @@ struct Shared {
     alignas(16) float token[kScaleSlots][kScaleBlocks][TOKENS];      // per block: token scale (x block scale)
     alignas(16) float weight[TILES ? kScaleSlots : 1][kScaleBlocks][TILES ? kRows : 1];  // 1 x 128 tiles: the weight rows' scales
     uint64_t full[S::kStages], empty[S::kStages];
-    uint64_t tmem_full[4], tmem_empty[4];
+    uint64_t tmem_full[S::kBufs], tmem_empty[S::kBufs];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint64_t part_full, part_empty;
     uint32_t tmem, dead;
@@ -424,12 +424,12 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
 // x 7168 in 48 clusters of 6 on two CTAs per SM takes 17 us, in 32 of 3 11.
 // Asked once, of the kernel of which one CTA fits an SM (of one that allocates
 // TMEM the runtime counts no second CTA, although it runs).
-int clusters_per_turn(int split) {
+int clusters_per_turn(int split, int sms) {
     static std::atomic<int> known[kMostSplit + 1];
     int n = known[split].load(std::memory_order_relaxed);
     if (n > 0) return n;
     using S = Shape<128, false>;
-    const int most = sm_count() / split;
+    const int most = sms / split;
     n = max_clusters(reinterpret_cast<const void*>(gemm_stream_kernel<0, 128>), S::kThreads, smem_bytes<128, false>(1), split);
     n = n <= 0 || n > most ? most : n;
     known[split].store(n, std::memory_order_relaxed);
@@ -437,14 +437,14 @@ int clusters_per_turn(int split) {
 }
 
 template <int TOKENS>
-StreamPlan plan(const GemmProblem& p) {
+StreamPlan plan(const GemmProblem& p, int sms) {
     const int ctas = p.b_tiles ? Shape<TOKENS, true>::kCtas : Shape<TOKENS, false>::kCtas;  // per SM
     const int64_t tiles_n = (p.n + kRows - 1) / kRows, tiles_m = (p.m + TOKENS - 1) / TOKENS, kb = blocks_of(p.k);
     const int64_t busy = p.groups < p.m ? p.groups : p.m;  // groups with rows, at most
-    StreamPlan r = {(tiles_m + busy - 1) * tiles_n, 1, ctas * sm_count()};
+    StreamPlan r = {(tiles_m + busy - 1) * tiles_n, 1, ctas * sms};
     // shares of the contraction: as many as run at one time, each at least two blocks long
     for (int split = 2; split <= kMostSplit && kb >= 2 * split; ++split) {
-        const int clusters = ctas * clusters_per_turn(split);
+        const int clusters = ctas * clusters_per_turn(split, sms);
         if (r.items <= clusters) r = {r.items, split, clusters};
     }
     return r;
@@ -452,7 +452,7 @@ StreamPlan plan(const GemmProblem& p) {
 
 template <int TOKENS>
 fp8_status_t run(const char* fn, const GemmProblem& p, const CUtensorMap& a, const CUtensorMap& b, cudaStream_t st) {
-    const StreamPlan how = plan<TOKENS>(p);
+    const StreamPlan how = plan<TOKENS>(p, sm_count());
     const int64_t clusters = how.items + 1 < how.clusters ? how.items + 1 : how.clusters;
     const auto go = [&](auto kernel, size_t smem) {
         return launch_cluster(fn, kernel, dim3((unsigned)(clusters * how.split)), dim3(Shape<TOKENS, false>::kThreads), smem,
@@ -465,12 +465,12 @@ fp8_status_t run(const char* fn, const GemmProblem& p, const CUtensorMap& a, con
 
 }  // namespace
 
-StreamPlan stream_plan(const GemmProblem& p, int tokens) {
+StreamPlan stream_plan(const GemmProblem& p, int tokens, int sms) {
     switch (tokens) {
-        case 16: return plan<16>(p);
-        case 32: return plan<32>(p);
-        case 64: return plan<64>(p);
-        default: return plan<128>(p);
+        case 16: return plan<16>(p, sms);
+        case 32: return plan<32>(p, sms);
+        case 64: return plan<64>(p, sms);
+        default: return plan<128>(p, sms);
     }
 }
 
