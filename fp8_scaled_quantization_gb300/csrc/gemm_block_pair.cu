@@ -19,13 +19,14 @@
 // arrive across the pair, the product is issued, takes its 512, and reports back
 // to both CTAs; two buffers share that way, and TMEM has no room for a third
 // (four of half the width run the tensor core at half its rate: 1000 cycles).
-// 1 x 128 tiles, 1330 cycles: the scaling warps themselves, with two operations
+// 1 x 128 tiles, 1240 cycles: the scaling warps themselves, with two operations
 // per element and 1020 cycles without any wait.  A spill in the loop costs more
 // than any of this gains (a load from local memory takes 300 cycles with shared
-// memory this full).  A tile costs another 2500 cycles, mostly to store it.
+// memory this full).  A tile costs another 2500 cycles (fp32 outputs: 4900),
+// mostly to store it.
 // Measured: 4001 x 7168 x 18432 (rows, n, k) 381 us, 2770 TFLOP/s; 16384 x 18432 x
-// 7168 against [k, n] 1.53 ms, 2830; 4096 x 14336 x 8192 in 1 x 128 tiles 535 to
-// 565 us.  The SM clock falls from 2070 to about 1850 MHz meanwhile (power).
+// 7168 against [k, n] 1.53 ms, 2830; 4096 x 14336 x 8192 in 1 x 128 tiles 525 us.  The SM
+// clock falls from 2070 to about 1850 MHz meanwhile (power).
 #include "fp8q_host.h"
 #include "fp8q_tcgen05.cuh"
 #include "gemm_block.cuh"
