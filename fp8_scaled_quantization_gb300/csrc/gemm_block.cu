@@ -137,7 +137,7 @@ namespace {
 // where the stream kernel reaches 6.5 TB/s and the pair kernel 4.5 (96 rows over
 // 64 experts, 2048 x 7168 each: stream/16 99, stream/32 107, pair 137).  Over 405
 // forms and sizes (8 to 4096 rows, weights of 512 x 2048 to 18432 x 7168) the
-// choices take 0.2% more than the fastest do, 17% at worst.
+// choices take 0.2% more than the fastest do, 18% at worst.
 struct Choice {
     int tokens;  // 0: the pair kernel
     double us;
