@@ -216,7 +216,7 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 or 32 columns of this warp's 32 lanes: lane l gets row l, r[j] column j.
+// 16 columns of this warp's 32 lanes: lane l gets row l, r[j] column j.
 __device__ __forceinline__ void tmem_ld_32x16(uint32_t addr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
