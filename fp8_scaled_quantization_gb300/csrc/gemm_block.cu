@@ -126,10 +126,10 @@ fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, 
 namespace {
 // Which kernel, by estimated times in microseconds from what both measured on
 // GB300 (one call, in a CUDA graph, cold weights; [m, n, k] bf16 out):
-//   [8, 7168, 18432]   stream/16 25   pair 64      [48, 14336, 4096]  stream/32 18  stream/64 20  pair 22
-//   [64, 7168, 7168]   stream/64 17   pair 30      [256, 4096, 4096]  stream/32 17  stream/128 20 pair 18
-//   [256, 7168, 7168]  pair 30  stream/128 31      [512, 1024, 4096]  stream/64 13  pair 18
-//   in 1 x 128 tiles: [256, 2048, 7168]  stream/128 18  pair 41    [768, 7168, 7168]  pair 79  stream/128 99
+//   [8, 7168, 18432]   stream/16 25   pair 64      [48, 14336, 4096]  stream/32 17  stream/64 20  pair 20
+//   [64, 7168, 7168]   stream/64 17   pair 29      [256, 4096, 4096]  stream/32 16  stream/128 20 pair 18
+//   [256, 7168, 7168]  pair 30  stream/128 28      [512, 1024, 4096]  stream/64 12  pair 18
+//   in 1 x 128 tiles: [256, 2048, 7168]  stream/128 17  pair 41    [768, 7168, 7168]  pair 79  stream/128 90
 // A pair of CTAs takes 0.46 (1 x 128 tiles: 0.67) per 128-block of a 256 x 256
 // tile, whatever part of the tile is used.  A CTA of the stream kernel takes
 // kBlock per block with 16 / 32 / 64 / 128 tokens, with two CTAs per SM up to 64
@@ -137,7 +137,7 @@ namespace {
 // where the stream kernel reaches 6.5 TB/s and the pair kernel 4.5 (96 rows over
 // 64 experts, 2048 x 7168 each: stream/16 99, stream/32 107, pair 137).  Over 405
 // forms and sizes (8 to 4096 rows, weights of 512 x 2048 to 18432 x 7168) the
-// choices take 0.2% more than the fastest do, 18% at worst.
+// choices take 0.3% more than the fastest do, 16% at worst.
 struct Choice {
     int tokens;  // 0: the pair kernel
     double us;
@@ -153,7 +153,7 @@ Choice choose(const GemmProblem& p) {
     const double memory = (busy * (double)p.n * (double)p.k + (double)p.m * (double)(p.k + 2 * p.n)) / 6.5e6;
     const double pair = ceil(tiles(256) * (double)((p.n + 255) / 256) / (double)(sms / 2)) * (double)kb * (p.b_tiles ? 0.67 : 0.46);
     Choice best = {0, 4.0 + most(pair, memory * 6.5 / 4.5)};
-    constexpr double kBlock[2][4] = {{0.40, 0.39, 0.66, 0.53}, {0.45, 0.47, 0.40, 0.57}}, kJoin[4] = {1.0, 1.8, 2.2, 4.0};
+    constexpr double kBlock[2][4] = {{0.40, 0.39, 0.66, 0.53}, {0.43, 0.44, 0.39, 0.54}}, kJoin[4] = {1.0, 1.8, 2.2, 4.0};
     for (int i = 0; i < 4; ++i) {
         const int tokens = 16 << i;
         const StreamPlan plan = stream_plan(p, tokens, (int)sms);
