@@ -524,6 +524,8 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                         }
                     }
                 }
+                // the other CTA's last arrivals on this one's barriers have come before it ends
+                for (uint32_t i = it > 2 ? it - 2 : 0; i < it; ++i) w.wait(smem_addr(&sh.tmem_empty[i & 1]), (i >> 1) & 1);
             }
         } else if (warp == 9) {
             // ---- scales: this CTA's 128 rows and the pair's 256 columns (or their two 128-blocks)

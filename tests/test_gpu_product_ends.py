@@ -1,0 +1,49 @@
+"""The ends of the block-scaled product kernels, where CTAs of a cluster leave: tiles
+whose last columns are not there, so that some warps have nothing to store after their
+last arrival, launched one after another, each result against the plain 64-bit one."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import fp8_scaled_quantization_gb300 as fq
+import gemm_reference as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(native_lib):
+    return native_lib
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def blocks(n):
+    return -(-n // 128)
+
+
+@pytest.mark.parametrize("m,n", [(1, 1), (300, 1), (256, 128), (129, 130), (520, 257), (700, 520)])
+@pytest.mark.parametrize("counts", [[128], [1, 0, 127, 300], [256, 129, 640]])
+def test_pairs_leave_after_each_others_last_arrivals(m, n, counts):
+    """Ragged contractions always take CTA pairs; n is at most 128 columns beyond a tile of 256."""
+    rows, e, g = sum(counts), len(counts), gen(m + n)
+    a, sa = R.finite_codes((m, rows), 1, g, DEV), R.scales((m, blocks(rows)), g, DEV)
+    b, sb = R.finite_codes((n, rows), 0, g, DEV), R.scales((n, blocks(rows)), g, DEV)
+    ends = torch.tensor(counts, dtype=torch.int64, device=DEV).cumsum(0)
+    ds = [torch.full((e, m, n), float("nan"), device=DEV) for _ in range(40)]
+    for d in ds:
+        fq.fp8_gemm_block_grouped_wgrad(a, sa, b, sb, ends, d, fq.E5M2, fq.E4M3)
+    av, bv, start = R.values(a, sa, 1, 1), R.values(b, sb, 0, 1), 0
+    for i, c in enumerate(counts):
+        value, bound = R.product(av[:, start:start + c], bv[:, start:start + c])
+        # a group that is not aligned to 128 touches up to two blocks more than its length says
+        R.check(ds[0][i], value, bound * (128 + blocks(c) + 6) / (128 + blocks(c) + 4))
+        start += c
+    assert all(torch.equal(d, ds[0]) for d in ds[1:])
+    assert fq.wait_timeouts() == 0
