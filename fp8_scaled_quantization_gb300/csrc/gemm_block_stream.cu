@@ -245,7 +245,9 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
             if (lane < split) cluster_arrive<true>(cluster_addr(smem_addr(&sh.part_full), lane));
             w.template wait<true>(smem_addr(&sh.part_full), items & 1);
             __syncwarp();
-            const int j0 = tokens * rank / split, j1 = tokens * (rank + 1) / split;
+            // A lane without a column reads nothing: what it read it would not wait for, and the
+            // CTA that holds it may leave once this one's warps have met it.
+            const int j0 = tokens * rank / split, j1 = col < p.n ? tokens * (rank + 1) / split : j0;
             for (int j = j0 + (warp >> 2); j < j1; j += S::kScalers / 4) {
                 float v[kMostSplit];
 #pragma unroll
@@ -255,7 +257,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
 #pragma unroll
                 for (int r = 1; r < kMostSplit; ++r)
                     if (r < split) sum = __fadd_rn(sum, v[r]);
-                if (col < p.n) store_out(p, (int64_t)(item.row0 + j) * p.n + col, sum);
+                store_out(p, (int64_t)(item.row0 + j) * p.n + col, sum);
             }
             __syncwarp();
             // (nothing overwrites the last item's sums)

@@ -47,3 +47,24 @@ def test_pairs_leave_after_each_others_last_arrivals(m, n, counts):
         start += c
     assert all(torch.equal(d, ds[0]) for d in ds[1:])
     assert fq.wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("form", ["nk", "kn", "tiles"])
+@pytest.mark.parametrize("m", [1, 7, 16, 33, 64, 100])
+@pytest.mark.parametrize("n", [1, 32, 33, 129, 160, 300])
+def test_clusters_leave_after_reads_of_each_others_sums(n, m, form):
+    """Few columns and a long contraction: as many CTAs share it as a cluster holds, and in
+    the last 128 columns whole warps have no column to join."""
+    k, g = 2300, gen(n + m)
+    a, sa = R.finite_codes((m, k), 0, g, DEV), R.scales((m, blocks(k)), g, DEV)
+    shape, scales = {"nk": ((n, k), (blocks(n), blocks(k))), "kn": ((k, n), (blocks(k), blocks(n))),
+                     "tiles": ((n, k), (n, blocks(k)))}[form]
+    b, sb = R.finite_codes(shape, 0, g, DEV), R.scales(scales, g, DEV)
+    ds = [torch.full((m, n), float("nan"), device=DEV) for _ in range(40)]
+    for d in ds:
+        fq.fp8_gemm_block(a, sa, b, sb, d, b_layout=fq.B_KN if form == "kn" else fq.B_NK,
+                          b_block_rows=1 if form == "tiles" else 128)
+    bv = R.values(b, sb, 0, 1 if form == "tiles" else 128)
+    R.check(ds[0], *R.product(R.values(a, sa, 0, 1), bv.T if form == "kn" else bv))
+    assert all(torch.equal(d, ds[0]) for d in ds[1:])
+    assert fq.wait_timeouts() == 0
