@@ -119,20 +119,27 @@ struct Waiter {
         return done != 0;
     }
 
+    // Polls for one limit's time; whether the phase completed.
     // CLUSTER: acquire what the other CTA's threads wrote before they arrived.
     template <bool CLUSTER = false>
-    __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
-        if (poll<CLUSTER>(bar, parity) || dead) return;
+    static __device__ __forceinline__ bool within_limit(uint32_t bar, uint32_t parity) {
         // Reading the timer takes longer than most waits do: not before many polls.
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
-            if (poll<CLUSTER>(bar, parity)) return;
+            if (poll<CLUSTER>(bar, parity)) return true;
         const uint64_t t0 = global_ns();
 #pragma unroll 1
         for (uint32_t i = 0; i < kMbarWaitMaxPolls; ++i) {
-            if (poll<CLUSTER>(bar, parity)) return;
+            if (poll<CLUSTER>(bar, parity)) return true;
             if ((i & 15) == 15 && global_ns() - t0 > kMbarWaitLimitNs) break;
         }
+        return false;
+    }
+
+    template <bool CLUSTER = false>
+    __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) {
+        if (poll<CLUSTER>(bar, parity) || dead) return;
+        if (within_limit<CLUSTER>(bar, parity)) return;
         dead = true;
         atomicAdd(&g_wait_timeouts, 1ull);
     }

@@ -634,12 +634,20 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             // ---- masking: steps of other groups become zeros, in both operands (their codes may be NaN)
             const uint32_t base = smem_addr(tiles), full0 = cluster_addr(smem_addr(&sh.full[0]), 0);
             uint32_t stage = 0, phases = 0;  // bit s: the phase of landed[s]
-            for (int t = first; t < total; t += step) {
+            uint32_t passed = 0;             // blocks and tiles since this warp last waited
+            for (int t = first; t < total; t += step, ++passed) {
                 const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
-                for (int b = 0; b < tile.blks; ++b) {
+                for (int b = 0; b < tile.blks; ++b, ++passed) {
                     const int x = (tile.blk0 + b) * kBlk;
                     if (is_cut(tile, x, (int)p.k)) {
-                        w.wait(smem_addr(&sh.landed[stage]), phases >> stage & 1);
+                        // The other roles keep step with the ring; this one waits here while they go
+                        // through all that it passed.  A contraction of 8e8 steps takes 4 s, so each
+                        // 2^16 blocks (0.05 s, tiles of one block 0.2) add a limit's time.
+                        const uint32_t bar = smem_addr(&sh.landed[stage]), parity = phases >> stage & 1;
+                        for (uint32_t i = passed >> 16; i > 0 && !w.dead && !Waiter::within_limit(bar, parity); --i)
+                            if (*(volatile uint32_t*)&sh.dead != 0) break;
+                        passed = 0;
+                        w.wait(bar, parity);
                         phases ^= 1u << stage;
                         __syncwarp();
                         mask_stage(base + stage * kStageBytes, tile.k_lo - x, tile.k_hi - x, lane);

@@ -68,3 +68,21 @@ def test_clusters_leave_after_reads_of_each_others_sums(n, m, form):
     R.check(ds[0], *R.product(R.values(a, sa, 0, 1), bv.T if form == "kn" else bv))
     assert all(torch.equal(d, ds[0]) for d in ds[1:])
     assert fq.wait_timeouts() == 0
+
+
+def test_a_group_end_behind_a_long_contraction():
+    """8e8 rows of one expert, four seconds for one CTA pair: the block that its end cuts is
+    masked only then, and what waits for that block must not have given up."""
+    rows = 3 * 2 ** 28
+    ends = [rows - 200, rows - 75, rows]
+    a, b = (torch.zeros((1, rows), dtype=torch.uint8, device=DEV) for _ in range(2))
+    one = 0x38  # 1.0 in E4M3: every sum below is exact
+    at = torch.cat([torch.arange(0, rows - 300, 2 ** 20 + 7), torch.arange(rows - 290, rows)]).to(DEV)
+    a[0, at], b[0, at] = one, one
+    a[0, rows - 150], b[0, rows - 40] = 0x7F, 0x7F  # NaN in groups 1 and 2 only
+    scale = torch.ones((1, blocks(rows)), device=DEV)
+    d = torch.empty((3, 1, 1), device=DEV)
+    fq.fp8_gemm_block_grouped_wgrad(a, scale, b, scale, torch.tensor(ends, device=DEV), d)
+    torch.cuda.synchronize()
+    assert fq.wait_timeouts() == 0
+    assert d[0].item() == int((at < ends[0]).sum()) and d[1].isnan().all() and d[2].isnan().all()
