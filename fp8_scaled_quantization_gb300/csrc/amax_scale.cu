@@ -260,7 +260,8 @@ extern "C" fp8_status_t fp8_amax(const void* x, fp8_dtype_t dtype, int64_t n, fl
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     fp8_status_t s;
-    Workspace* ws = stream_workspace(st, &s);
+    StreamUse use(st);
+    Workspace* ws = use.workspace(&s);
     if (!ws) return s;
     int nparts = 0;
     s = enqueue_amax_partials(x, dtype, n, ws, st, &nparts);

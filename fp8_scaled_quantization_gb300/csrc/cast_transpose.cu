@@ -257,10 +257,11 @@ extern "C" fp8_status_t fp8_quantize_cast_transpose(const void* x, fp8_dtype_t d
     const int64_t ntiles = ((cols + kTile - 1) / kTile) * ((rows + kTile - 1) / kTile);
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    StreamUse use(st);
     Workspace* ws = nullptr;
     if (amax_out) {
         fp8_status_t s;
-        ws = stream_workspace(st, &s);
+        ws = use.workspace(&s);
         if (!ws) return s;
     }
     if (n == 0 && !amax_out) return FP8_OK;

@@ -50,15 +50,30 @@ fp8_status_t block_ct_wait_timeouts(unsigned long long* count);
 fp8_status_t gemm_pair_wait_timeouts(unsigned long long* count);
 fp8_status_t gemm_stream_wait_timeouts(unsigned long long* count);
 
-// Workspace of (current device, stream) for per-CTA partials; nullptr on
-// failure (the error message is set).
-Workspace* stream_workspace(cudaStream_t stream, fp8_status_t* st);
+// One call's use of the memory that the library keeps for (current device,
+// stream).  The first request takes that stream's lock, and the object holds it
+// to its end, after the call's last launch: the launches of a call that writes
+// and then reads that memory follow one another on the stream, whatever other
+// host threads launch there.  (A call may call another one on its stream.)
+class StreamUse {
+public:
+    explicit StreamUse(cudaStream_t stream) : stream_(stream) {}
+    ~StreamUse();
+    StreamUse(const StreamUse&) = delete;
+    StreamUse& operator=(const StreamUse&) = delete;
 
-// At least `bytes` bytes of scratch of (current device, stream), 256-byte
-// aligned, kept for later calls on the stream; a larger request allocates anew
-// and leaves the smaller one to those who captured its address.  nullptr on
-// failure (the error message is set).
-void* stream_scratch(cudaStream_t stream, size_t bytes, fp8_status_t* st);
+    // For per-CTA partials; nullptr on failure (the error message is set).
+    Workspace* workspace(fp8_status_t* st);
+    // At least `bytes` bytes of scratch, 256-byte aligned, kept for later calls on
+    // the stream; a larger request allocates anew and leaves the smaller one to
+    // those who captured its address.  nullptr on failure (the error message is set).
+    void* scratch(size_t bytes, fp8_status_t* st);
+
+private:
+    bool take(fp8_status_t* st);
+    cudaStream_t stream_;
+    struct StreamMemory* held_ = nullptr;
+};
 
 // Let `kernel` use `smem` bytes of dynamic shared memory on the current device
 // (asked of the runtime once per kernel, device and size).

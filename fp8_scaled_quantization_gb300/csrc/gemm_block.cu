@@ -91,7 +91,7 @@ fp8_status_t check_groups(const char* fn, int groups, const int64_t* ends) {
 }  // namespace
 
 fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, const Operand& b, CUtensorMap* map_b,
-                          cudaStream_t st) {
+                          StreamUse& use, cudaStream_t st) {
     const Operand* const in[2] = {&a, &b};
     CUtensorMap* const map[2] = {map_a, map_b};
     size_t need[2];
@@ -102,7 +102,7 @@ fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, 
     fp8_status_t s = FP8_OK;
     uint8_t* scratch = nullptr;
     if (need[0] + need[1] > 0) {
-        scratch = static_cast<uint8_t*>(stream_scratch(st, need[0] + need[1], &s));
+        scratch = static_cast<uint8_t*>(use.scratch(need[0] + need[1], &s));
         if (scratch == nullptr) return s;
     }
     for (int i = 0; i < 2; ++i) {

@@ -44,9 +44,10 @@ struct Operand {
 
 // Tensor maps of the operands of one product.  The bulk copies need 16-byte
 // aligned rows: an operand whose base or row length is not is first copied
-// into the stream's scratch with its rows a multiple of 16 apart.
+// into the stream's scratch with its rows a multiple of 16 apart; `use` lasts
+// until the product that reads it is launched.
 fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, const Operand& b, CUtensorMap* map_b,
-                          cudaStream_t st);
+                          StreamUse& use, cudaStream_t st);
 
 // gemm_block_pair.cu: 256 x 256 outputs per CTA pair.
 fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st);

@@ -679,8 +679,9 @@ fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st
     const bool bulk = aligned16(p.d) && p.n % (p.out_f32 ? 4 : 8) == 0 && !p.accumulate;
     const Operand oa = {p.a, p.k, p.m, 1, 128}, ob = {p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups, 128};
     CUtensorMap a = {}, b = {}, d = {};
+    StreamUse use(st);
     fp8_status_t s = FP8_OK;
-    if (p.k > 0) s = operand_maps(fn, oa, &a, ob, &b, st);
+    if (p.k > 0) s = operand_maps(fn, oa, &a, ob, &b, use, st);
     if (bulk && s == FP8_OK) s = encode_out_map(&d, p.d, p.out_f32, p.n, p.m, p.b_tiles ? p.groups : 1);
     if (s != FP8_OK) return s;
     const int64_t tiles_n = (p.n + kPairN - 1) / kPairN, tiles_m = (p.m + kPairM - 1) / kPairM;

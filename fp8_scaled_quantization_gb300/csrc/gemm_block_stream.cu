@@ -481,7 +481,8 @@ StreamPlan stream_plan(const GemmProblem& p, int tokens, int sms) {
 fp8_status_t run_gemm_stream(const char* fn, const GemmProblem& p, int tokens, cudaStream_t st) {
     const Operand oa = {p.a, p.k, p.m, 1, tokens}, ob = {p.b, p.b_kn ? p.n : p.k, p.b_kn ? p.k : p.n, p.groups, 128};
     CUtensorMap a = {}, b = {};
-    const fp8_status_t s = operand_maps(fn, oa, &a, ob, &b, st);
+    StreamUse use(st);
+    const fp8_status_t s = operand_maps(fn, oa, &a, ob, &b, use, st);
     if (s != FP8_OK) return s;
     switch (tokens) {
         case 16: return run<16>(fn, p, a, b, st);

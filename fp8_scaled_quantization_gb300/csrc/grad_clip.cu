@@ -354,7 +354,8 @@ fp8_status_t for_tables(const char* fn, const Tensors& g, int64_t reps, Go go) {
 template <int N>
 fp8_status_t run(const char* fn, const Tensors& g, bool clip, Clip c, cudaStream_t st) {
     fp8_status_t s = FP8_OK;
-    Workspace* ws = stream_workspace(st, &s);
+    StreamUse use(st);
+    Workspace* ws = use.workspace(&s);
     if (!ws) return s;
     double* parts = reinterpret_cast<double*>(ws->sat);
     c.parts = parts;

@@ -220,7 +220,8 @@ extern "C" fp8_status_t fp8_amax_grouped(int count, const void* const* xs, const
         if (t.chunk_begin[count] > kMaxPartials) return fail(FP8_ERR_UNSUPPORTED, "%s: group too large", fn);
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    Workspace* ws = stream_workspace(st, &s);
+    StreamUse use(st);
+    Workspace* ws = use.workspace(&s);
     if (!ws) return s;
     const dim3 grid((unsigned)t.chunk_begin[count]), block(kThreads);
     const int r = (int)reps;

@@ -264,10 +264,11 @@ extern "C" fp8_status_t fp8_quantize(const void* x, fp8_dtype_t dtype, int64_t n
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool reduce = amax_out != nullptr || sat_count_out != nullptr;
     if (n == 0 && !reduce) return FP8_OK;
+    StreamUse use(st);
     Workspace* ws = nullptr;
     if (reduce) {
         fp8_status_t s;
-        ws = stream_workspace(st, &s);
+        ws = use.workspace(&s);
         if (!ws) return s;
     }
     int nparts = 0;
@@ -304,7 +305,8 @@ extern "C" fp8_status_t fp8_quantize_delayed(const void* x, fp8_dtype_t dtype, i
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     fp8_status_t s;
-    Workspace* ws = stream_workspace(st, &s);
+    StreamUse use(st);
+    Workspace* ws = use.workspace(&s);
     if (!ws) return s;
     int nparts = 0;
     s = enqueue_cast(static_cast<const uint8_t*>(x), dtype == FP8_DT_BF16, n, (int)fmt, scale, q_out, ws, true,
@@ -341,7 +343,8 @@ extern "C" fp8_status_t fp8_quantize_current(const void* x, fp8_dtype_t dtype, i
     if (reinterpret_cast<uintptr_t>(x) % dtype_size(dtype)) return fail(FP8_ERR_INVALID_ARG, "%s: x not element-aligned", fn);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     fp8_status_t s;
-    Workspace* ws = stream_workspace(st, &s);
+    StreamUse use(st);
+    Workspace* ws = use.workspace(&s);
     if (!ws) return s;
     const bool bf16 = dtype == FP8_DT_BF16;
     if (n == 0 || !aligned16(x) || !aligned16(q_out)) {

@@ -20,13 +20,18 @@ thread_local char g_last_error[512] = "";
 std::atomic<unsigned long long> g_launches{0};
 
 std::mutex g_mu;
-std::map<int, int> g_sm_count;                                 // device -> SMs
-std::map<std::pair<int, uintptr_t>, Workspace*> g_workspaces;  // (device, stream) -> ws
-struct Scratch {
-    std::vector<void*> all;  // the last one is in use, the others may be held by captured graphs
-    size_t bytes = 0;
+std::map<int, int> g_sm_count;  // device -> SMs
+}  // namespace
+
+struct StreamMemory {
+    std::recursive_mutex mu;
+    Workspace* ws = nullptr;
+    std::vector<void*> scratch;  // the last one is in use, the others may be held by captured graphs
+    size_t scratch_bytes = 0;
 };
-std::map<std::pair<int, uintptr_t>, Scratch> g_scratch;
+
+namespace {
+std::map<std::pair<int, uintptr_t>, StreamMemory> g_streams;  // (device, stream); entries stay, for those who wait for one
 }  // namespace
 
 fp8_status_t fail(fp8_status_t st, const char* fmt, ...) {
@@ -160,60 +165,65 @@ fp8_status_t encode_out_map(CUtensorMap* map, void* base, bool f32, int64_t cols
     return FP8_OK;
 }
 
-Workspace* stream_workspace(cudaStream_t stream, fp8_status_t* st) {
+bool StreamUse::take(fp8_status_t* st) {
     *st = FP8_OK;
+    if (held_ != nullptr) return true;
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) {
         *st = cuda_status(e, "cudaGetDevice");
-        return nullptr;
+        return false;
     }
-    std::lock_guard<std::mutex> lk(g_mu);
-    auto key = std::make_pair(dev, reinterpret_cast<uintptr_t>(stream));
-    auto it = g_workspaces.find(key);
-    if (it != g_workspaces.end()) return it->second;
+    StreamMemory* m;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        m = &g_streams[std::make_pair(dev, reinterpret_cast<uintptr_t>(stream_))];
+    }
+    m->mu.lock();
+    held_ = m;
+    return true;
+}
+
+StreamUse::~StreamUse() {
+    if (held_ != nullptr) held_->mu.unlock();
+}
+
+Workspace* StreamUse::workspace(fp8_status_t* st) {
+    if (!take(st)) return nullptr;
+    if (held_->ws != nullptr) return held_->ws;
     // First use on this stream.  Relax the thread's capture mode so that the
     // allocation is legal while a stream is being captured.  The partial slots
     // need no initial value: a launch writes every slot its finalize reads.
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     cudaThreadExchangeStreamCaptureMode(&mode);
     void* p = nullptr;
-    e = cudaMalloc(&p, sizeof(Workspace));
+    const cudaError_t e = cudaMalloc(&p, sizeof(Workspace));
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) {
         *st = cuda_status(e, "cudaMalloc(workspace)");
         return nullptr;
     }
-    auto* ws = static_cast<Workspace*>(p);
-    g_workspaces[key] = ws;
-    return ws;
+    held_->ws = static_cast<Workspace*>(p);
+    return held_->ws;
 }
 
-void* stream_scratch(cudaStream_t stream, size_t bytes, fp8_status_t* st) {
-    *st = FP8_OK;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) {
-        *st = cuda_status(e, "cudaGetDevice");
-        return nullptr;
-    }
-    std::lock_guard<std::mutex> lk(g_mu);
-    Scratch& s = g_scratch[std::make_pair(dev, reinterpret_cast<uintptr_t>(stream))];
-    if (s.bytes >= bytes) return s.all.back();
+void* StreamUse::scratch(size_t bytes, fp8_status_t* st) {
+    if (!take(st)) return nullptr;
+    if (held_->scratch_bytes >= bytes) return held_->scratch.back();
     // a quarter more than asked for, so that slowly growing requests do not allocate each time
     const size_t want = (bytes + bytes / 4 + 255) & ~(size_t)255;
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     cudaThreadExchangeStreamCaptureMode(&mode);
     void* p = nullptr;
-    e = cudaMalloc(&p, want);
+    const cudaError_t e = cudaMalloc(&p, want);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) {
         cudaGetLastError();  // the failed allocation is reported here, not by a later launch
         *st = cuda_status(e, "cudaMalloc(scratch)");
         return nullptr;
     }
-    s.all.push_back(p);
-    s.bytes = want;
+    held_->scratch.push_back(p);
+    held_->scratch_bytes = want;
     return p;
 }
 
@@ -254,18 +264,19 @@ fp8_status_t fp8_release_stream_workspace(void* stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_status(e, "fp8_release_stream_workspace: cudaGetDevice");
-    std::vector<void*> mine;
+    StreamMemory* m = nullptr;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        const auto key = std::make_pair(dev, reinterpret_cast<uintptr_t>(stream));
-        if (auto it = g_workspaces.find(key); it != g_workspaces.end()) {
-            mine.push_back(it->second);
-            g_workspaces.erase(it);
-        }
-        if (auto it = g_scratch.find(key); it != g_scratch.end()) {
-            mine.insert(mine.end(), it->second.all.begin(), it->second.all.end());
-            g_scratch.erase(it);
-        }
+        const auto it = g_streams.find(std::make_pair(dev, reinterpret_cast<uintptr_t>(stream)));
+        if (it != g_streams.end()) m = &it->second;
+    }
+    std::vector<void*> mine;
+    if (m != nullptr) {
+        std::lock_guard<std::recursive_mutex> lk(m->mu);  // after the calls that are being enqueued
+        mine.swap(m->scratch);
+        m->scratch_bytes = 0;
+        if (m->ws != nullptr) mine.push_back(m->ws);
+        m->ws = nullptr;
     }
     if (mine.empty()) return FP8_OK;  // nothing was allocated for this stream
     // The stream's queued work may still use the memory.

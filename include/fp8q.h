@@ -41,10 +41,13 @@
  *           delayed update) store one partial per CTA in a per-(device,
  *           stream) workspace; a one-CTA finalize kernel launched right after
  *           the main kernel reduces them.  Calls on the same stream are
- *           ordered and safe.  Calls on different streams use different
- *           workspaces and are safe.  A CUDA graph captured from a stream
- *           keeps that stream's workspace address: do not replay such a graph
- *           concurrently with other work on the capturing stream.  The first
+ *           ordered and safe, from several host threads too: a call of more
+ *           than one launch enqueues them together.  Calls on different
+ *           streams use different workspaces and are safe.  A CUDA graph
+ *           captured from a stream keeps that stream's workspace address: do
+ *           not replay such a graph concurrently with other work on the
+ *           capturing stream, or with another graph captured from it.  The
+ *           same holds for the scratch of odd operands.  The first
  *           call on a new stream allocates (cudaMalloc) with the thread's
  *           capture mode relaxed, so it may happen during capture.
  *
