@@ -65,8 +65,9 @@ public:
     // For per-CTA partials; nullptr on failure (the error message is set).
     Workspace* workspace(fp8_status_t* st);
     // At least `bytes` bytes of scratch, 256-byte aligned, kept for later calls on
-    // the stream; a larger request allocates anew and leaves the smaller one to
-    // those who captured its address.  nullptr on failure (the error message is set).
+    // the stream; a larger request allocates anew and frees the smaller one in
+    // stream order, unless a call that was being captured got its address: that one
+    // stays for the graph.  nullptr on failure (the error message is set).
     void* scratch(size_t bytes, fp8_status_t* st);
 
 private:

@@ -26,8 +26,11 @@ std::map<int, int> g_sm_count;  // device -> SMs
 struct StreamMemory {
     std::recursive_mutex mu;
     Workspace* ws = nullptr;
-    std::vector<void*> scratch;  // the last one is in use, the others may be held by captured graphs
+    void* scratch = nullptr;        // in use
     size_t scratch_bytes = 0;
+    bool scratch_captured = false;  // a graph may hold its address
+    std::vector<void*> captured;    // outgrown, held by graphs
+    std::vector<void*> outgrown;    // while the stream was being captured: freed by a later call
 };
 
 namespace {
@@ -209,21 +212,47 @@ Workspace* StreamUse::workspace(fp8_status_t* st) {
 
 void* StreamUse::scratch(size_t bytes, fp8_status_t* st) {
     if (!take(st)) return nullptr;
-    if (held_->scratch_bytes >= bytes) return held_->scratch.back();
+    StreamMemory& m = *held_;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream_, &status);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        *st = cuda_status(e, "cudaStreamIsCapturing");
+        return nullptr;
+    }
+    const bool capturing = status != cudaStreamCaptureStatusNone;
+    if (m.scratch_bytes >= bytes) {
+        m.scratch_captured |= capturing;
+        return m.scratch;
+    }
     // a quarter more than asked for, so that slowly growing requests do not allocate each time
     const size_t want = (bytes + bytes / 4 + 255) & ~(size_t)255;
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     cudaThreadExchangeStreamCaptureMode(&mode);
+    // The smaller one goes first, in stream order (work that uses it is before it on the
+    // stream), so that both need not fit at once.
+    if (m.scratch != nullptr) {
+        std::vector<void*>& to = m.scratch_captured ? m.captured : m.outgrown;
+        to.push_back(m.scratch);
+        m.scratch = nullptr;
+        m.scratch_bytes = 0;
+    }
     void* p = nullptr;
-    const cudaError_t e = cudaMalloc(&p, want);
+    if (capturing) {  // an allocation in stream order would become part of the graph
+        e = cudaMalloc(&p, want);
+    } else {
+        for (; e == cudaSuccess && !m.outgrown.empty(); m.outgrown.pop_back()) e = cudaFreeAsync(m.outgrown.back(), stream_);
+        if (e == cudaSuccess) e = cudaMallocAsync(&p, want, stream_);
+    }
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) {
         cudaGetLastError();  // the failed allocation is reported here, not by a later launch
-        *st = cuda_status(e, "cudaMalloc(scratch)");
+        *st = cuda_status(e, "allocation of scratch");
         return nullptr;
     }
-    held_->scratch.push_back(p);
-    held_->scratch_bytes = want;
+    m.scratch = p;
+    m.scratch_bytes = want;
+    m.scratch_captured = capturing;
     return p;
 }
 
@@ -271,16 +300,23 @@ fp8_status_t fp8_release_stream_workspace(void* stream) {
         if (it != g_streams.end()) m = &it->second;
     }
     std::vector<void*> mine;
+    bool graphs = false;
     if (m != nullptr) {
         std::lock_guard<std::recursive_mutex> lk(m->mu);  // after the calls that are being enqueued
-        mine.swap(m->scratch);
+        graphs = m->scratch_captured || !m->captured.empty();
+        mine.swap(m->captured);
+        mine.insert(mine.end(), m->outgrown.begin(), m->outgrown.end());
+        m->outgrown.clear();
+        if (m->scratch != nullptr) mine.push_back(m->scratch);
+        m->scratch = nullptr;
         m->scratch_bytes = 0;
+        m->scratch_captured = false;
         if (m->ws != nullptr) mine.push_back(m->ws);
         m->ws = nullptr;
     }
     if (mine.empty()) return FP8_OK;  // nothing was allocated for this stream
-    // The stream's queued work may still use the memory.
-    e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    // The stream's queued work may still use the memory, and graphs that run elsewhere.
+    e = graphs ? cudaDeviceSynchronize() : cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     for (void* p : mine) {
         const cudaError_t f = cudaFree(p);
         if (e == cudaSuccess) e = f;

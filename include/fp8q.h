@@ -487,8 +487,11 @@ fp8_status_t fp8_block128_scales_to_mx(const float* scale_inv, int64_t rows, int
  *   Alignment       operands with 16-byte aligned bases and rows that are
  *                   multiples of 16 bytes are read in place.  Others are first
  *                   copied, with their rows 16-byte aligned, into scratch of
- *                   the stream, which grows to the largest such call (about
- *                   1.25 times its codes) and is kept for later ones;
+ *                   the stream, which grows to the largest such call (at most
+ *                   1.25 times its aligned codes) and is kept for later ones.
+ *                   What it outgrew is freed in stream order, except what a
+ *                   captured call used: its graph holds that address, and it
+ *                   stays until fp8_release_stream_workspace.
  *                   FP8_ERR_CUDA if it cannot be allocated.  D may start
  *                   anywhere; whole 16-byte rows are written faster.
  * NaN codes and E5M2 infinities follow fp32 arithmetic (the sign and payload
