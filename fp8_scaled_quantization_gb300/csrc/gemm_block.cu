@@ -59,13 +59,16 @@ fp8_status_t check(const char* fn, const GemmProblem& p, int layout, int b_block
         return fail(FP8_ERR_UNSUPPORTED, "%s: 1x128 tiles of B run along the contraction: B must be [n, k]", fn);
     if (p.accumulate && out_dtype != FP8_DT_FP32)
         return fail(FP8_ERR_UNSUPPORTED, "%s: accumulate needs an fp32 output", fn);
-    constexpr int64_t kMost = (1ll << 31) - 256, kTile = 64;
+    constexpr int64_t kMost = (1ll << 31) - 256, kMostTiles = 1ll << 30;
     if (p.m > kMost || p.n > kMost || p.k > kMost)
         return fail(FP8_ERR_UNSUPPORTED, "%s: sizes must be below 2^31 - 256", fn);
-    // tiles are numbered with 32 bits
-    const int64_t tn = (p.n + kTile - 1) / kTile, tm = (p.m + kTile - 1) / kTile;
-    if ((tm + p.groups) * tn > kMost || (p.groups > 1 && tm * tn * p.groups > kMost))
-        return fail(FP8_ERR_UNSUPPORTED, "%s: too many output tiles", fn);
+    // Tiles are numbered with 32 bits: 256 x 256 outputs per group where the contraction
+    // is ragged; else at least 16 x 128, and one more along m for each group (and for
+    // the rows after the last one).
+    const bool ragged_k = p.b_tiles && p.ends != nullptr;
+    const int64_t tiles = ragged_k ? ((p.m + 255) / 256) * ((p.n + 255) / 256) * p.groups
+                                   : ((p.m + 15) / 16 + p.groups) * ((p.n + 127) / 128);
+    if (tiles > kMostTiles) return fail(FP8_ERR_UNSUPPORTED, "%s: too many output tiles", fn);
     if (p.m == 0 || p.n == 0) return FP8_OK;
     if (p.d == nullptr) return fail(FP8_ERR_INVALID_ARG, "%s: d is NULL", fn);
     if ((reinterpret_cast<uintptr_t>(p.d) & (uintptr_t)(dtype_size(out_dtype) - 1)) != 0)
