@@ -94,13 +94,14 @@ __device__ __forceinline__ float squares(const uint8_t* x, bool f32, bool vec, i
         }
         fold();
     }
-    for (int64_t i = last + threadIdx.x; i < hi; i += 4 * kThreads) {
+    for (int64_t i = last + threadIdx.x, step = 1; i < hi; i += 4 * kThreads, ++step) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float v = i + j * kThreads < hi ? element(x, f32, i + j * kThreads) : 0.0f;
             bits |= __float_as_uint(v);
             add(v, j);
         }
+        if (step % 16 == 0) fold();
     }
     *any = bits & (f32 ? 0x7FFFFFFFu : 0x7FFF7FFFu);
     fold();
@@ -122,9 +123,8 @@ __device__ __forceinline__ double block_sum_f64(double v, double* smem) {
 
 // Pass 1: one CTA per `reps` chunks, one 64-bit partial per CTA.
 //
-// A thread adds its squares in fp32: four sums of at most 16 values per chunk,
-// and those of its chunks one after another (unaligned tensors: four sums of 16 *
-// reps values).
+// A thread adds its squares in fp32: four sums of at most 16 values, then those
+// sums one after another, at most reps of them.
 // Squares leave the fp32 range for |x| above 2^63 and below 2^-63: where the
 // thread's sum is not below 2^120, or is below 2^-100 with some x nonzero, it
 // reads its elements again scaled by 2^-96 or 2^96, and the power of two is
