@@ -88,8 +88,9 @@ __device__ __forceinline__ Item locate(const GemmProblem& p, const GroupTable& g
     return r;
 }
 
-// acc += s_j * P_j over the warp's tokens: scales s at `token` (shared memory),
-// times the lane's own weight-row scale w2 (a pair of it) with 1 x 128 tiles.
+// acc += s_j * P_j over the warp's tokens, scales s at `token` (shared memory); with
+// 1 x 128 tiles acc += s_j * (P_j * w), w the lane's own weight-row scale (w2: a pair of
+// it).  That order is the pair kernel's: which one runs must not show in the result.
 // TMEM is read one piece ahead of the arithmetic; the sums are single numbers, as
 // packed pairs leave the compiler fewer registers (256 x 7168 x 7168 with 64
 // tokens: 34.6 us, packed 35.5, without reading ahead 38.6).
@@ -104,16 +105,18 @@ __device__ __forceinline__ void scale_add(float (&acc)[MINE], uint32_t from, con
         if (c + 1 < kPieces) tmem_ld_32x16(from + (c + 1) * 16, v[(c + 1) & 1]);
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
-            float4 s = *reinterpret_cast<const float4*>(token + c * 16 + j);
-            if constexpr (B_TILES) {
-                const float2 s0 = unpack2(mul2(pack2(s.x, s.y), w2)), s1 = unpack2(mul2(pack2(s.z, s.w), w2));
-                s = make_float4(s0.x, s0.y, s1.x, s1.y);
-            }
+            const float4 s = *reinterpret_cast<const float4*>(token + c * 16 + j);
             float* const at = acc + c * 16 + j;
-            at[0] = __fmaf_rn(__uint_as_float(v[c & 1][j]), s.x, at[0]);
-            at[1] = __fmaf_rn(__uint_as_float(v[c & 1][j + 1]), s.y, at[1]);
-            at[2] = __fmaf_rn(__uint_as_float(v[c & 1][j + 2]), s.z, at[2]);
-            at[3] = __fmaf_rn(__uint_as_float(v[c & 1][j + 3]), s.w, at[3]);
+            uint32_t* const x = v[c & 1] + j;
+            if constexpr (B_TILES) {
+                const float2 x0 = unpack2(mul2(pack2(x[0], x[1]), w2)), x1 = unpack2(mul2(pack2(x[2], x[3]), w2));
+                x[0] = __float_as_uint(x0.x), x[1] = __float_as_uint(x0.y);
+                x[2] = __float_as_uint(x1.x), x[3] = __float_as_uint(x1.y);
+            }
+            at[0] = __fmaf_rn(__uint_as_float(x[0]), s.x, at[0]);
+            at[1] = __fmaf_rn(__uint_as_float(x[1]), s.y, at[1]);
+            at[2] = __fmaf_rn(__uint_as_float(x[2]), s.z, at[2]);
+            at[3] = __fmaf_rn(__uint_as_float(x[3]), s.w, at[3]);
         }
     }
 }

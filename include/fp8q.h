@@ -463,7 +463,10 @@ fp8_status_t fp8_block128_scales_to_mx(const float* scale_inv, int64_t rows, int
  * steps of the contraction (the last one may be shorter)
  *   P_b[i, j] = sum over k in b of decode(A[i, k]) * decode(B[j, k])
  *   D[i, j]   = sum over b of (sa[i, b] * sb[j, b]) * P_b[i, j]
- * with P_b and the sum over b in fp32 and one rounding to D's type.
+ *               (1 x 128 tiles of B: of (P_b[i, j] * sb[j, b]) * sa[i, b])
+ * with P_b and the sum over b in fp32 and one rounding to D's type.  The inner
+ * products are rounded to fp32, and may leave its range, as they stand here,
+ * whatever the sizes.
  *
  *   a, scale_inv_a  device uint8[m, k] and float[m, ceil(k/128)]: codes and
  *                   factors as fp8_quantize_block(1, 128) or
