@@ -218,8 +218,8 @@ class BlockLinearStep:
         dev, rows = x.device, x.shape[0]
 
         def both(c):  # rowwise and columnwise codes with their factors
-            return [torch.empty((rows, c), dtype=torch.uint8, device=dev), _f32(dev, rows * -(-c // 128)).view(rows, -1),
-                    torch.empty((c, rows), dtype=torch.uint8, device=dev), _f32(dev, c * -(-rows // 128)).view(c, -1)]
+            return [torch.empty((rows, c), dtype=torch.uint8, device=dev), _f32(dev, (rows, -(-c // 128))),
+                    torch.empty((c, rows), dtype=torch.uint8, device=dev), _f32(dev, (c, -(-rows // 128)))]
 
         self.qx, self.qdy = both(inn), both(out)
         self.qw = torch.empty(weight.shape, dtype=torch.uint8, device=dev)
