@@ -132,7 +132,7 @@ namespace {
 //   [8, 7168, 18432]   stream/16 25   pair 64      [48, 14336, 4096]  stream/32 17  stream/64 20  pair 20
 //   [64, 7168, 7168]   stream/64 17   pair 29      [256, 4096, 4096]  stream/32 16  stream/128 20 pair 18
 //   [256, 7168, 7168]  pair 30  stream/128 28      [512, 1024, 4096]  stream/64 12  pair 18
-//   in 1 x 128 tiles: [256, 2048, 7168]  stream/128 17  pair 41    [768, 7168, 7168]  pair 79  stream/128 90
+//   in 1 x 128 tiles: [256, 2048, 7168]  stream/128 16  pair 41    [768, 7168, 7168]  pair 79  stream/128 90
 // A pair of CTAs takes 0.46 (1 x 128 tiles: 0.67) per 128-block of a 256 x 256
 // tile, whatever part of the tile is used.  A CTA of the stream kernel takes
 // kBlock per block with 16 / 32 / 64 / 128 tokens, with two CTAs per SM up to 64

@@ -24,9 +24,12 @@
 // than any of this gains (a load from local memory takes 300 cycles with shared
 // memory this full).  A tile costs another 2500 cycles (fp32 outputs: 4900),
 // mostly to store it.
-// Measured: 4001 x 7168 x 18432 (rows, n, k) 381 us, 2770 TFLOP/s; 16384 x 18432 x
-// 7168 against [k, n] 1.53 ms, 2830; 4096 x 14336 x 8192 in 1 x 128 tiles 525 us.  The SM
-// clock falls from 2070 to about 1850 MHz meanwhile (power).
+// Measured, a call after a pause and calls back to back, where the power limit holds
+// the SM clock at 1730 to 1880 MHz instead of 2070: 4001 x 7168 x 18432 (rows, n, k)
+// 389 and 429 us (2720 and 2460 TFLOP/s); 16384 x 18432 x 7168 against [k, n] 1.54 and
+// 1.70 ms (2810, 2550); 4096 x 14336 x 8192 in 1 x 128 tiles 528 and 538 us (1820, 1790).
+// Two figures beside one choice below were taken together, after pauses: compare
+// them with one another only.
 #include "fp8q_host.h"
 #include "fp8q_tcgen05.cuh"
 #include "gemm_block.cuh"

