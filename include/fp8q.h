@@ -145,11 +145,12 @@ fp8_status_t fp8_test_drop_tile_copy(int tile);
 
 /* Frees the reduction workspace (96 KB) and the products' scratch that the calls
  * made on `stream` on the current device, after waiting for the work queued on
- * that stream.  A later call on the stream that needs one allocates a new one.  Returns FP8_OK when there
- * is none.  Call it before destroying a stream when many short-lived streams
- * are used, and not while the stream is being captured or while a captured
- * graph whose kernels used that workspace may still be launched (its nodes
- * hold the workspace's address). */
+ * that stream (on the device, where a captured call used the scratch).  A later
+ * call on the stream that needs one allocates a new one.  Returns FP8_OK when
+ * there is none.  Call it before destroying a stream when many short-lived
+ * streams are used, and not while the stream is being captured or while a
+ * captured graph whose kernels used that memory may still be launched (its
+ * nodes hold the address). */
 fp8_status_t fp8_release_stream_workspace(void* stream);
 
 /* ------------------------------------------------------------------------ */
