@@ -25,6 +25,7 @@ DT_BF16, DT_FP32 = 0, 1
 AMAX_MAX, AMAX_MOST_RECENT = 0, 1
 COLUMNWISE_FROM_ORIGINAL, COLUMNWISE_FROM_ROWWISE_DEQUANTIZED = 0, 1
 B_NK, B_KN = 0, 1
+ACT_SILU, ACT_GELU_TANH = 0, 1
 FP8_MAX = {E4M3: 448.0, E5M2: 57344.0}
 
 __all__ = [
@@ -34,6 +35,7 @@ __all__ = [
     "fp8_block128_scales_to_mx", "fp8_amax_noalloc", "fp8_quantize_current", "fp8_quantize_hybrid", "fp8_quantize_block_cast_transpose",
     "fp8_amax_grouped", "fp8_quantize_grouped", "COLUMNWISE_FROM_ORIGINAL", "COLUMNWISE_FROM_ROWWISE_DEQUANTIZED",
     "B_NK", "B_KN", "fp8_gemm_block", "fp8_gemm_block_grouped", "fp8_gemm_block_grouped_wgrad",
+    "ACT_SILU", "ACT_GELU_TANH", "fp8_gemm_block_gated", "fp8_gemm_block_gated_grouped", "fp8_gated_block_backward",
     "fp8_grad_norm_grouped", "fp8_grad_clip_grouped",
     "launch_count", "version", "library", "release_stream_workspace", "wait_timeouts",
 ]
@@ -435,6 +437,66 @@ def fp8_gemm_block_grouped_wgrad(a, scale_inv_a, b, scale_inv_b, group_ends, d, 
     ends, pa, psa, pb, psb, pd = _ptrs(group_ends, a, scale_inv_a, b, scale_inv_b, d)
     _check(library().fp8_gemm_block_grouped_wgrad(groups, ends, pa, fmt_a, psa, pb, fmt_b, psb, m, n, rows, pd, _dt(d),
                                                   int(accumulate), _stream(stream)))
+
+
+def _codes(q, scale_inv, shape, scale_shape, name):
+    """Pointers of an optional pair of codes and scales of these shapes."""
+    if q is None and scale_inv is None:
+        return None, None
+    if q is None or scale_inv is None:
+        raise ValueError(f"{name} and scale_inv_{name} go together")
+    _operand(q, scale_inv, shape, scale_shape, name)
+    return _ptrs(q, scale_inv)
+
+
+def fp8_gemm_block_gated(a, scale_inv_a, b, scale_inv_b, h, scale_inv_h, gu=None, scale_inv_gu=None, fmt_a=E4M3,
+                         fmt_b=E4M3, act=ACT_SILU, stream=None):
+    """h [m, n] = E4M3 codes (1 x 128 factors) of act(a b[0]^T) * (a b[1]^T): a [m, k] with 1 x 128
+    factors, b [2, n, k] (gate, up) with 128 x 128 factors each.  gu [m, 2, n]: the checkpoint,
+    E4M3 codes (1 x 128 factors) of both projections, which fp8_gated_block_backward reads."""
+    m, k = _rows_cols(a)
+    n = _out(h, m)
+    kb, nb = -(-k // 128), -(-n // 128)
+    _operand(a, scale_inv_a, (m, k), (m, kb), "a")
+    _operand(b, scale_inv_b, (2, n, k), (2, nb, kb), "b")
+    _operand(h, scale_inv_h, (m, n), (m, nb), "h")
+    pgu, psgu = _codes(gu, scale_inv_gu, (m, 2, n), (m, 2, nb), "gu")
+    pa, psa, pb, psb, ph, psh = _ptrs(a, scale_inv_a, b, scale_inv_b, h, scale_inv_h)
+    _check(library().fp8_gemm_block_gated(pa, fmt_a, psa, pb, fmt_b, psb, act, m, n, k, ph, psh, pgu, psgu,
+                                          _stream(stream)))
+
+
+def fp8_gemm_block_gated_grouped(a, scale_inv_a, b, scale_inv_b, group_ends, h, scale_inv_h, gu=None,
+                                 scale_inv_gu=None, fmt_a=E4M3, fmt_b=E4M3, act=ACT_SILU, stream=None):
+    """fp8_gemm_block_gated per expert over rows sorted by expert: rows group_ends[e-1] ..
+    group_ends[e]-1 of a [rows, k] with b[e] ([groups, 2, n, k]); rows after the last end get
+    codes 0 and factors 1.  group_ends: int64 on the device."""
+    rows, k = _rows_cols(a)
+    groups = _ends(group_ends)
+    n = _out(h, rows)
+    kb, nb = -(-k // 128), -(-n // 128)
+    _operand(a, scale_inv_a, (rows, k), (rows, kb), "a")
+    _operand(b, scale_inv_b, (groups, 2, n, k), (groups, 2, nb, kb), "b")
+    _operand(h, scale_inv_h, (rows, n), (rows, nb), "h")
+    pgu, psgu = _codes(gu, scale_inv_gu, (rows, 2, n), (rows, 2, nb), "gu")
+    ends, pa, psa, pb, psb, ph, psh = _ptrs(group_ends, a, scale_inv_a, b, scale_inv_b, h, scale_inv_h)
+    _check(library().fp8_gemm_block_gated_grouped(groups, ends, pa, fmt_a, psa, pb, fmt_b, psb, act, rows, n, k, ph,
+                                                  psh, pgu, psgu, _stream(stream)))
+
+
+def fp8_gated_block_backward(dh, gu, scale_inv_gu, dgu=None, scale_inv_dgu=None, dgu_t=None, scale_inv_dgu_t=None,
+                             h_t=None, scale_inv_h_t=None, fmt_grad=E4M3, act=ACT_SILU, stream=None):
+    """From dh [rows, n] (bfloat16 / float32) and the checkpoint gu [rows, 2, n], 1 x 128 codes of
+    the projections' gradients, dgu [rows, 2, n] and transposed dgu_t [2, n, rows] (fmt_grad), and
+    of h^T, h_t [n, rows] (E4M3); each pair of outputs may be left out."""
+    rows, n = _rows_cols(dh)
+    nb, rb = -(-n // 128), -(-rows // 128)
+    _operand(gu, scale_inv_gu, (rows, 2, n), (rows, 2, nb), "gu")
+    outs = (*_codes(dgu, scale_inv_dgu, (rows, 2, n), (rows, 2, nb), "dgu"),
+            *_codes(dgu_t, scale_inv_dgu_t, (2, n, rows), (2, n, rb), "dgu_t"),
+            *_codes(h_t, scale_inv_h_t, (n, rows), (n, rb), "h_t"))
+    pd, pgu, psgu = _ptrs(dh, gu, scale_inv_gu)
+    _check(library().fp8_gated_block_backward(pd, _dt(dh), pgu, psgu, act, rows, n, fmt_grad, *outs, _stream(stream)))
 
 
 _GRAD_DTYPES = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}

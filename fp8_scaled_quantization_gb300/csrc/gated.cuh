@@ -1,0 +1,61 @@
+// gated.cuh -- the gated activation h = act(g) * u of a feed-forward block, its
+// derivative, and the E4M3 tiles that its kernels write.
+//
+//   act(g)  = g * s,  s = 1 / (1 + exp(-y))      SiLU: y = g
+//   act'(g) = s + act(g) * (1 - s) * y'          GELU (tanh form, 0.5 g (1 + tanh z) with
+//                                                z = c (g + 0.044715 g^3)): y = 2 z
+// Both are one sigmoid, so one exponential and one reciprocal per element.
+#pragma once
+
+#include "fp8q_device.cuh"
+
+namespace fp8q {
+
+constexpr int kSilu = FP8_ACT_SILU, kGeluTanh = FP8_ACT_GELU_TANH;
+
+// The hardware's approximations, two units in the last place each.  Their
+// argument is rounded up to four times (GELU's polynomial, the product with log2
+// e), so that exp(-y) is off by up to (|y| + 1) * 2^-22 of its value: far below
+// the FP8 step of what is written.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Constants and their products are rounded once.
+constexpr double kLog2E = 1.4426950408889634, kGeluTwoC = 1.5957691216057308 /* 2 sqrt(2 / pi) */, kGeluCube = 0.044715;
+// Beyond it the sigmoid of GELU is 0 or 1, and g^2 stays finite (0 * Inf would make a NaN of 0).
+constexpr float kGeluFar = 32.0f;
+
+// s(g), and y'(g) where DERIVATIVE (1 for SiLU).
+template <int ACT, bool DERIVATIVE>
+__device__ __forceinline__ float gate(float g, float* dy) {
+    float t;  // -y log2 e
+    if constexpr (ACT == kSilu) {
+        t = g * (float)-kLog2E;
+    } else {
+        const float c = fminf(fmaxf(g, -kGeluFar), kGeluFar), c2 = c * c;
+        t = c * __fmaf_rn(c2, (float)(-kLog2E * kGeluTwoC * kGeluCube), (float)(-kLog2E * kGeluTwoC));
+        if constexpr (DERIVATIVE) *dy = __fmaf_rn(c2, (float)(3.0 * kGeluTwoC * kGeluCube), (float)kGeluTwoC);
+    }
+    return rcp_approx(1.0f + exp2_approx(t));
+}
+
+template <int ACT>
+__device__ __forceinline__ float gated(float g, float u) {
+    return g * gate<ACT, false>(g, nullptr) * u;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The larger magnitude; a NaN in either is the result (bit patterns of
+// magnitudes order as the magnitudes do, with Inf and then NaN above them).
+__device__ __forceinline__ uint32_t max_abs(uint32_t m, float v) { return umax(m, abs_bits(v)); }
+
+}  // namespace fp8q

@@ -82,6 +82,8 @@ fp8_status_t check(const char* fn, const GemmProblem& p, int layout, int b_block
     return FP8_OK;
 }
 
+}  // namespace
+
 fp8_status_t check_groups(const char* fn, int groups, const int64_t* ends) {
     if (groups < 1 || groups > kMaxGroups)
         return fail(FP8_ERR_INVALID_ARG, "%s: groups must be in [1, %d]", fn, kMaxGroups);
@@ -90,8 +92,6 @@ fp8_status_t check_groups(const char* fn, int groups, const int64_t* ends) {
         return fail(FP8_ERR_INVALID_ARG, "%s: group_ends is not 8-byte aligned", fn);
     return FP8_OK;
 }
-
-}  // namespace
 
 fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, const Operand& b, CUtensorMap* map_b,
                           StreamUse& use, cudaStream_t st) {

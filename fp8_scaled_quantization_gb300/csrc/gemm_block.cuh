@@ -17,6 +17,15 @@ constexpr int kMaxGroups = 1024;   // groups of one grouped call
 // D[m, n] = sum over 128-blocks b of sa[m, b] * sb[n, b] * sum_k in b of
 // dec(A[m, k]) * dec(B[n, k]).  `ends` (device, `groups` entries) cuts the rows
 // of A (RAGGED_M) or the contraction (RAGGED_K) into groups; NULL: one group.
+// A gated problem has two matrices B per group, one after the other ([groups, 2,
+// n, k]: gate and up), and writes `gated` in place of d.
+struct GatedOut {
+    uint8_t* h;   // [m, n] E4M3 codes, and factors [m, blocks of n]
+    float* sh;
+    uint8_t* gu;  // nullable: [m, 2, n] and factors [m, 2, blocks of n]
+    float* sgu;
+    int act;
+};
 struct GemmProblem {
     const uint8_t* a;
     const uint8_t* b;
@@ -33,6 +42,7 @@ struct GemmProblem {
     bool b_tiles;    // 1 x 128 scale tiles of B instead of 128 x 128 blocks
     bool out_f32;
     bool accumulate; // D += (fp32 only)
+    GatedOut gated = {};
 };
 
 // One operand as stored: `groups` row-major [rows, inner] matrices of codes.
@@ -49,7 +59,10 @@ struct Operand {
 fp8_status_t operand_maps(const char* fn, const Operand& a, CUtensorMap* map_a, const Operand& b, CUtensorMap* map_b,
                           StreamUse& use, cudaStream_t st);
 
-// gemm_block_pair.cu: 256 x 256 outputs per CTA pair.
+// gemm_block.cu: the checks of a grouped call's groups.
+fp8_status_t check_groups(const char* fn, int groups, const int64_t* ends);
+
+// gemm_block_pair.cu: 256 x 256 outputs per CTA pair; gated: 256 x 128.
 fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st);
 
 // gemm_block_stream.cu: 128 columns of D per CTA and `tokens` (16, 32, 64 or 128)

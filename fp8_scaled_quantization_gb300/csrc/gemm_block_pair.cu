@@ -32,6 +32,7 @@
 // them with one another only.
 #include "fp8q_host.h"
 #include "fp8q_tcgen05.cuh"
+#include "gated.cuh"
 #include "gemm_block.cuh"
 
 namespace fp8q {
@@ -67,6 +68,7 @@ struct Shared {
     uint64_t tmem_full[2], tmem_empty[2];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
     uint32_t tmem, dead;
+    uint32_t peer[2][128];  // gated: per column half and row, the largest |h| (bits)
     int groups[2 * kMaxGroups + 3];
 };
 template <bool TILES>
@@ -86,7 +88,7 @@ struct Tile {
     int blk0, blks;     // its 128-blocks
 };
 
-template <bool RAGGED_K>
+template <bool RAGGED_K, int TILE_N = kPairN>
 __device__ __forceinline__ Tile locate(const GemmProblem& p, const GroupTable& g, int count, int tiles_n, int t) {
     Tile r;
     const int e = find_group(g, count, t);
@@ -99,7 +101,7 @@ __device__ __forceinline__ Tile locate(const GemmProblem& p, const GroupTable& g
     r.group = e;
     r.row0 = (RAGGED_K ? 0 : begin) + (strip * kRaster + in_strip % high) * kPairM;
     r.row_end = RAGGED_K ? m : end;
-    r.col0 = in_strip / high * kPairN;
+    r.col0 = in_strip / high * TILE_N;
     r.k_lo = RAGGED_K ? begin : 0;
     r.k_hi = RAGGED_K ? end : (e < p.groups ? k : 0);
     // an empty contraction has no blocks, wherever it lies
@@ -343,13 +345,155 @@ __device__ __forceinline__ void store_tile(const GemmProblem& p, const CUtensorM
     }
 }
 
+// ---- the gated form: 256 rows x 128 columns of h per pair.  The pair's 256
+// columns of B are the 128 of the gate and the 128 of the up projection that
+// belong to them, so warps w and w + 4 hold both of the same 32 rows, a row per
+// lane: what a 1 x 128 tile's scale needs lies in one lane (the projections) or two
+// (h).  Each of the two warps passes half of its columns to the other through the
+// staging buffers and computes h for 64 columns.
+
+// `WORDS` words of E4M3 codes (v * scale, four per word) of a lane's row to the
+// warp's staging buffer, whose rows are 4 * WORDS bytes.
+template <int WORDS>
+__device__ __forceinline__ uint32_t staged(uint32_t stage, int row, int piece) {
+    const int swizzle = WORDS == 32 ? row & 7 : row >> 1 & 3;  // 16-byte pieces: rows spread over the banks
+    return stage + row * (WORDS * 4) + ((piece ^ swizzle) << 4);
+}
+template <int WORDS>
+__device__ __forceinline__ void stage_codes(const float* v, float scale, uint32_t stage, int lane) {
+#pragma unroll
+    for (int j = 0; j < WORDS / 4; ++j) {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float* const x = v + j * 16 + i * 4;
+            const float2 lo = fmul2_rn(x[0], x[1], scale), hi = fmul2_rn(x[2], x[3], scale);
+            c[i] = cvt4<kE4M3>(lo.x, lo.y, hi.x, hi.y);
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(staged<WORDS>(stage, lane, j)), "r"(c[0]), "r"(c[1]),
+                     "r"(c[2]), "r"(c[3])
+                     : "memory");
+    }
+}
+
+// The staged rows (rows of them, `to` columns that are there) to `out` by plain stores;
+// wide: 16-byte aligned rows whose end is too.
+template <int WORDS>
+__device__ __forceinline__ void copy_codes(uint8_t* out, int64_t pitch, uint32_t stage, int lane, int rows, int to, bool wide) {
+    if (to <= 0) return;
+    if (wide) {
+        constexpr int kPieces = WORDS / 4, kAtOnce = 32 / kPieces;  // lanes per row, rows per step
+        const int piece = lane % kPieces;
+        if (piece * 16 >= to) return;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
+            const int r = r0 + lane / kPieces;
+            uint32_t v[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(staged<WORDS>(stage, r, piece))
+                         : "memory");
+            if (r < rows) *reinterpret_cast<uint4*>(out + r * pitch + piece * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    } else {  // bytes, a row per step
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r) {
+#pragma unroll
+            for (int x = lane; x < WORDS * 4; x += 32) {
+                uint32_t v;
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(staged<WORDS>(stage, r, x >> 4) + (x & 15)) : "memory");
+                if (x < to) out[r * pitch + x] = (uint8_t)v;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ float tile_scale(uint32_t amax_bits, float* factor) {
+    float s;
+    scale_from_amax<kE4M3>(__uint_as_float(amax_bits), 0, &s, factor);
+    return s;
+}
+
+// h for the 64 columns that this lane keeps (the first of a gate warp, the last of an up
+// warp), into its sums; the other warp's half of them at `theirs`.  Their largest |h|.
+template <int ACT, int HALF>
+__device__ __forceinline__ uint32_t gate_columns(float* v, uint32_t theirs, int lane) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float o[4];
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
+                     : "r"(theirs + j * 512 + lane * 16)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float& x = v[HALF * 64 + j * 4 + i];
+            x = HALF == 0 ? gated<ACT>(x, o[i]) : gated<ACT>(o[i], x);
+            most = max_abs(most, x);
+        }
+    }
+    return most;
+}
+
+// A warp's part of a gated tile: rows row0 .. (at most 32, before row_end), columns col0 ..
+// of h; HALF 0: acc holds the gate's sums, 1: the up projection's.
+template <int HALF>
+__device__ __forceinline__ void store_gated(const GemmProblem& p, Sums<false>& acc, uint32_t (&peer)[2][128], uint32_t stages,
+                                            int warp, int lane, int64_t row0, int64_t row_end, int col0) {
+    const GatedOut& out = p.gated;
+    const uint32_t mine = stages + warp * kOuts * kOutBytes, theirs = stages + (warp ^ 4) * kOuts * kOutBytes;
+    const int rows = (int)(row_end - row0 < 32 ? row_end - row0 : 32), quarter = warp & 3;  // (rows may be negative)
+    const int there = (int)(p.n - col0 < 128 ? p.n - col0 : 128);
+    const int64_t nb = blocks_of(p.n), row = row0 + lane;
+    if (there < 128) {  // columns that are not there count for no maximum
+#pragma unroll
+        for (int i = 0; i < 128; ++i) acc.v[i] = i < there ? acc.v[i] : 0.0f;
+    }
+    if (out.gu != nullptr) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) most = max_abs(most, acc.v[i]);
+        float factor;
+        const float scale = tile_scale(most, &factor);
+        stage_codes<32>(acc.v, scale, mine, lane);
+        if (lane < rows) out.sgu[(row * 2 + HALF) * nb + col0 / kBlk] = factor;
+        __syncwarp();
+        copy_codes<32>(out.gu + (row0 * 2 + HALF) * p.n + col0, 2 * p.n, mine, lane, rows, there,
+                       p.n % 16 == 0 && aligned_to_16(out.gu));
+        __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float* const x = acc.v + (1 - HALF) * 64 + j * 4;
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + j * 512 + lane * 16), "f"(x[0]), "f"(x[1]),
+                     "f"(x[2]), "f"(x[3])
+                     : "memory");
+    }
+    group_sync(1 + quarter, 64);
+    uint32_t most = out.act == kSilu ? gate_columns<kSilu, HALF>(acc.v, theirs, lane)
+                                     : gate_columns<kGeluTanh, HALF>(acc.v, theirs, lane);
+    peer[HALF][quarter * 32 + lane] = most;
+    group_sync(1 + quarter, 64);  // (and the other warp has read this one's columns)
+    most = umax(most, peer[1 - HALF][quarter * 32 + lane]);
+    float factor;
+    const float scale = tile_scale(most, &factor);
+    if (HALF == 0 && lane < rows) out.sh[row * nb + col0 / kBlk] = factor;
+    stage_codes<16>(acc.v + HALF * 64, scale, mine, lane);
+    __syncwarp();
+    copy_codes<16>(out.h + row0 * p.n + col0 + HALF * 64, p.n, mine, lane, rows, there - HALF * 64,
+                   p.n % 16 == 0 && aligned_to_16(out.h));
+    __syncwarp();
+}
+
 // FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: both
-// operands in 1 x 128 tiles, contraction ragged.
+// operands in 1 x 128 tiles, contraction ragged; 3: gated, two B [n, k] per group.
 template <int FORM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ CUtensorMap map_a,
                  const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d, bool bulk_store) {
-    constexpr bool RAGGED_K = FORM == 2, B_KN = FORM == 1, B_TILES = FORM == 2;
+    constexpr bool RAGGED_K = FORM == 2, B_KN = FORM == 1, B_TILES = FORM == 2, GATED = FORM == 3;
+    constexpr int kTileN = GATED ? kPairN / 2 : kPairN;  // columns of the output
     extern __shared__ uint8_t raw[];
     uint8_t* const tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* const out = tiles + kStages * kStageBytes;
@@ -380,7 +524,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
         prefetch_map(&map_b);
     }
     pdl_begin();
-    const int tiles_n = (int)((p.n + kPairN - 1) / kPairN);
+    const int tiles_n = (int)((p.n + kTileN - 1) / kTileN);
     const int count = RAGGED_K ? p.groups : p.groups + 1;
     const GroupTable groups(sh.groups, p.groups);
     const int total = build_groups(groups, p.ends, p.groups, RAGGED_K ? p.k : p.m, kPairM, RAGGED_K ? p.m : 0, tiles_n);
@@ -488,8 +632,13 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             const int matrix = RAGGED_K ? sh.matrix[at_place] : 0;
             at_place = (at_place + 1) % kPlaces;
             const int64_t r0 = place.x + (int)rank * 128 + (warp & 3) * 32, c0 = place.z + half * 128;
-            store_tile<B_TILES>(p, &map_d, bulk_store, acc, smem_addr(out) + warp * kOuts * kOutBytes, lane, r0, place.y, c0,
-                                matrix);
+            if constexpr (GATED) {
+                if (half == 0) store_gated<0>(p, acc, sh.peer, smem_addr(out), warp, lane, r0, place.y, place.z);
+                else store_gated<1>(p, acc, sh.peer, smem_addr(out), warp, lane, r0, place.y, place.z);
+            } else {
+                store_tile<B_TILES>(p, &map_d, bulk_store, acc, smem_addr(out) + warp * kOuts * kOutBytes, lane, r0, place.y,
+                                    c0, matrix);
+            }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
@@ -502,7 +651,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                 const uint64_t a0 = tile_desc(smem_addr(tiles)), b0 = tile_desc(smem_addr(tiles) + kTileBytes);
                 uint32_t it = 0, stage = 0, phase = 0;
                 for (int t = first; t < total; t += step) {
-                    const int blks = locate<RAGGED_K>(p, groups, count, tiles_n, t).blks;
+                    const int blks = locate<RAGGED_K, kTileN>(p, groups, count, tiles_n, t).blks;
                     for (int b = 0; b < blks; ++b) {
                         const uint64_t at = a0 + stage * (kStageBytes >> 4), bt = b0 + stage * (kStageBytes >> 4);
                         const uint32_t buf = it & 1;
@@ -537,7 +686,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             const bool wide_b = kb % kScaleBlocks == 0 && (reinterpret_cast<uintptr_t>(p.sb) & 15u) == 0;
             uint32_t group = 0, at_place = 0;
             for (int t = first; t < total; t += step) {
-                const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
+                const Tile tile = locate<RAGGED_K, kTileN>(p, groups, count, tiles_n, t);
                 for (int done = 0; done == 0 || done < tile.blks; done += kScaleBlocks, ++group) {  // (once without blocks, too)
                     const int g0 = tile.blk0 + done, to = min(tile.blks - done, kScaleBlocks);
                     const bool whole = to > 0 && g0 % kScaleBlocks == 0;  // an aligned piece of a row of scales
@@ -575,9 +724,10 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                             }
                         }
                     } else {
-                        // lanes 4h + j load the scale of block g0 + j, column block h
-                        const int64_t n = tile.col0 / kBlk + ((lane >> 2) & 1), cb = n < nb ? n : nb - 1;
-                        const float* sb = p.sb + (int64_t)tile.group * kb * nb;
+                        // lanes 4h + j load the scale of block g0 + j, column block h (gated: of matrix h)
+                        const int h2 = (lane >> 2) & 1;
+                        const int64_t n = tile.col0 / kBlk + (GATED ? 0 : h2), cb = n < nb ? n : nb - 1;
+                        const float* sb = p.sb + (GATED ? 2 * (int64_t)tile.group + h2 : (int64_t)tile.group) * kb * nb;
                         const int j = lane & 3;
                         float c = 0.0f;
                         if (j < to) c = __ldg(sb + (B_KN ? (int64_t)(g0 + j) * nb + cb : cb * kb + g0 + j));
@@ -607,7 +757,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             const uint32_t base = smem_addr(tiles), full0 = cluster_addr(smem_addr(&sh.full[0]), 0);
             uint32_t it = 0, stage = 0, phase = 0;
             for (int t = first; t < total; t += step) {
-                const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
+                const Tile tile = locate<RAGGED_K, kTileN>(p, groups, count, tiles_n, t);
                 const int row = tile.row0 + (int)rank * 128, col = tile.col0 + (int)rank * 128;
                 for (int b = 0; b < tile.blks; ++b, ++it) {
                     const uint32_t a = base + stage * kStageBytes, bt = a + kTileBytes;
@@ -620,7 +770,8 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
                         if (RAGGED_K && is_cut(tile, x, (int)p.k)) bar = smem_addr(&sh.landed[stage]);
                         cluster_arrive_expect_tx(bar, kStageBytes);
                         tma_tile<true>(a, &map_a, x, row, 0, bar);
-                        if constexpr (B_KN) tma_tile<true>(bt, &map_b, col, x, tile.group, bar);
+                        if constexpr (GATED) tma_tile<true>(bt, &map_b, x, tile.col0, 2 * tile.group + (int)rank, bar);
+                        else if constexpr (B_KN) tma_tile<true>(bt, &map_b, col, x, tile.group, bar);
                         else tma_tile<true>(bt, &map_b, x, col, RAGGED_K ? 0 : tile.group, bar);
                     }
                     __syncwarp();
@@ -639,7 +790,7 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             uint32_t stage = 0, phases = 0;  // bit s: the phase of landed[s]
             uint32_t passed = 0;             // blocks and tiles since this warp last waited
             for (int t = first; t < total; t += step, ++passed) {
-                const Tile tile = locate<RAGGED_K>(p, groups, count, tiles_n, t);
+                const Tile tile = locate<RAGGED_K, kTileN>(p, groups, count, tiles_n, t);
                 for (int b = 0; b < tile.blks; ++b, ++passed) {
                     const int x = (tile.blk0 + b) * kBlk;
                     if (is_cut(tile, x, (int)p.k)) {
@@ -679,21 +830,24 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
 
 fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st) {
     const int64_t inner_b = p.b_kn ? p.n : p.k, rows_b = p.b_kn ? p.k : p.n;
-    const bool bulk = aligned16(p.d) && p.n % (p.out_f32 ? 4 : 8) == 0 && !p.accumulate;
-    const Operand oa = {p.a, p.k, p.m, 1, 128}, ob = {p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups, 128};
+    const bool gated = p.gated.h != nullptr;
+    const bool bulk = !gated && aligned16(p.d) && p.n % (p.out_f32 ? 4 : 8) == 0 && !p.accumulate;
+    const Operand oa = {p.a, p.k, p.m, 1, 128}, ob = {p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups * (gated ? 2 : 1), 128};
     CUtensorMap a = {}, b = {}, d = {};
     StreamUse use(st);
     fp8_status_t s = FP8_OK;
     if (p.k > 0) s = operand_maps(fn, oa, &a, ob, &b, use, st);
     if (bulk && s == FP8_OK) s = encode_out_map(&d, p.d, p.out_f32, p.n, p.m, p.b_tiles ? p.groups : 1);
     if (s != FP8_OK) return s;
-    const int64_t tiles_n = (p.n + kPairN - 1) / kPairN, tiles_m = (p.m + kPairM - 1) / kPairM;
+    const int64_t tile_n = gated ? kPairN / 2 : kPairN;
+    const int64_t tiles_n = (p.n + tile_n - 1) / tile_n, tiles_m = (p.m + kPairM - 1) / kPairM;
     const int64_t most = p.b_tiles ? tiles_m * tiles_n * p.groups : (tiles_m + p.groups - 1) * tiles_n;
     const int sms = sm_count() / 2, pairs = (int)(most < sms ? most : sms);
     const auto go = [&](auto kernel, size_t smem) {
         return launch_smem(fn, kernel, dim3(2 * pairs), dim3(kThreads), smem, st, p, a, b, d, bulk);
     };
-    return p.b_tiles ? go(gemm_pair_kernel<2>, smem_bytes<true>())
+    return gated     ? go(gemm_pair_kernel<3>, smem_bytes<false>())
+           : p.b_tiles ? go(gemm_pair_kernel<2>, smem_bytes<true>())
            : p.b_kn  ? go(gemm_pair_kernel<1>, smem_bytes<false>())
                      : go(gemm_pair_kernel<0>, smem_bytes<false>());
 }

@@ -1,0 +1,74 @@
+// gemm_gated.cu -- the gated feed-forward block's first half in block-scaled FP8:
+// both projections, the activation, their product and its 1 x 128 quantization in
+// one kernel.  The C entry points, their checks and the choice of kernel.
+//
+// "Megatron FP8" §6 (forward products over FP8 operands), §21 (experts); "Low
+// Precision Training and Rollout" (128 x 128 weight blocks).
+//
+// Unfused, the projections come out as BF16 (4 bytes per element of h), the
+// activation reads them and writes h, and the cast reads that and writes codes: 9
+// bytes an element and two launches more, where 1 byte (with the checkpoint 3)
+// leaves this kernel.
+#include "fp8q_host.h"
+#include "gemm_block.cuh"
+
+namespace fp8q {
+namespace {
+
+fp8_status_t check(const char* fn, const GemmProblem& p) {
+    const GatedOut& o = p.gated;
+    if (!valid_fmt(p.fmt_a) || !valid_fmt(p.fmt_b)) return fail(FP8_ERR_INVALID_ARG, "%s: unknown format", fn);
+    if (o.act != FP8_ACT_SILU && o.act != FP8_ACT_GELU_TANH)
+        return fail(FP8_ERR_INVALID_ARG, "%s: unknown activation %d", fn, o.act);
+    if (p.m < 0 || p.n < 0 || p.k < 0) return fail(FP8_ERR_INVALID_ARG, "%s: negative size", fn);
+    constexpr int64_t kMost = (1ll << 31) - 256, kMostTiles = 1ll << 30;
+    if (p.m > kMost || p.n > kMost || p.k > kMost)
+        return fail(FP8_ERR_UNSUPPORTED, "%s: sizes must be below 2^31 - 256", fn);
+    // tiles are numbered with 32 bits: at least 16 x 128, one more along m for each group
+    if (((p.m + 15) / 16 + p.groups) * ((p.n + 127) / 128) > kMostTiles)
+        return fail(FP8_ERR_UNSUPPORTED, "%s: too many output tiles", fn);
+    if ((o.gu == nullptr) != (o.sgu == nullptr))
+        return fail(FP8_ERR_INVALID_ARG, "%s: the checkpoint needs both its codes and its scales", fn);
+    if (p.m == 0 || p.n == 0) return FP8_OK;
+    if (o.h == nullptr || o.sh == nullptr) return fail(FP8_ERR_INVALID_ARG, "%s: h or its scales are NULL", fn);
+    if (p.k > 0 && (p.a == nullptr || p.b == nullptr || p.sa == nullptr || p.sb == nullptr))
+        return fail(FP8_ERR_INVALID_ARG, "%s: an operand or its scales are NULL", fn);
+    for (const float* s : {p.k > 0 ? p.sa : nullptr, p.k > 0 ? p.sb : nullptr, (const float*)o.sh, (const float*)o.sgu})
+        if ((reinterpret_cast<uintptr_t>(s) & 3u) != 0)
+            return fail(FP8_ERR_INVALID_ARG, "%s: scales are not 4-byte aligned", fn);
+    return FP8_OK;
+}
+
+fp8_status_t run(const char* fn, const GemmProblem& p, cudaStream_t st) { return run_gemm_pair(fn, p, st); }
+
+}  // namespace
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" fp8_status_t fp8_gemm_block_gated(const uint8_t* a, fp8_format_t fmt_a, const float* scale_inv_a,
+                                             const uint8_t* b, fp8_format_t fmt_b, const float* scale_inv_b,
+                                             fp8_activation_t act, int64_t m, int64_t n, int64_t k, uint8_t* h,
+                                             float* scale_inv_h, uint8_t* gu, float* scale_inv_gu, void* stream) {
+    const char* fn = "fp8_gemm_block_gated";
+    const GemmProblem p = {a, b, scale_inv_a, scale_inv_b, nullptr, nullptr, m, n, k, 1, (int)fmt_a, (int)fmt_b,
+                           false, false, false, false, {h, scale_inv_h, gu, scale_inv_gu, (int)act}};
+    const fp8_status_t s = check(fn, p);
+    if (s != FP8_OK || m == 0 || n == 0) return s;
+    return run(fn, p, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" fp8_status_t fp8_gemm_block_gated_grouped(int groups, const int64_t* group_ends, const uint8_t* a,
+                                                     fp8_format_t fmt_a, const float* scale_inv_a, const uint8_t* b,
+                                                     fp8_format_t fmt_b, const float* scale_inv_b, fp8_activation_t act,
+                                                     int64_t rows, int64_t n, int64_t k, uint8_t* h, float* scale_inv_h,
+                                                     uint8_t* gu, float* scale_inv_gu, void* stream) {
+    const char* fn = "fp8_gemm_block_gated_grouped";
+    fp8_status_t s = check_groups(fn, groups, group_ends);
+    if (s != FP8_OK) return s;
+    const GemmProblem p = {a, b, scale_inv_a, scale_inv_b, nullptr, group_ends, rows, n, k, groups, (int)fmt_a, (int)fmt_b,
+                           false, false, false, false, {h, scale_inv_h, gu, scale_inv_gu, (int)act}};
+    s = check(fn, p);
+    if (s != FP8_OK || rows == 0 || n == 0) return s;
+    return run(fn, p, static_cast<cudaStream_t>(stream));
+}

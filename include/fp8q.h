@@ -102,6 +102,11 @@ typedef enum {
     FP8_B_KN = 1  /* [k, n]: a weight read the other way round   */
 } fp8_b_layout_t;
 
+/* Activation of a gated feed-forward block.  Both are g * sigmoid(y): SiLU with
+ * y = g; GELU in its tanh form, 0.5 g (1 + tanh(z)) with z = sqrt(2/pi) (g +
+ * 0.044715 g^3), with y = 2 z. */
+typedef enum { FP8_ACT_SILU = 0, FP8_ACT_GELU_TANH = 1 } fp8_activation_t;
+
 typedef enum {
     FP8_OK = 0,
     FP8_ERR_INVALID_ARG = 1, /* NULL pointer, negative size, bad enum or margin */
@@ -550,6 +555,85 @@ fp8_status_t fp8_gemm_block_grouped_wgrad(int groups, const int64_t* group_ends,
                                           const float* scale_inv_a, const uint8_t* b, fp8_format_t fmt_b,
                                           const float* scale_inv_b, int64_t m, int64_t n, int64_t rows, void* d,
                                           fp8_dtype_t out_dtype, int accumulate, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The gated feed-forward block                                              */
+/* ------------------------------------------------------------------------ */
+/* The first half of a block y = (act(X Wg^T) * (X Wu^T)) Wd^T in one call: both
+ * projections, the activation, their product, and its cast to what the down
+ * projection's product takes ("Megatron FP8" §6; "Low Precision Training and
+ * Rollout": 128 x 128 weight blocks).  With g = X Wg^T and u = X Wu^T as
+ * fp8_gemm_block sums them (fp32, not rounded to BF16),
+ *   h[i, j] = act(g[i, j]) * u[i, j]   in fp32,
+ * quantized in 1 x 128 tiles to E4M3 by the rule of fp8_quantize_block(1, 128).
+ * The exponential and the reciprocal of the activation are the hardware's: h is
+ * off by up to (|y| + 8) * 2^-22 of its value, and an act(g) below 1e-36 in
+ * magnitude may become 0.  (g = -Inf gives NaN, as Inf * 0 does.)
+ *
+ *   a, scale_inv_a   device uint8[m, k] and float[m, ceil(k/128)], 1 x 128 tiles.
+ *   b, scale_inv_b   device uint8[2, n, k] and float[2, ceil(n/128),
+ *                    ceil(k/128)]: the gate's weight, then the up projection's,
+ *                    each with 128 x 128 blocks of its own.  With n % 128 == 0
+ *                    both together are also one [2 n, k] operand.
+ *   h, scale_inv_h   device uint8[m, n] and float[m, ceil(n/128)].
+ *   gu, scale_inv_gu the checkpoint, both or neither NULL: device uint8[m, 2, n]
+ *                    and float[m, 2, ceil(n/128)], E4M3 codes of g and u in 1 x
+ *                    128 tiles: what fp8_gated_block_backward reads, a quarter
+ *                    of the bytes of g and u in BF16 and of h beside them.  h is
+ *                    computed from g and u before they are rounded.
+ *   Sizes            m, n, k >= 0, each below 2^31 - 256; k == 0 gives g = u = 0,
+ *                    and zeros have codes 0 and factor 1.
+ *   Alignment        of a and b as for fp8_gemm_block (odd rows are copied).
+ *                    Outputs may start anywhere; n % 16 == 0 and 16-byte aligned
+ *                    codes are written faster.
+ * An output must not overlap another or an input.  Results do not depend on the
+ * stream, on other calls or on earlier ones.  One launch, plus one per operand
+ * that is copied; the kernels' waits are bounded and counted by fp8_wait_timeouts. */
+fp8_status_t fp8_gemm_block_gated(const uint8_t* a, fp8_format_t fmt_a, const float* scale_inv_a, const uint8_t* b,
+                                  fp8_format_t fmt_b, const float* scale_inv_b, fp8_activation_t act, int64_t m,
+                                  int64_t n, int64_t k, uint8_t* h, float* scale_inv_h, uint8_t* gu,
+                                  float* scale_inv_gu, void* stream);
+
+/* The same per expert over rows sorted by expert ("Megatron FP8" §21); groups and
+ * group_ends as for fp8_gemm_block_grouped, b [groups, 2, n, k] and scale_inv_b
+ * [groups, 2, ceil(n/128), ceil(k/128)].  Rows after the last group's end get
+ * codes 0 and factors 1, in h and in the checkpoint. */
+fp8_status_t fp8_gemm_block_gated_grouped(int groups, const int64_t* group_ends, const uint8_t* a, fp8_format_t fmt_a,
+                                          const float* scale_inv_a, const uint8_t* b, fp8_format_t fmt_b,
+                                          const float* scale_inv_b, fp8_activation_t act, int64_t rows, int64_t n,
+                                          int64_t k, uint8_t* h, float* scale_inv_h, uint8_t* gu, float* scale_inv_gu,
+                                          void* stream);
+
+/* The backward pass of the activation from that checkpoint.  With g, u the values
+ * that the checkpoint's codes stand for (code * factor) and dh the gradient of h,
+ * in fp32,
+ *   dg = dh * u * act'(g),   du = dh * act(g),   h = act(g) * u,
+ * each quantized in 1 x 128 tiles from fp32 by the rule of fp8_quantize_block(1,
+ * 128): dg and du to fmt_grad along their rows (for the input gradient) and
+ * transposed (tiles along the rows of dh; for the weights' gradients), h to E4M3
+ * transposed (for the down projection's weight gradient).  Precision of act and
+ * act' as above (act' to (|y| + 8) * 2^-22, absolute).
+ *
+ *   dh               device [rows, n] of dtype (BF16 or fp32), element-aligned.
+ *   gu, scale_inv_gu device uint8[rows, 2, n] and float[rows, 2, ceil(n/128)], E4M3.
+ *   dgu, scale_inv_dgu      uint8[rows, 2, n] and float[rows, 2, ceil(n/128)];
+ *                    with n % 128 == 0 also one [rows, 2 n] operand: of
+ *                    fp8_gemm_block with b as the [2 n, k] weight and FP8_B_KN.
+ *   dgu_t, scale_inv_dgu_t  uint8[2, n, rows] and float[2, n, ceil(rows/128)],
+ *                    also one [2 n, rows] operand (of fp8_gemm_block with
+ *                    b_block_rows 1, or fp8_gemm_block_grouped_wgrad).
+ *   h_t, scale_inv_h_t      uint8[n, rows] and float[n, ceil(rows/128)].
+ *                    Each pair of outputs may be NULL, not all three.
+ *   Sizes            rows, n >= 0, each below 2^31 - 256.
+ * The scale tiles along the rows sit at multiples of 128 of the buffer, which is
+ * what the grouped weight gradient expects of rows sorted by expert.  A tile that
+ * holds Inf or NaN gets factor 1 and codes by the element rule.  Codes and dh that
+ * are aligned to 16 bytes, with n % 16 == 0 and rows % 16 == 0, are read and
+ * written faster.  An output must not overlap another or an input.  One launch. */
+fp8_status_t fp8_gated_block_backward(const void* dh, fp8_dtype_t dtype, const uint8_t* gu, const float* scale_inv_gu,
+                                      fp8_activation_t act, int64_t rows, int64_t n, fp8_format_t fmt_grad,
+                                      uint8_t* dgu, float* scale_inv_dgu, uint8_t* dgu_t, float* scale_inv_dgu_t,
+                                      uint8_t* h_t, float* scale_inv_h_t, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Global gradient norm and clipping                                         */
