@@ -9,14 +9,17 @@
 // gradient's), h transposed only (the down projection's weight gradient): 9 bytes
 // an element with a BF16 dh, each read or written once.
 //
-// One CTA of 16 warps per 128 x 128 tile at a time.  A warp has 8 whole rows and
-// a lane 4 columns of them, so that a row's maximum is one warp reduction, a
-// word of row codes is a lane's 4 columns, and a word of transposed codes a
-// lane's 4 rows: no byte is moved between lanes to transpose.  Column maxima go
-// through shared memory, and so do the transposed codes, to be written 16 bytes
-// per lane.
+// One CTA of 16 warps per SM takes 128 x 128 tiles, one after another.  A warp has
+// 8 whole rows and a lane 4 columns of them, so that a row's maximum is one warp
+// reduction, a word of row codes is a lane's 4 columns, and a word of transposed
+// codes a lane's 4 rows: no byte is moved between lanes to transpose.  All 96
+// values of a lane stay in registers until both scales are known.  Column maxima
+// go through shared memory, and so do the transposed codes, to be written 16 bytes
+// per lane.  The next tile's inputs are copied into shared memory meanwhile.
+#include <type_traits>
+
 #include "fp8q_host.h"
-#include "fp8q_pipeline.cuh"
+#include "fp8q_tcgen05.cuh"
 #include "gated.cuh"
 
 namespace fp8q {
@@ -36,16 +39,90 @@ struct Backward {
     float* sdgu_t;
     uint8_t* h_t;        // [n, rows] E4M3, factors [n, blocks of rows]; nullable
     float* sh_t;
-    bool words_in;       // 4 columns of dh and gu load as aligned words
-    bool words_out;      // and store to dgu
+    int copy_in;         // columns of dh and gu that one asynchronous copy takes: 16, 4 (aligned to that) or 0
+    bool words_out;      // 4 columns store to dgu as an aligned word
     bool pieces_t;       // transposed rows are multiples of 16 bytes, 16-byte aligned
 };
 
+template <bool F32>
+struct Stage {  // a tile's inputs; rows and columns that are not there are zeros
+    using Grad = typename std::conditional<F32, float, uint16_t>::type;
+    alignas(16) Grad dh[kTile][kTile];
+    alignas(16) uint8_t gu[2][kTile][kTile];
+    float factor[kTile][2];
+};
+
+template <bool F32>
 struct Smem {
-    uint32_t most[3][kWarps][kTile];       // column maxima of each warp's rows: dg, du, h
-    float scale[3][kTile];
+    static constexpr int kStages = F32 ? 1 : 2;  // (two of fp32 do not fit)
+    Stage<F32> stage[kStages];
+    alignas(16) float most[3][kWarps][kTile];     // column maxima of each warp's rows: dg, du, h
+    alignas(16) float scale[3][kTile];
     alignas(16) uint8_t codes[3][kTile * kTile];  // transposed codes, 8-byte pieces swizzled
 };
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool there) {
+    const int size = there ? BYTES : 0;  // the rest is filled with zeros
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(size) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src), "n"(BYTES), "r"(size)
+                     : "memory");
+}
+
+// Copies of a tile's inputs, COLUMNS of them at a time, which lie inside or outside the
+// array as a whole.
+template <int COLUMNS, bool F32>
+__device__ __forceinline__ void load_pieces(const Backward& p, Stage<F32>& s, int64_t r0, int64_t c0) {
+    constexpr int kPieces = kTile / COLUMNS, kBytes = COLUMNS * (F32 ? 4 : 2);
+    const int x = threadIdx.x % kPieces * COLUMNS;
+    const int64_t c = c0 + x;
+#pragma unroll
+    for (int y = threadIdx.x / kPieces; y < kTile; y += kThreads / kPieces) {
+        const int64_t r = r0 + y;
+        const bool there = r < p.rows && c < p.n;
+        const int64_t at = there ? r * p.n + c : 0;
+        const char* const d = static_cast<const char*>(p.dh) + at * (F32 ? 4 : 2);
+#pragma unroll
+        for (int b = 0; b < kBytes; b += 16)
+            copy_async<(kBytes < 16 ? kBytes : 16)>(reinterpret_cast<char*>(&s.dh[y][x]) + b, d + (there ? b : 0), there);
+        const uint8_t* const g = p.gu + (there ? at + r * p.n : 0);
+        copy_async<COLUMNS>(&s.gu[0][y][x], g, there);
+        copy_async<COLUMNS>(&s.gu[1][y][x], g + (there ? p.n : 0), there);
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int tr, int tc, int nb) {
+    const int64_t r0 = (int64_t)tr * kTile, c0 = (int64_t)tc * kTile;
+    if (p.copy_in == 16) {
+        load_pieces<16>(p, s, r0, c0);
+    } else if (p.copy_in == 4) {
+        load_pieces<4>(p, s, r0, c0);
+    } else {
+        const int x = threadIdx.x % kTile;
+        for (int y = threadIdx.x / kTile; y < kTile; y += kThreads / kTile) {
+            const bool there = r0 + y < p.rows && c0 + x < p.n;
+            const int64_t at = (r0 + y) * p.n + c0 + x;
+            s.dh[y][x] = there ? __ldg(static_cast<const typename Stage<F32>::Grad*>(p.dh) + at) : 0;
+            s.gu[0][y][x] = there ? __ldg(p.gu + at + (r0 + y) * p.n) : 0;
+            s.gu[1][y][x] = there ? __ldg(p.gu + at + (r0 + y + 1) * p.n) : 0;
+        }
+    }
+    if (threadIdx.x < 2 * kTile) {
+        const int64_t r = r0 + (threadIdx.x >> 1);
+        const bool there = r < p.rows;
+        copy_async<4>(&s.factor[threadIdx.x >> 1][threadIdx.x & 1], p.sgu + (there ? (2 * r + (threadIdx.x & 1)) * nb + tc : 0), there);
+    }
+}
+
+// max(m, |a|, |b|), a NaN if any of them is one.
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
 
 // Four codes of values whose tile holds Inf or NaN (scale 1), each by its own rule.
 template <int FMT>
@@ -67,63 +144,73 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 // lane, so that a warp's stores (column 4 lane + j) and the copy's reads spread over the banks.
 __device__ __forceinline__ uint32_t piece_at(int col, int piece) { return col * kTile + ((piece ^ (col >> 2 & 15)) << 3); }
 
+// Two columns at once, as packed pairs (fma.rn.f32x2 and its like).
+template <int ACT>
+__device__ __forceinline__ void differentiate(uint64_t d, uint64_t g, uint64_t u, uint64_t* dg, uint64_t* du, uint64_t* h) {
+    const float2 gv = unpack2(g);
+    float dy[2] = {1.0f, 1.0f};
+    const uint64_t s = pack2(gate<ACT, true>(gv.x, &dy[0]), gate<ACT, true>(gv.y, &dy[1]));
+    const uint64_t a = mul2(g, s), one = pack2(1.0f, 1.0f), rest = fma2(s, pack2(-1.0f, -1.0f), one);
+    const uint64_t slope = fma2(ACT == kSilu ? a : mul2(a, pack2(dy[0], dy[1])), rest, s);
+    *dg = mul2(mul2(d, u), slope);
+    *du = mul2(d, a);
+    *h = mul2(a, u);
+}
+
 template <int FMT, int ACT, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __grid_constant__ Backward p) {
     extern __shared__ __align__(128) uint8_t raw[];
-    Smem& sm = *reinterpret_cast<Smem*>(raw);
+    Smem<F32>& sm = *reinterpret_cast<Smem<F32>*>(raw);
+    constexpr int kStages = Smem<F32>::kStages;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nb = (int)((p.n + kTile - 1) / kTile), rb = (int)((p.rows + kTile - 1) / kTile);
+    const int total = nb * rb;
     pdl_begin();
-    for (int64_t t = blockIdx.x; t < (int64_t)nb * rb; t += gridDim.x) {
-        const int tr = (int)(t / nb), tc = (int)(t % nb);
+    const auto load = [&](int t, int stage) {
+        if (t < total) load_tile<F32>(p, sm.stage[stage], t / nb, t % nb, nb);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load(blockIdx.x, 0);
+    int at = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        const int tr = t / nb, tc = t % nb;
         const int64_t r0 = (int64_t)tr * kTile + warp * kRows, c0 = (int64_t)tc * kTile + lane * 4;
         const int cols = (int)(p.n - c0 < 4 ? p.n - c0 : 4);  // of this lane
+        const Stage<F32>& st = sm.stage[at];
+        // this tile's inputs have landed; with two stages, the other one was left by all before the last tile's columns
+        if (kStages == 2) {
+            load(t + gridDim.x, at ^ 1);
+            at ^= 1;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncthreads();  // (and the codes of the last tile have been read)
         float dg[kRows][4], du[kRows][4], h[kRows][4];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const int64_t r = r0 + i;
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            uint32_t gq = 0, uq = 0;
-            float sg = 0.0f, su = 0.0f;
-            if (r < p.rows && cols > 0) {
-                const uint8_t* const g = p.gu + 2 * r * p.n + c0;
-                const int64_t at = r * p.n + c0;
-                if (p.words_in) {
-                    gq = __ldg(reinterpret_cast<const uint32_t*>(g));
-                    uq = __ldg(reinterpret_cast<const uint32_t*>(g + p.n));
-                    if constexpr (F32) {
-                        const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.dh) + at));
-                        d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
-                    } else {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.dh) + at));
-                        d[0] = bf16lo(v.x), d[1] = bf16hi(v.x), d[2] = bf16lo(v.y), d[3] = bf16hi(v.y);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j >= cols) break;
-                        gq |= (uint32_t)__ldg(g + j) << (8 * j);
-                        uq |= (uint32_t)__ldg(g + p.n + j) << (8 * j);
-                        d[j] = F32 ? __ldg(static_cast<const float*>(p.dh) + at + j)
-                                   : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.dh) + at + j) << 16);
-                    }
-                }
-                sg = __ldg(p.sgu + 2 * r * nb + tc);
-                su = __ldg(p.sgu + (2 * r + 1) * nb + tc);
+            const int y = warp * kRows + i;
+            uint64_t d[2];
+            if constexpr (F32) {
+                const float4 v = *reinterpret_cast<const float4*>(&st.dh[y][lane * 4]);
+                d[0] = pack2(v.x, v.y), d[1] = pack2(v.z, v.w);
+            } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(&st.dh[y][lane * 4]);
+                d[0] = pack2(bf16lo(v.x), bf16hi(v.x)), d[1] = pack2(bf16lo(v.y), bf16hi(v.y));
             }
-            const uint32_t gh[2] = {fp8x2_to_f16x2<kE4M3>(gq), fp8x2_to_f16x2<kE4M3>(gq >> 16)};
-            const uint32_t uh[2] = {fp8x2_to_f16x2<kE4M3>(uq), fp8x2_to_f16x2<kE4M3>(uq >> 16)};
+            const uint32_t gq = *reinterpret_cast<const uint32_t*>(&st.gu[0][y][lane * 4]);
+            const uint32_t uq = *reinterpret_cast<const uint32_t*>(&st.gu[1][y][lane * 4]);
+            const float2 f = *reinterpret_cast<const float2*>(st.factor[y]);
+            const uint64_t sg = pack2(f.x, f.x), su = pack2(f.y, f.y);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float gv = (j & 1 ? f16_hi_to_f32(gh[j >> 1]) : f16_lo_to_f32(gh[j >> 1])) * sg;
-                const float uv = (j & 1 ? f16_hi_to_f32(uh[j >> 1]) : f16_lo_to_f32(uh[j >> 1])) * su;
-                float dy = 1.0f;
-                const float s = gate<ACT, true>(gv, &dy), a = gv * s;
-                const float slope = __fmaf_rn(ACT == kSilu ? a : a * dy, 1.0f - s, s);
-                const bool there = j < cols && r < p.rows;  // (a factor that is NaN counts for no other row)
-                dg[i][j] = there ? d[j] * uv * slope : 0.0f;
-                du[i][j] = there ? d[j] * a : 0.0f;
-                h[i][j] = there ? a * uv : 0.0f;
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t gh = fp8x2_to_f16x2<kE4M3>(gq >> (16 * j)), uh = fp8x2_to_f16x2<kE4M3>(uq >> (16 * j));
+                const uint64_t g = mul2(pack2(f16_lo_to_f32(gh), f16_hi_to_f32(gh)), sg);
+                const uint64_t u = mul2(pack2(f16_lo_to_f32(uh), f16_hi_to_f32(uh)), su);
+                uint64_t vg, vu, vh;
+                differentiate<ACT>(d[j], g, u, &vg, &vu, &vh);
+                const float2 a = unpack2(vg), b = unpack2(vu), c = unpack2(vh);
+                dg[i][2 * j] = a.x, dg[i][2 * j + 1] = a.y;
+                du[i][2 * j] = b.x, du[i][2 * j + 1] = b.y;
+                h[i][2 * j] = c.x, h[i][2 * j + 1] = c.y;
             }
         }
 
@@ -132,10 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
             uint32_t mine = 0;
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                uint32_t a = 0, b = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) a = max_abs(a, dg[i][j]), b = max_abs(b, du[i][j]);
-                a = warp_max_u32(a), b = warp_max_u32(b);
+                const float ma = max_abs3(max_abs3(0.0f, dg[i][0], dg[i][1]), dg[i][2], dg[i][3]);
+                const float mb = max_abs3(max_abs3(0.0f, du[i][0], du[i][1]), du[i][2], du[i][3]);
+                const uint32_t a = warp_max_u32(__float_as_uint(ma)), b = warp_max_u32(__float_as_uint(mb));
                 if (lane == i) mine = a;
                 if (lane == 8 + i) mine = b;
             }
@@ -165,23 +251,31 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
         }
 
         // ---- along the columns
-        if (p.dgu_t == nullptr && p.h_t == nullptr) continue;
+        if (p.dgu_t == nullptr && p.h_t == nullptr) {
+            __syncthreads();  // all have read this tile's inputs
+            if (kStages == 1) load(t + gridDim.x, 0);
+            continue;
+        }
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             const float (&v)[kRows][4] = k == 0 ? dg : k == 1 ? du : h;
-            uint32_t m[4] = {0, 0, 0, 0};
+            float m[4];
 #pragma unroll
-            for (int i = 0; i < kRows; ++i)
+            for (int j = 0; j < 4; ++j) {
+                m[j] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m[j] = max_abs(m[j], v[i][j]);
-            *reinterpret_cast<uint4*>(&sm.most[k][warp][lane * 4]) = make_uint4(m[0], m[1], m[2], m[3]);
+                for (int i = 0; i < kRows; i += 2) m[j] = max_abs3(m[j], v[i][j], v[i + 1][j]);
+            }
+            *reinterpret_cast<float4*>(&sm.most[k][warp][lane * 4]) = make_float4(m[0], m[1], m[2], m[3]);
         }
-        __syncthreads();  // (and the codes of the last tile have been read)
+        __syncthreads();
+        if (kStages == 1) load(t + gridDim.x, 0);
         if (threadIdx.x < 3 * kTile) {
             const int k = threadIdx.x / kTile, col = threadIdx.x % kTile;
-            uint32_t m = 0;
+            float most = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = umax(m, sm.most[k][w][col]);
+            for (int w = 0; w < kWarps; w += 2) most = max_abs3(most, sm.most[k][w][col], sm.most[k][w + 1][col]);
+            const uint32_t m = __float_as_uint(most);
             float scale, factor;
             if (k < 2) scale_from_amax<FMT>(__uint_as_float(m), 0, &scale, &factor);
             else scale_from_amax<kE4M3>(__uint_as_float(m), 0, &scale, &factor);
@@ -260,7 +354,7 @@ fp8_status_t run(const char* fn, const Backward& p, bool f32, int fmt, int act, 
     const int64_t tiles = ((p.n + kTile - 1) / kTile) * ((p.rows + kTile - 1) / kTile);
     const int sms = sm_count();
     const auto go = [&](auto kernel) {
-        return launch_smem(fn, kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kThreads), sizeof(Smem), st, p);
+        return launch_smem(fn, kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kThreads), f32 ? sizeof(Smem<true>) : sizeof(Smem<false>), st, p);
     };
     const auto pick = [&](auto silu, auto gelu) { return act == kSilu ? go(silu) : go(gelu); };
     if (fmt == kE4M3)
@@ -286,8 +380,10 @@ extern "C" fp8_status_t fp8_gated_block_backward(const void* dh, fp8_dtype_t dty
     if (act != FP8_ACT_SILU && act != FP8_ACT_GELU_TANH)
         return fail(FP8_ERR_INVALID_ARG, "%s: unknown activation %d", fn, (int)act);
     if (rows < 0 || n < 0) return fail(FP8_ERR_INVALID_ARG, "%s: negative size", fn);
-    constexpr int64_t kMost = (1ll << 31) - 256;
+    constexpr int64_t kMost = (1ll << 31) - 256, kMostTiles = 1ll << 30;
     if (rows > kMost || n > kMost) return fail(FP8_ERR_UNSUPPORTED, "%s: sizes must be below 2^31 - 256", fn);
+    if (((rows + kTile - 1) / kTile) * ((n + kTile - 1) / kTile) > kMostTiles)
+        return fail(FP8_ERR_UNSUPPORTED, "%s: too many tiles", fn);
     if ((dgu == nullptr) != (scale_inv_dgu == nullptr) || (dgu_t == nullptr) != (scale_inv_dgu_t == nullptr) ||
         (h_t == nullptr) != (scale_inv_h_t == nullptr))
         return fail(FP8_ERR_INVALID_ARG, "%s: each output needs both its codes and its scales", fn);
@@ -303,7 +399,11 @@ extern "C" fp8_status_t fp8_gated_block_backward(const void* dh, fp8_dtype_t dty
             return fail(FP8_ERR_INVALID_ARG, "%s: scales are not 4-byte aligned", fn);
     const auto aligned = [](const void* q, uintptr_t to) { return reinterpret_cast<uintptr_t>(q) % to == 0; };
     Backward p = {dh, gu, scale_inv_gu, rows, n, dgu, scale_inv_dgu, dgu_t, scale_inv_dgu_t, h_t, scale_inv_h_t};
-    p.words_in = n % 4 == 0 && aligned(gu, 4) && aligned(dh, 4 * dtype_size(dtype));
+    const auto copies = [&](int columns) {
+        const int bytes = columns * dtype_size(dtype);
+        return n % columns == 0 && aligned(gu, columns) && aligned(dh, bytes < 16 ? bytes : 16);
+    };
+    p.copy_in = copies(16) ? 16 : copies(4) ? 4 : 0;
     p.words_out = n % 4 == 0 && aligned(dgu, 4);
     p.pieces_t = rows % 16 == 0 && aligned16(dgu_t) && aligned16(h_t);
     return run(fn, p, dtype == FP8_DT_FP32, (int)fmt_grad, (int)act, static_cast<cudaStream_t>(stream));

@@ -58,6 +58,7 @@ def backward(L, dt=0, act=0, rows=4, n=4, fmt=0, dh=BAD, gu=BAD, sgu=BAD, dgu=BA
     (lambda L: backward(L, act=2), 1, "unknown activation"),
     (lambda L: backward(L, rows=-1), 1, "negative size"),
     (lambda L: backward(L, n=2 ** 31), 2, "below 2^31"),
+    (lambda L: backward(L, rows=2 ** 24, n=2 ** 24), 2, "too many tiles"),
     (lambda L: backward(L, sdgu=None), 1, "both"),
     (lambda L: backward(L, dt_=None), 1, "both"),
     (lambda L: backward(L, sht=None), 1, "both"),
