@@ -144,6 +144,54 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
 // lane, so that a warp's stores (column 4 lane + j) and the copy's reads spread over the banks.
 __device__ __forceinline__ uint32_t piece_at(int col, int piece) { return col * kTile + ((piece ^ (col >> 2 & 15)) << 3); }
 
+// The transposed codes of a tile from shared memory to the outputs.
+__device__ __forceinline__ void write_columns(const Backward& p, const uint8_t (&codes)[3][kTile * kTile], int tr, int tc,
+                                              int warp, int lane) {
+    const int rows = (int)(p.rows - (int64_t)tr * kTile < kTile ? p.rows - (int64_t)tr * kTile : kTile);
+    const int there = (int)(p.n - (int64_t)tc * kTile < kTile ? p.n - (int64_t)tc * kTile : kTile);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        uint8_t* const out = k < 2 ? p.dgu_t : p.h_t;
+        if (out == nullptr) continue;
+        const int64_t first = (k == 1 ? p.n : 0) + (int64_t)tc * kTile;
+        uint8_t* const base = out + first * p.rows + (int64_t)tr * kTile;
+        if (p.pieces_t) {  // 4 columns of 8 times 16 bytes per warp and step
+            const int col = warp * 4 + (lane >> 3), piece = lane & 7;
+            uint8_t* q = base + col * p.rows + piece * 16;
+#pragma unroll
+            for (int step = 0; step < 2; ++step, q += 64 * p.rows) {
+                // two pieces of 8 bytes that the swizzle keeps together, in either order
+                const uint4 v = *reinterpret_cast<const uint4*>(&codes[k][piece_at(col + step * 64, 2 * piece) & ~15u]);
+                const bool swap = (col >> 2) & 1;
+                if (col + step * 64 < there && piece * 16 < rows)
+                    stg_stream(q, swap ? make_uint4(v.z, v.w, v.x, v.y) : v);
+            }
+        } else {  // a column per warp and step, 4 bytes of it per lane
+#pragma unroll 1
+            for (int col = warp; col < there; col += kWarps) {
+                uint8_t* const q = base + col * p.rows;
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(&codes[k][piece_at(col, lane >> 1) + (lane & 1) * 4]);
+                const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, w, 1);
+                const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(q) & 3u);
+                if (rows == kTile && off + lane > 0) {
+                    // the aligned word that starts `off` bytes before this lane's
+                    if (lane > 0) *reinterpret_cast<uint32_t*>(q + lane * 4 - off) = __funnelshift_l(before, w, 8 * off);
+                    if (lane == 0 || lane == 31)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)  // the first one's last bytes, the last one's first
+                            if (lane == 0 ? i < 4 - (int)off : i >= 4 - (int)off) q[lane * 4 + i] = (uint8_t)(w >> (8 * i));
+                } else if (rows == kTile) {
+                    *reinterpret_cast<uint32_t*>(q) = w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (lane * 4 + i < rows) q[lane * 4 + i] = (uint8_t)(w >> (8 * i));
+                }
+            }
+        }
+    }
+}
+
 // Two columns at once, as packed pairs (fma.rn.f32x2 and its like).
 template <int ACT>
 __device__ __forceinline__ void differentiate(uint64_t d, uint64_t g, uint64_t u, uint64_t* dg, uint64_t* du, uint64_t* h) {
@@ -171,19 +219,21 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     load(blockIdx.x, 0);
-    int at = 0;
+    const bool columns = p.dgu_t != nullptr || p.h_t != nullptr;
+    int at = 0, last = -1;  // the tile whose transposed codes wait in shared memory
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
         const int tr = t / nb, tc = t % nb;
         const int64_t r0 = (int64_t)tr * kTile + warp * kRows, c0 = (int64_t)tc * kTile + lane * 4;
-        const int cols = (int)(p.n - c0 < 4 ? p.n - c0 : 4);  // of this lane
+        const int cols = (int)(p.n - c0 < 4 ? p.n - c0 : 4), rows = (int)(p.rows - r0 < kRows ? p.rows - r0 : kRows);  // here
         const Stage<F32>& st = sm.stage[at];
-        // this tile's inputs have landed; with two stages, the other one was left by all before the last tile's columns
-        if (kStages == 2) {
+        if (kStages == 2) {  // the other stage was left by all before the last tile's maxima
             load(t + gridDim.x, at ^ 1);
             at ^= 1;
         }
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        __syncthreads();  // (and the codes of the last tile have been read)
+        __syncthreads();  // this tile's inputs have landed, and the last one's codes are all there
+        if (last >= 0) write_columns(p, sm.codes, last / nb, last % nb, warp, lane);
+
         float dg[kRows][4], du[kRows][4], h[kRows][4];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
@@ -213,32 +263,61 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
                 h[i][2 * j] = c.x, h[i][2 * j + 1] = c.y;
             }
         }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {  // the largest of each column, of this warp's rows
+            const float (&v)[kRows][4] = k == 0 ? dg : k == 1 ? du : h;
+            float m[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m[j] = max_abs3(fabsf(v[0][j]), v[1][j], v[2][j]);
+#pragma unroll
+                for (int i = 3; i < kRows; i += 2) m[j] = max_abs3(m[j], v[i][j], v[i + 1 < kRows ? i + 1 : i][j]);
+            }
+            *reinterpret_cast<float4*>(&sm.most[k][warp][lane * 4]) = make_float4(m[0], m[1], m[2], m[3]);
+        }
+        __syncthreads();
+        if (kStages == 1) load(t + gridDim.x, 0);
 
-        // ---- along the rows: lane 8 k + i derives the scale of row i of dg (k 0) or du (k 1)
+        // ---- scales of the columns, a thread each; meanwhile the rows
+        if (columns && threadIdx.x < 3 * kTile) {
+            const int k = threadIdx.x / kTile, col = threadIdx.x % kTile;
+            float most = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; w += 2) most = max_abs3(most, sm.most[k][w][col], sm.most[k][w + 1][col]);
+            const uint32_t m = __float_as_uint(most);
+            float scale, factor;
+            if (k < 2) scale_from_amax<FMT>(most, 0, &scale, &factor);
+            else scale_from_amax<kE4M3>(most, 0, &scale, &factor);
+            // the sign, which no scale has, marks a tile with Inf or NaN
+            sm.scale[k][col] = m >= 0x7F800000u ? -scale : scale;
+            const int64_t c = (int64_t)tc * kTile + col;
+            float* const out = k < 2 ? p.sdgu_t : p.sh_t;
+            if (out != nullptr && c < p.n) out[((k == 1 ? p.n : 0) + c) * rb + tr] = factor;
+        }
+        // lane 8 k + i derives the scale of row i of dg (k 0) or du (k 1)
         if (p.dgu != nullptr) {
             uint32_t mine = 0;
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                const float ma = max_abs3(max_abs3(0.0f, dg[i][0], dg[i][1]), dg[i][2], dg[i][3]);
-                const float mb = max_abs3(max_abs3(0.0f, du[i][0], du[i][1]), du[i][2], du[i][3]);
+                const float ma = max_abs3(max_abs3(dg[i][0], dg[i][0], dg[i][1]), dg[i][2], dg[i][3]);
+                const float mb = max_abs3(max_abs3(du[i][0], du[i][0], du[i][1]), du[i][2], du[i][3]);
                 const uint32_t a = warp_max_u32(__float_as_uint(ma)), b = warp_max_u32(__float_as_uint(mb));
                 if (lane == i) mine = a;
                 if (lane == 8 + i) mine = b;
             }
             float scale, factor;
             scale_from_amax<FMT>(__uint_as_float(mine), 0, &scale, &factor);
-            if (lane < 16 && r0 + (lane & 7) < p.rows)
-                p.sdgu[(2 * (r0 + (lane & 7)) + (lane >> 3)) * nb + tc] = factor;
+            if (lane < 16 && (lane & 7) < rows) p.sdgu[(2 * (r0 + (lane & 7)) + (lane >> 3)) * nb + tc] = factor;
+            uint8_t* q = p.dgu + 2 * r0 * p.n + c0;
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < 2; ++k, q += p.n) {
                     const float (&v)[4] = k == 0 ? dg[i] : du[i];
                     const float s = __shfl_sync(0xFFFFFFFFu, scale, 8 * k + i);
                     const uint32_t top = FMT == kE5M2 ? __shfl_sync(0xFFFFFFFFu, mine, 8 * k + i) : 0u;
                     const uint32_t c = codes4<FMT>(v[0], v[1], v[2], v[3], s, top >= 0x7F800000u);
-                    if (r0 + i >= p.rows || cols <= 0) continue;
-                    uint8_t* const q = p.dgu + (2 * (r0 + i) + k) * p.n + c0;
+                    if (i >= rows || cols <= 0) continue;
                     if (p.words_out) {
                         *reinterpret_cast<uint32_t*>(q) = c;
                     } else {
@@ -249,104 +328,47 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
                 }
             }
         }
+        if (!columns) continue;
+        __syncthreads();
 
-        // ---- along the columns
-        if (p.dgu_t == nullptr && p.h_t == nullptr) {
-            __syncthreads();  // all have read this tile's inputs
-            if (kStages == 1) load(t + gridDim.x, 0);
-            continue;
-        }
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const float (&v)[kRows][4] = k == 0 ? dg : k == 1 ? du : h;
-            float m[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                m[j] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kRows; i += 2) m[j] = max_abs3(m[j], v[i][j], v[i + 1][j]);
-            }
-            *reinterpret_cast<float4*>(&sm.most[k][warp][lane * 4]) = make_float4(m[0], m[1], m[2], m[3]);
-        }
-        __syncthreads();
-        if (kStages == 1) load(t + gridDim.x, 0);
-        if (threadIdx.x < 3 * kTile) {
-            const int k = threadIdx.x / kTile, col = threadIdx.x % kTile;
-            float most = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; w += 2) most = max_abs3(most, sm.most[k][w][col], sm.most[k][w + 1][col]);
-            const uint32_t m = __float_as_uint(most);
-            float scale, factor;
-            if (k < 2) scale_from_amax<FMT>(__uint_as_float(m), 0, &scale, &factor);
-            else scale_from_amax<kE4M3>(__uint_as_float(m), 0, &scale, &factor);
-            // the sign, which no scale has, marks a tile with Inf or NaN
-            sm.scale[k][col] = m >= 0x7F800000u ? -scale : scale;
-            const int64_t c = (int64_t)tc * kTile + col;
-            float* const out = k < 2 ? p.sdgu_t : p.sh_t;
-            if (out != nullptr && c < p.n) out[((k == 1 ? p.n : 0) + c) * rb + tr] = factor;
-        }
-        __syncthreads();
+        // ---- transposed codes: products of two columns at a time, codes of four rows
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             const float (&v)[kRows][4] = k == 0 ? dg : k == 1 ? du : h;
             const float4 s4 = *reinterpret_cast<const float4*>(&sm.scale[k][lane * 4]);
             const float s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; j += 2) {
+                const uint64_t s2 = pack2(fabsf(s[j]), fabsf(s[j + 1]));
+                float2 x[kRows];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) x[i] = unpack2(mul2(pack2(v[i][j], v[i][j + 1]), s2));
+                uint2 c[2];
                 constexpr int kGrad = FMT;
-                uint2 c;
                 if (k < 2) {
-                    c.x = codes4<kGrad>(v[0][j], v[1][j], v[2][j], v[3][j], fabsf(s[j]), s[j] < 0.0f);
-                    c.y = codes4<kGrad>(v[4][j], v[5][j], v[6][j], v[7][j], fabsf(s[j]), s[j] < 0.0f);
-                } else {
-                    c.x = codes4<kE4M3>(v[0][j], v[1][j], v[2][j], v[3][j], fabsf(s[j]), false);
-                    c.y = codes4<kE4M3>(v[4][j], v[5][j], v[6][j], v[7][j], fabsf(s[j]), false);
-                }
-                *reinterpret_cast<uint2*>(&sm.codes[k][piece_at(lane * 4 + j, warp)]) = c;
-            }
-        }
-        __syncthreads();
-        const int rows = (int)(p.rows - (int64_t)tr * kTile < kTile ? p.rows - (int64_t)tr * kTile : kTile);
-#pragma unroll 1
-        for (int k = 0; k < 3; ++k) {
-            uint8_t* const out = k < 2 ? p.dgu_t : p.h_t;
-            if (out == nullptr) continue;
-            const int64_t first = (k == 1 ? p.n : 0) + (int64_t)tc * kTile;
-            uint8_t* const base = out + first * p.rows + (int64_t)tr * kTile;
-            const int there = (int)(p.n - (int64_t)tc * kTile < kTile ? p.n - (int64_t)tc * kTile : kTile);
-            if (p.pieces_t) {  // 4 columns of 8 pieces per warp and step
-#pragma unroll
-                for (int step = 0; step < 2; ++step) {
-                    const int col = step * 64 + warp * 4 + (lane >> 3), piece = lane & 7;
-                    const uint2 a = *reinterpret_cast<const uint2*>(&sm.codes[k][piece_at(col, 2 * piece)]);
-                    const uint2 b = *reinterpret_cast<const uint2*>(&sm.codes[k][piece_at(col, 2 * piece + 1)]);
-                    if (col < there && piece * 16 < rows)
-                        stg_stream(base + col * p.rows + piece * 16, make_uint4(a.x, a.y, b.x, b.y));
-                }
-            } else {  // a column per warp and step, 4 bytes of it per lane
-#pragma unroll 1
-                for (int col = warp; col < there; col += kWarps) {
-                    uint8_t* const q = base + col * p.rows;
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(&sm.codes[k][piece_at(col, lane >> 1) + (lane & 1) * 4]);
-                    const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, w, 1);
-                    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(q) & 3u);
-                    if (rows == kTile && off + lane > 0) {
-                        // the aligned word that starts `off` bytes before this lane's
-                        if (lane > 0) *reinterpret_cast<uint32_t*>(q + lane * 4 - off) = __funnelshift_l(before, w, 8 * off);
-                        if (lane == 0 || lane == 31)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)  // the first one's last bytes, the last one's first
-                                if (lane == 0 ? i < 4 - (int)off : i >= 4 - (int)off) q[lane * 4 + i] = (uint8_t)(w >> (8 * i));
-                    } else if (rows == kTile) {
-                        *reinterpret_cast<uint32_t*>(q) = w;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (lane * 4 + i < rows) q[lane * 4 + i] = (uint8_t)(w >> (8 * i));
+                    c[0] = make_uint2(cvt4<kGrad>(x[0].x, x[1].x, x[2].x, x[3].x), cvt4<kGrad>(x[4].x, x[5].x, x[6].x, x[7].x));
+                    c[1] = make_uint2(cvt4<kGrad>(x[0].y, x[1].y, x[2].y, x[3].y), cvt4<kGrad>(x[4].y, x[5].y, x[6].y, x[7].y));
+                    if (kGrad == kE5M2) {  // (the scale of a tile with Inf or NaN is 1)
+                        if (s[j] < 0.0f)
+                            c[0] = make_uint2(cvt4_exact<kGrad>(x[0].x, x[1].x, x[2].x, x[3].x),
+                                              cvt4_exact<kGrad>(x[4].x, x[5].x, x[6].x, x[7].x));
+                        if (s[j + 1] < 0.0f)
+                            c[1] = make_uint2(cvt4_exact<kGrad>(x[0].y, x[1].y, x[2].y, x[3].y),
+                                              cvt4_exact<kGrad>(x[4].y, x[5].y, x[6].y, x[7].y));
                     }
+                } else {
+                    c[0] = make_uint2(cvt4<kE4M3>(x[0].x, x[1].x, x[2].x, x[3].x), cvt4<kE4M3>(x[4].x, x[5].x, x[6].x, x[7].x));
+                    c[1] = make_uint2(cvt4<kE4M3>(x[0].y, x[1].y, x[2].y, x[3].y), cvt4<kE4M3>(x[4].y, x[5].y, x[6].y, x[7].y));
                 }
+                *reinterpret_cast<uint2*>(&sm.codes[k][piece_at(lane * 4 + j, warp)]) = c[0];
+                *reinterpret_cast<uint2*>(&sm.codes[k][piece_at(lane * 4 + j + 1, warp)]) = c[1];
             }
         }
+        last = t;
+    }
+    if (last >= 0) {
+        __syncthreads();
+        write_columns(p, sm.codes, last / nb, last % nb, warp, lane);
     }
 }
 
