@@ -8,6 +8,7 @@
 #pragma once
 
 #include "fp8q_device.cuh"
+#include "fp8q_tcgen05.cuh"
 
 namespace fp8q {
 
@@ -45,6 +46,23 @@ __device__ __forceinline__ float gate(float g, float* dy) {
         if constexpr (DERIVATIVE) *dy = __fmaf_rn(c2, (float)(3.0 * kGeluTwoC * kGeluCube), (float)kGeluTwoC);
     }
     return rcp_approx(1.0f + exp2_approx(t));
+}
+
+// The same of two values as a packed pair.
+template <int ACT, bool DERIVATIVE>
+__device__ __forceinline__ uint64_t gate2(uint64_t g, uint64_t* dy) {
+    const auto both = [](double v) { return pack2((float)v, (float)v); };
+    uint64_t t;
+    if constexpr (ACT == kSilu) {
+        t = mul2(g, both(-kLog2E));
+    } else {
+        const float2 v = unpack2(g);
+        const uint64_t c = pack2(fminf(fmaxf(v.x, -kGeluFar), kGeluFar), fminf(fmaxf(v.y, -kGeluFar), kGeluFar)), c2 = mul2(c, c);
+        t = mul2(c, fma2(c2, both(-kLog2E * kGeluTwoC * kGeluCube), both(-kLog2E * kGeluTwoC)));
+        if constexpr (DERIVATIVE) *dy = fma2(c2, both(3.0 * kGeluTwoC * kGeluCube), both(kGeluTwoC));
+    }
+    const float2 x = unpack2(t), e = unpack2(add2(pack2(exp2_approx(x.x), exp2_approx(x.y)), both(1.0)));
+    return pack2(rcp_approx(e.x), rcp_approx(e.y));
 }
 
 template <int ACT>

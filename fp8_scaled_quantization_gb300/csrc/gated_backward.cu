@@ -32,7 +32,7 @@ struct Backward {
     const void* dh;      // [rows, n]
     const uint8_t* gu;   // [rows, 2, n] E4M3, factors [rows, 2, blocks of n]
     const float* sgu;
-    int64_t rows, n;
+    int rows, n;
     uint8_t* dgu;        // as gu; nullable
     float* sdgu;
     uint8_t* dgu_t;      // [2, n, rows], factors [2, n, blocks of rows]; nullable
@@ -43,6 +43,9 @@ struct Backward {
     bool words_out;      // 4 columns store to dgu as an aligned word
     bool pieces_t;       // transposed rows are multiples of 16 bytes, 16-byte aligned
 };
+
+// A 64-bit product of two sizes or indexes, none of them negative.
+__device__ __forceinline__ int64_t wide(uint32_t a, uint32_t b) { return (int64_t)((uint64_t)a * b); }
 
 template <bool F32>
 struct Stage {  // a tile's inputs; rows and columns that are not there are zeros
@@ -59,6 +62,7 @@ struct Smem {
     alignas(16) float most[3][kWarps][kTile];     // column maxima of each warp's rows: dg, du, h
     alignas(16) float scale[3][kTile];
     alignas(16) uint8_t codes[3][kTile * kTile];  // transposed codes, 8-byte pieces swizzled
+    alignas(16) float exchange[kWarps][2 * kRows];  // row maxima and scales within a warp
 };
 
 template <int BYTES>
@@ -74,46 +78,56 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, bool ther
 // Copies of a tile's inputs, COLUMNS of them at a time, which lie inside or outside the
 // array as a whole.
 template <int COLUMNS, bool F32>
-__device__ __forceinline__ void load_pieces(const Backward& p, Stage<F32>& s, int64_t r0, int64_t c0) {
-    constexpr int kPieces = kTile / COLUMNS, kBytes = COLUMNS * (F32 ? 4 : 2);
-    const int x = threadIdx.x % kPieces * COLUMNS;
-    const int64_t c = c0 + x;
+__device__ __forceinline__ void load_pieces(const Backward& p, Stage<F32>& s, int r0, int c0) {
+    constexpr int kPieces = kTile / COLUMNS, kSize = F32 ? 4 : 2, kBytes = COLUMNS * kSize, kStep = kThreads / kPieces;
+    constexpr int kOne = kBytes < 16 ? kBytes : 16;
+    const int x = threadIdx.x % kPieces * COLUMNS, y0 = threadIdx.x / kPieces;
+    const int64_t row = wide(r0 + y0, p.n), at = row + c0 + x;
+    const char* d = static_cast<const char*>(p.dh) + at * kSize;
+    const uint8_t *g = p.gu + at + row, *u = g + p.n;
+    if (r0 + kTile <= p.rows && c0 + kTile <= p.n) {  // all are there
 #pragma unroll
-    for (int y = threadIdx.x / kPieces; y < kTile; y += kThreads / kPieces) {
-        const int64_t r = r0 + y;
-        const bool there = r < p.rows && c < p.n;
-        const int64_t at = there ? r * p.n + c : 0;
-        const char* const d = static_cast<const char*>(p.dh) + at * (F32 ? 4 : 2);
+        for (int y = 0; y < kTile; y += kStep, d += wide(p.n, kStep * kSize), g += wide(p.n, 2 * kStep), u += wide(p.n, 2 * kStep)) {
 #pragma unroll
-        for (int b = 0; b < kBytes; b += 16)
-            copy_async<(kBytes < 16 ? kBytes : 16)>(reinterpret_cast<char*>(&s.dh[y][x]) + b, d + (there ? b : 0), there);
-        const uint8_t* const g = p.gu + (there ? at + r * p.n : 0);
-        copy_async<COLUMNS>(&s.gu[0][y][x], g, there);
-        copy_async<COLUMNS>(&s.gu[1][y][x], g + (there ? p.n : 0), there);
+            for (int b = 0; b < kBytes; b += 16)
+                copy_async<kOne>(reinterpret_cast<char*>(&s.dh[y0 + y][x]) + b, d + b, true);
+            copy_async<COLUMNS>(&s.gu[0][y0 + y][x], g, true);
+            copy_async<COLUMNS>(&s.gu[1][y0 + y][x], u, true);
+        }
+    } else {
+#pragma unroll 1
+        for (int y = 0; y < kTile; y += kStep, d += wide(p.n, kStep * kSize), g += wide(p.n, 2 * kStep), u += wide(p.n, 2 * kStep)) {
+            const bool there = r0 + y0 + y < p.rows && c0 + x < p.n;
+#pragma unroll
+            for (int b = 0; b < kBytes; b += 16)
+                copy_async<kOne>(reinterpret_cast<char*>(&s.dh[y0 + y][x]) + b, there ? d + b : p.dh, there);
+            copy_async<COLUMNS>(&s.gu[0][y0 + y][x], there ? g : p.gu, there);
+            copy_async<COLUMNS>(&s.gu[1][y0 + y][x], there ? u : p.gu, there);
+        }
     }
 }
 
 template <bool F32>
 __device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int tr, int tc, int nb) {
-    const int64_t r0 = (int64_t)tr * kTile, c0 = (int64_t)tc * kTile;
+    const int r0 = tr * kTile, c0 = tc * kTile;
     if (p.copy_in == 16) {
         load_pieces<16>(p, s, r0, c0);
     } else if (p.copy_in == 4) {
         load_pieces<4>(p, s, r0, c0);
     } else {
         const int x = threadIdx.x % kTile;
+#pragma unroll 1
         for (int y = threadIdx.x / kTile; y < kTile; y += kThreads / kTile) {
             const bool there = r0 + y < p.rows && c0 + x < p.n;
-            const int64_t at = (r0 + y) * p.n + c0 + x;
+            const int64_t row = wide(r0 + y, p.n), at = row + c0 + x;
             s.dh[y][x] = there ? __ldg(static_cast<const typename Stage<F32>::Grad*>(p.dh) + at) : 0;
-            s.gu[0][y][x] = there ? __ldg(p.gu + at + (r0 + y) * p.n) : 0;
-            s.gu[1][y][x] = there ? __ldg(p.gu + at + (r0 + y + 1) * p.n) : 0;
+            s.gu[0][y][x] = there ? __ldg(p.gu + at + row) : 0;
+            s.gu[1][y][x] = there ? __ldg(p.gu + at + row + p.n) : 0;
         }
     }
     if (threadIdx.x < 2 * kTile) {
-        const int64_t r = r0 + (threadIdx.x >> 1);
-        const bool there = r < p.rows;
-        copy_async<4>(&s.factor[threadIdx.x >> 1][threadIdx.x & 1], p.sgu + (there ? (2 * r + (threadIdx.x & 1)) * nb + tc : 0), there);
+        const bool there = r0 + (int)(threadIdx.x >> 1) < p.rows;
+        copy_async<4>(&s.factor[0][0] + threadIdx.x, p.sgu + (there ? wide(2 * r0 + threadIdx.x, nb) + tc : 0), there);
     }
 }
 
@@ -124,20 +138,15 @@ __device__ __forceinline__ float max_abs3(float m, float a, float b) {
     return r;
 }
 
-// Four codes of values whose tile holds Inf or NaN (scale 1), each by its own rule.
+// Four codes of scaled values.  cvt.satfinite gives every code by the rule but that of
+// an E5M2 infinity, which is the code of the largest value and one more; `special`:
+// there may be some (a finite value times its tile's scale is finite).
 template <int FMT>
-__device__ __noinline__ uint32_t cvt4_exact(float a, float b, float c, float d) {
-    uint32_t sat;
-    return quant_one<FMT>(a, 1.0f, &sat) | quant_one<FMT>(b, 1.0f, &sat) << 8 | quant_one<FMT>(c, 1.0f, &sat) << 16 |
-           quant_one<FMT>(d, 1.0f, &sat) << 24;
-}
-
-// cvt.satfinite gives every code by the rule but that of an E5M2 infinity.
-template <int FMT>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float scale, bool special) {
-    if (FMT == kE5M2 && special) return cvt4_exact<FMT>(a, b, c, d);
-    const float2 lo = fmul2_rn(a, b, scale), hi = fmul2_rn(c, d, scale);
-    return cvt4<FMT>(lo.x, lo.y, hi.x, hi.y);
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, bool special) {
+    uint32_t r = cvt4<FMT>(a, b, c, d);
+    if (FMT == kE5M2 && special)
+        r += (isinf(a) ? 1u : 0u) + (isinf(b) ? 1u << 8 : 0u) + (isinf(c) ? 1u << 16 : 0u) + (isinf(d) ? 1u << 24 : 0u);
+    return r;
 }
 
 // Where the 8 bytes of a warp's rows in column `col` lie: pieces move with the column's
@@ -147,29 +156,27 @@ __device__ __forceinline__ uint32_t piece_at(int col, int piece) { return col * 
 // The transposed codes of a tile from shared memory to the outputs.
 __device__ __forceinline__ void write_columns(const Backward& p, const uint8_t (&codes)[3][kTile * kTile], int tr, int tc,
                                               int warp, int lane) {
-    const int rows = (int)(p.rows - (int64_t)tr * kTile < kTile ? p.rows - (int64_t)tr * kTile : kTile);
-    const int there = (int)(p.n - (int64_t)tc * kTile < kTile ? p.n - (int64_t)tc * kTile : kTile);
+    const int rows = min(p.rows - tr * kTile, kTile), there = min(p.n - tc * kTile, kTile);
+    const int64_t mine = wide(lane >> 3, p.rows) + (lane & 7) * 16;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         uint8_t* const out = k < 2 ? p.dgu_t : p.h_t;
         if (out == nullptr) continue;
-        const int64_t first = (k == 1 ? p.n : 0) + (int64_t)tc * kTile;
-        uint8_t* const base = out + first * p.rows + (int64_t)tr * kTile;
+        uint8_t* const base = out + wide((k == 1 ? (uint32_t)p.n : 0u) + tc * kTile, p.rows) + tr * kTile;
         if (p.pieces_t) {  // 4 columns of 8 times 16 bytes per warp and step
             const int col = warp * 4 + (lane >> 3), piece = lane & 7;
-            uint8_t* q = base + col * p.rows + piece * 16;
+            uint8_t* q = base + wide(warp * 4, p.rows) + mine;
+            const int left = piece * 16 < rows ? there - col : 0;
 #pragma unroll
-            for (int step = 0; step < 2; ++step, q += 64 * p.rows) {
-                // two pieces of 8 bytes that the swizzle keeps together, in either order
+            for (int step = 0; step < 2; ++step, q += wide(64, p.rows)) {
+                // two pieces of 8 bytes that the swizzle keeps together, the warp's all in one order
                 const uint4 v = *reinterpret_cast<const uint4*>(&codes[k][piece_at(col + step * 64, 2 * piece) & ~15u]);
-                const bool swap = (col >> 2) & 1;
-                if (col + step * 64 < there && piece * 16 < rows)
-                    stg_stream(q, swap ? make_uint4(v.z, v.w, v.x, v.y) : v);
+                if (step * 64 < left) stg_stream(q, warp & 1 ? make_uint4(v.z, v.w, v.x, v.y) : v);
             }
         } else {  // a column per warp and step, 4 bytes of it per lane
 #pragma unroll 1
             for (int col = warp; col < there; col += kWarps) {
-                uint8_t* const q = base + col * p.rows;
+                uint8_t* const q = base + wide(col, p.rows);
                 const uint32_t w = *reinterpret_cast<const uint32_t*>(&codes[k][piece_at(col, lane >> 1) + (lane & 1) * 4]);
                 const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, w, 1);
                 const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(q) & 3u);
@@ -195,14 +202,18 @@ __device__ __forceinline__ void write_columns(const Backward& p, const uint8_t (
 // Two columns at once, as packed pairs (fma.rn.f32x2 and its like).
 template <int ACT>
 __device__ __forceinline__ void differentiate(uint64_t d, uint64_t g, uint64_t u, uint64_t* dg, uint64_t* du, uint64_t* h) {
-    const float2 gv = unpack2(g);
-    float dy[2] = {1.0f, 1.0f};
-    const uint64_t s = pack2(gate<ACT, true>(gv.x, &dy[0]), gate<ACT, true>(gv.y, &dy[1]));
-    const uint64_t a = mul2(g, s), one = pack2(1.0f, 1.0f), rest = fma2(s, pack2(-1.0f, -1.0f), one);
-    const uint64_t slope = fma2(ACT == kSilu ? a : mul2(a, pack2(dy[0], dy[1])), rest, s);
+    uint64_t dy;
+    const uint64_t s = gate2<ACT, true>(g, &dy), a = mul2(g, s), rest = fma2(s, pack2(-1.0f, -1.0f), pack2(1.0f, 1.0f));
+    const uint64_t slope = fma2(ACT == kSilu ? a : mul2(a, dy), rest, s);
     *dg = mul2(mul2(d, u), slope);
     *du = mul2(d, a);
     *h = mul2(a, u);
+}
+
+// Two E4M3 codes (the low half of c) times a factor, as a packed pair.
+__device__ __forceinline__ uint64_t values2(uint32_t c, uint64_t factor) {
+    const uint32_t v = fp8x2_to_f16x2<kE4M3>(c);
+    return mul2(pack2(f16_lo_to_f32(v), f16_hi_to_f32(v)), factor);
 }
 
 template <int FMT, int ACT, bool F32>
@@ -210,29 +221,33 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
     extern __shared__ __align__(128) uint8_t raw[];
     Smem<F32>& sm = *reinterpret_cast<Smem<F32>*>(raw);
     constexpr int kStages = Smem<F32>::kStages;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nb = (int)((p.n + kTile - 1) / kTile), rb = (int)((p.rows + kTile - 1) / kTile);
-    const int total = nb * rb;
+    // (a shuffle tells the compiler that the number is the same in the whole warp)
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int nb = (p.n + kTile - 1) / kTile, rb = (p.rows + kTile - 1) / kTile;
+    // tiles blockIdx.x + i * gridDim.x, along the columns first; a step in tiles along both
+    const int step_r = gridDim.x / nb, step_c = gridDim.x % nb;
+    int tr = blockIdx.x / nb, tc = blockIdx.x % nb;
     pdl_begin();
-    const auto load = [&](int t, int stage) {
-        if (t < total) load_tile<F32>(p, sm.stage[stage], t / nb, t % nb, nb);
+    const auto load = [&](int r, int c, int stage) {
+        if (r < rb) load_tile<F32>(p, sm.stage[stage], r, c, nb);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    load(blockIdx.x, 0);
+    load(tr, tc, 0);
     const bool columns = p.dgu_t != nullptr || p.h_t != nullptr;
-    int at = 0, last = -1;  // the tile whose transposed codes wait in shared memory
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        const int tr = t / nb, tc = t % nb;
-        const int64_t r0 = (int64_t)tr * kTile + warp * kRows, c0 = (int64_t)tc * kTile + lane * 4;
-        const int cols = (int)(p.n - c0 < 4 ? p.n - c0 : 4), rows = (int)(p.rows - r0 < kRows ? p.rows - r0 : kRows);  // here
+    int at = 0, last_r = -1, last_c = 0;  // the tile whose transposed codes wait in shared memory
+    for (int next_r, next_c; tr < rb; tr = next_r, tc = next_c) {
+        next_r = tr + step_r, next_c = tc + step_c;
+        if (next_c >= nb) next_c -= nb, ++next_r;
+        const int r0 = tr * kTile + warp * kRows, c0 = tc * kTile + lane * 4;
+        const int cols = min(p.n - c0, 4), rows = min(p.rows - r0, kRows);  // here
         const Stage<F32>& st = sm.stage[at];
         if (kStages == 2) {  // the other stage was left by all before the last tile's maxima
-            load(t + gridDim.x, at ^ 1);
+            load(next_r, next_c, at ^ 1);
             at ^= 1;
         }
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncthreads();  // this tile's inputs have landed, and the last one's codes are all there
-        if (last >= 0) write_columns(p, sm.codes, last / nb, last % nb, warp, lane);
+        if (last_r >= 0) write_columns(p, sm.codes, last_r, last_c, warp, lane);
 
         float dg[kRows][4], du[kRows][4], h[kRows][4];
 #pragma unroll
@@ -252,9 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
             const uint64_t sg = pack2(f.x, f.x), su = pack2(f.y, f.y);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint32_t gh = fp8x2_to_f16x2<kE4M3>(gq >> (16 * j)), uh = fp8x2_to_f16x2<kE4M3>(uq >> (16 * j));
-                const uint64_t g = mul2(pack2(f16_lo_to_f32(gh), f16_hi_to_f32(gh)), sg);
-                const uint64_t u = mul2(pack2(f16_lo_to_f32(uh), f16_hi_to_f32(uh)), su);
+                const uint64_t g = values2(gq >> (16 * j), sg), u = values2(uq >> (16 * j), su);
                 uint64_t vg, vu, vh;
                 differentiate<ACT>(d[j], g, u, &vg, &vu, &vh);
                 const float2 a = unpack2(vg), b = unpack2(vu), c = unpack2(vh);
@@ -276,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
             *reinterpret_cast<float4*>(&sm.most[k][warp][lane * 4]) = make_float4(m[0], m[1], m[2], m[3]);
         }
         __syncthreads();
-        if (kStages == 1) load(t + gridDim.x, 0);
+        if (kStages == 1) load(next_r, next_c, 0);
 
         // ---- scales of the columns, a thread each; meanwhile the rows
         if (columns && threadIdx.x < 3 * kTile) {
@@ -290,43 +303,60 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
             else scale_from_amax<kE4M3>(most, 0, &scale, &factor);
             // the sign, which no scale has, marks a tile with Inf or NaN
             sm.scale[k][col] = m >= 0x7F800000u ? -scale : scale;
-            const int64_t c = (int64_t)tc * kTile + col;
+            const int c = tc * kTile + col;
             float* const out = k < 2 ? p.sdgu_t : p.sh_t;
-            if (out != nullptr && c < p.n) out[((k == 1 ? p.n : 0) + c) * rb + tr] = factor;
+            if (out != nullptr && c < p.n) out[wide((k == 1 ? (uint32_t)p.n : 0u) + c, rb) + tr] = factor;
         }
-        // lane 8 k + i derives the scale of row i of dg (k 0) or du (k 1)
+        // A warp's row maxima are the same in all lanes: they go through shared memory four words
+        // at a time, lane 2 i + k derives the scale of row i of dg (k 0) or du (k 1), and all
+        // come back the same way (fewer instructions than selects and shuffles).
         if (p.dgu != nullptr) {
-            uint32_t mine = 0;
+            float* const exchange = sm.exchange[warp];
+            uint32_t most[2 * kRows];
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const float ma = max_abs3(max_abs3(dg[i][0], dg[i][0], dg[i][1]), dg[i][2], dg[i][3]);
-                const float mb = max_abs3(max_abs3(du[i][0], du[i][0], du[i][1]), du[i][2], du[i][3]);
-                const uint32_t a = warp_max_u32(__float_as_uint(ma)), b = warp_max_u32(__float_as_uint(mb));
-                if (lane == i) mine = a;
-                if (lane == 8 + i) mine = b;
+            for (int i = 0; i < 2 * kRows; ++i) {
+                const float (&v)[4] = i & 1 ? du[i >> 1] : dg[i >> 1];
+                most[i] = warp_max_u32(__float_as_uint(max_abs3(max_abs3(v[0], v[0], v[1]), v[2], v[3])));
             }
-            float scale, factor;
-            scale_from_amax<FMT>(__uint_as_float(mine), 0, &scale, &factor);
-            if (lane < 16 && (lane & 7) < rows) p.sdgu[(2 * (r0 + (lane & 7)) + (lane >> 3)) * nb + tc] = factor;
-            uint8_t* q = p.dgu + 2 * r0 * p.n + c0;
+            if (lane == 0) {
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
+                for (int i = 0; i < 2 * kRows; i += 4)
+                    *reinterpret_cast<uint4*>(exchange + i) = make_uint4(most[i], most[i + 1], most[i + 2], most[i + 3]);
+            }
+            __syncwarp();
+            uint32_t top = 0;
+            if (lane < 2 * kRows) {
+                const float amax = exchange[lane];
+                float factor, scale;
+                scale_from_amax<FMT>(amax, 0, &scale, &factor);
+                top = __float_as_uint(amax);
+                exchange[lane] = scale;
+                if ((lane >> 1) < rows) p.sdgu[wide(2 * r0 + lane, nb) + tc] = factor;
+            }
+            const bool special = __any_sync(0xFFFFFFFFu, top >= 0x7F800000u);
+            uint8_t* q = p.dgu + wide(2 * r0, p.n) + c0;
+            const auto codes = [&](auto store) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k, q += p.n) {
-                    const float (&v)[4] = k == 0 ? dg[i] : du[i];
-                    const float s = __shfl_sync(0xFFFFFFFFu, scale, 8 * k + i);
-                    const uint32_t top = FMT == kE5M2 ? __shfl_sync(0xFFFFFFFFu, mine, 8 * k + i) : 0u;
-                    const uint32_t c = codes4<FMT>(v[0], v[1], v[2], v[3], s, top >= 0x7F800000u);
-                    if (i >= rows || cols <= 0) continue;
-                    if (p.words_out) {
-                        *reinterpret_cast<uint32_t*>(q) = c;
-                    } else {
+                for (int i0 = 0; i0 < 2 * kRows; i0 += 4) {
+                    const float4 s4 = *reinterpret_cast<const float4*>(exchange + i0);
+                    const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i, q += p.n) {
+                        const float (&v)[4] = i & 1 ? du[(i0 + i) >> 1] : dg[(i0 + i) >> 1];
+                        const float2 a = fmul2_rn(v[0], v[1], s[i]), b = fmul2_rn(v[2], v[3], s[i]);
+                        store((i0 + i) >> 1, codes4<FMT>(a.x, a.y, b.x, b.y, special));
+                    }
+                }
+            };
+            if (p.words_out && rows == kRows && (tc + 1) * kTile <= p.n)  // all are there
+                codes([&](int, uint32_t c) { *reinterpret_cast<uint32_t*>(q) = c; });
+            else
+                codes([&](int i, uint32_t c) {
+                    if (i < rows)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (j < cols) q[j] = (uint8_t)(c >> (8 * j));
-                    }
-                }
-            }
+                });
         }
         if (!columns) continue;
         __syncthreads();
@@ -344,18 +374,11 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) x[i] = unpack2(mul2(pack2(v[i][j], v[i][j + 1]), s2));
                 uint2 c[2];
-                constexpr int kGrad = FMT;
                 if (k < 2) {
-                    c[0] = make_uint2(cvt4<kGrad>(x[0].x, x[1].x, x[2].x, x[3].x), cvt4<kGrad>(x[4].x, x[5].x, x[6].x, x[7].x));
-                    c[1] = make_uint2(cvt4<kGrad>(x[0].y, x[1].y, x[2].y, x[3].y), cvt4<kGrad>(x[4].y, x[5].y, x[6].y, x[7].y));
-                    if (kGrad == kE5M2) {  // (the scale of a tile with Inf or NaN is 1)
-                        if (s[j] < 0.0f)
-                            c[0] = make_uint2(cvt4_exact<kGrad>(x[0].x, x[1].x, x[2].x, x[3].x),
-                                              cvt4_exact<kGrad>(x[4].x, x[5].x, x[6].x, x[7].x));
-                        if (s[j + 1] < 0.0f)
-                            c[1] = make_uint2(cvt4_exact<kGrad>(x[0].y, x[1].y, x[2].y, x[3].y),
-                                              cvt4_exact<kGrad>(x[4].y, x[5].y, x[6].y, x[7].y));
-                    }
+                    c[0] = make_uint2(codes4<FMT>(x[0].x, x[1].x, x[2].x, x[3].x, s[j] < 0.0f),
+                                      codes4<FMT>(x[4].x, x[5].x, x[6].x, x[7].x, s[j] < 0.0f));
+                    c[1] = make_uint2(codes4<FMT>(x[0].y, x[1].y, x[2].y, x[3].y, s[j + 1] < 0.0f),
+                                      codes4<FMT>(x[4].y, x[5].y, x[6].y, x[7].y, s[j + 1] < 0.0f));
                 } else {
                     c[0] = make_uint2(cvt4<kE4M3>(x[0].x, x[1].x, x[2].x, x[3].x), cvt4<kE4M3>(x[4].x, x[5].x, x[6].x, x[7].x));
                     c[1] = make_uint2(cvt4<kE4M3>(x[0].y, x[1].y, x[2].y, x[3].y), cvt4<kE4M3>(x[4].y, x[5].y, x[6].y, x[7].y));
@@ -364,16 +387,16 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
                 *reinterpret_cast<uint2*>(&sm.codes[k][piece_at(lane * 4 + j + 1, warp)]) = c[1];
             }
         }
-        last = t;
+        last_r = tr, last_c = tc;
     }
-    if (last >= 0) {
+    if (last_r >= 0) {
         __syncthreads();
-        write_columns(p, sm.codes, last / nb, last % nb, warp, lane);
+        write_columns(p, sm.codes, last_r, last_c, warp, lane);
     }
 }
 
 fp8_status_t run(const char* fn, const Backward& p, bool f32, int fmt, int act, cudaStream_t st) {
-    const int64_t tiles = ((p.n + kTile - 1) / kTile) * ((p.rows + kTile - 1) / kTile);
+    const int64_t tiles = (int64_t)((p.n + kTile - 1) / kTile) * ((p.rows + kTile - 1) / kTile);
     const int sms = sm_count();
     const auto go = [&](auto kernel) {
         return launch_smem(fn, kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kThreads), f32 ? sizeof(Smem<true>) : sizeof(Smem<false>), st, p);
@@ -420,7 +443,7 @@ extern "C" fp8_status_t fp8_gated_block_backward(const void* dh, fp8_dtype_t dty
         if ((reinterpret_cast<uintptr_t>(s) & 3u) != 0)
             return fail(FP8_ERR_INVALID_ARG, "%s: scales are not 4-byte aligned", fn);
     const auto aligned = [](const void* q, uintptr_t to) { return reinterpret_cast<uintptr_t>(q) % to == 0; };
-    Backward p = {dh, gu, scale_inv_gu, rows, n, dgu, scale_inv_dgu, dgu_t, scale_inv_dgu_t, h_t, scale_inv_h_t};
+    Backward p = {dh, gu, scale_inv_gu, (int)rows, (int)n, dgu, scale_inv_dgu, dgu_t, scale_inv_dgu_t, h_t, scale_inv_h_t};
     const auto copies = [&](int columns) {
         const int bytes = columns * dtype_size(dtype);
         return n % columns == 0 && aligned(gu, columns) && aligned(dh, bytes < 16 ? bytes : 16);
