@@ -433,8 +433,6 @@ struct FinishArgs {
 
 // ------------------------------------------------------------ memory ops
 
-__device__ __forceinline__ bool aligned_to_16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // L2 eviction-priority policies (createpolicy, sm_80+).  Current scaling reads
 // x twice (amax, then the cast); the cast runs right after the amax pass in
 // reverse chunk order, so it starts on the part of x the amax pass touched

@@ -65,8 +65,8 @@ fp8_status_t check_groups(const char* fn, int groups, const int64_t* ends);
 // gemm_block_pair.cu: 256 x 256 outputs per CTA pair; gated: 256 x 128.
 fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st);
 
-// gemm_block_stream.cu: 128 columns of D per CTA and `tokens` (16, 32, 64 or 128)
-// rows at a time, k > 0; the contraction is not ragged.
+// gemm_block_stream.cu: 128 columns of D per CTA and `tokens` (16, 32, 64 or 128;
+// gated: not 128) rows at a time, k > 0; the contraction is not ragged.
 fp8_status_t run_gemm_stream(const char* fn, const GemmProblem& p, int tokens, cudaStream_t st);
 // How it does so: items of `tokens` rows and 128 columns (with ragged rows, at
 // most), CTAs that share an item's contraction, and clusters of them at one time.

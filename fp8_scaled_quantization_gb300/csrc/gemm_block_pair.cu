@@ -377,11 +377,11 @@ __device__ __forceinline__ void stage_codes(const float* v, float scale, uint32_
 }
 
 // The staged rows (rows of them, `to` columns that are there) to `out` by plain stores;
-// wide: 16-byte aligned rows whose end is too.
+// unit: 16 or 4 where rows, their ends and `out` are aligned to it, else 1 byte.
 template <int WORDS>
-__device__ __forceinline__ void copy_codes(uint8_t* out, int64_t pitch, uint32_t stage, int lane, int rows, int to, bool wide) {
+__device__ __forceinline__ void copy_codes(uint8_t* out, int64_t pitch, uint32_t stage, int lane, int rows, int to, int unit) {
     if (to <= 0) return;
-    if (wide) {
+    if (unit == 16) {
         constexpr int kPieces = WORDS / 4, kAtOnce = 32 / kPieces;  // lanes per row, rows per step
         const int piece = lane % kPieces;
         if (piece * 16 >= to) return;
@@ -395,17 +395,27 @@ __device__ __forceinline__ void copy_codes(uint8_t* out, int64_t pitch, uint32_t
                          : "memory");
             if (r < rows) *reinterpret_cast<uint4*>(out + r * pitch + piece * 16) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-    } else {  // bytes, a row per step
-#pragma unroll 1
-        for (int r = 0; r < rows; ++r) {
+    } else {
+        constexpr int kAtOnce = 32 / WORDS;
+        const int word = lane % WORDS;
+#pragma unroll 4
+        for (int r = lane / WORDS; r < rows; r += kAtOnce) {
+            uint32_t v;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(staged<WORDS>(stage, r, word >> 2) + (word & 3) * 4) : "memory");
+            uint8_t* const q = out + r * pitch + word * 4;
+            if (unit == 4) {
+                if (word * 4 < to) *reinterpret_cast<uint32_t*>(q) = v;
+            } else {
 #pragma unroll
-            for (int x = lane; x < WORDS * 4; x += 32) {
-                uint32_t v;
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(staged<WORDS>(stage, r, x >> 4) + (x & 15)) : "memory");
-                if (x < to) out[r * pitch + x] = (uint8_t)v;
+                for (int i = 0; i < 4; ++i)
+                    if (word * 4 + i < to) q[i] = (uint8_t)(v >> (8 * i));
             }
         }
     }
+}
+__device__ __forceinline__ int unit_of(const void* out, int64_t n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out) | (uintptr_t)n;
+    return a % 16 == 0 ? 16 : a % 4 == 0 ? 4 : 1;
 }
 
 __device__ __forceinline__ float tile_scale(uint32_t amax_bits, float* factor) {
@@ -460,7 +470,7 @@ __device__ __forceinline__ void store_gated(const GemmProblem& p, Sums<false>& a
         if (lane < rows) out.sgu[(row * 2 + HALF) * nb + col0 / kBlk] = factor;
         __syncwarp();
         copy_codes<32>(out.gu + (row0 * 2 + HALF) * p.n + col0, 2 * p.n, mine, lane, rows, there,
-                       p.n % 16 == 0 && aligned_to_16(out.gu));
+                       unit_of(out.gu, p.n));
         __syncwarp();
     }
 #pragma unroll
@@ -482,7 +492,7 @@ __device__ __forceinline__ void store_gated(const GemmProblem& p, Sums<false>& a
     stage_codes<16>(acc.v + HALF * 64, scale, mine, lane);
     __syncwarp();
     copy_codes<16>(out.h + row0 * p.n + col0 + HALF * 64, p.n, mine, lane, rows, there - HALF * 64,
-                   p.n % 16 == 0 && aligned_to_16(out.h));
+                   unit_of(out.h, p.n));
     __syncwarp();
 }
 

@@ -9,6 +9,11 @@
 // partial sums through distributed shared memory, in the order of their ranks,
 // so that results do not depend on timing and no workspace is needed.
 //
+// The gated form gives the gate's weight to the even CTAs of a cluster and the up
+// projection's to the odd ones, each half of them sharing the contraction; both
+// sums of a token meet where they are joined.  (A CTA that streamed both, one
+// after the other, needs twice the sums, and 64 tokens no longer fit an SM twice.)
+//
 // Roles per CTA: four warps (eight from 32 tokens on, each pair of them sharing
 // the tokens of 32 columns) scale, add, join and store; then one warp fills the
 // ring of operand tiles and gathers the scales, and one issues the products.
@@ -16,6 +21,7 @@
 
 #include "fp8q_host.h"
 #include "fp8q_tcgen05.cuh"
+#include "gated.cuh"
 #include "gemm_block.cuh"
 
 namespace fp8q {
@@ -25,6 +31,10 @@ constexpr int kRows = 128;        // rows of the weight per CTA
 constexpr int kScaleBlocks = 4;   // blocks of an item whose scales are gathered together
 constexpr int kScaleSlots = 3;
 constexpr int kMostSplit = 8;     // CTAs of a cluster
+
+// FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: B [n,
+// k], 1 x 128 tiles; 3: gated, two B [n, k] per group, 128 x 128 blocks.
+constexpr int kTiles = 2, kGated = 3;
 
 // Per number of tokens: ring depth and CTAs per SM.  Two CTAs per SM where their
 // tiles fit, so that one's start and end overlap the other's stream.
@@ -40,12 +50,15 @@ struct Shape {
     static constexpr int kThreads = (kScalers + 2) * 32;      // 10 warps leave 96 registers with two CTAs per SM
 };
 
-template <int TOKENS, bool TILES>
+template <int TOKENS, int FORM>
 struct Shared {
+    static constexpr bool TILES = FORM == kTiles;
     using S = Shape<TOKENS, TILES>;
     alignas(16) float part[TOKENS][kRows];                           // this CTA's partial sums
     alignas(16) float token[kScaleSlots][kScaleBlocks][TOKENS];      // per block: token scale (x block scale)
     alignas(16) float weight[TILES ? kScaleSlots : 1][kScaleBlocks][TILES ? kRows : 1];  // 1 x 128 tiles: the weight rows' scales
+    // gated: the largest |h|, |g| and |u| (bits) of each token that this CTA joins, in each warp's 32 columns
+    alignas(16) uint32_t most[FORM == kGated ? 3 : 1][FORM == kGated ? TOKENS / 2 : 1][4];
     uint64_t full[S::kStages], empty[S::kStages];
     uint64_t tmem_full[S::kBufs], tmem_empty[S::kBufs];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
@@ -54,10 +67,10 @@ struct Shared {
     int groups[1];  // the group table: as long as the launch asks for
 };
 
-template <int TOKENS, bool TILES>
+template <int TOKENS, int FORM>
 constexpr size_t smem_bytes(int groups) {
-    using S = Shape<TOKENS, TILES>;
-    constexpr size_t bytes = 1024 + (size_t)S::kStages * S::kStageBytes + sizeof(Shared<TOKENS, TILES>);
+    using S = Shape<TOKENS, FORM == kTiles>;
+    constexpr size_t bytes = 1024 + (size_t)S::kStages * S::kStageBytes + sizeof(Shared<TOKENS, FORM>);
     static_assert(S::kCtas * (bytes + group_table_bytes(256) + 1024) <= 228 * 1024, "shared memory of an SM");
     static_assert(bytes + group_table_bytes(kMaxGroups) <= 227 * 1024, "shared memory of a CTA");
     return bytes + group_table_bytes(groups);
@@ -72,7 +85,7 @@ struct Item {
 };
 
 template <int TOKENS>
-__device__ __forceinline__ Item locate(const GemmProblem& p, const GroupTable& g, int tiles_n, int t, int rank, int split) {
+__device__ __forceinline__ Item locate(const GemmProblem& p, const GroupTable& g, int tiles_n, int t, int share, int shares) {
     Item r;
     const int e = find_group(g, p.groups + 1, t);
     const int local = t - g.tile[e], begin = e > 0 ? g.end[e - 1] : 0, end = g.end[e];
@@ -83,8 +96,8 @@ __device__ __forceinline__ Item locate(const GemmProblem& p, const GroupTable& g
     r.row_end = end;
     r.col0 = local / tiles_m * kRows;
     const int blks = e < p.groups ? (int)blocks_of(p.k) : 0;
-    r.blk0 = (int)((int64_t)blks * rank / split);
-    r.blks = (int)((int64_t)blks * (rank + 1) / split) - r.blk0;
+    r.blk0 = (int)((int64_t)blks * share / shares);
+    r.blks = (int)((int64_t)blks * (share + 1) / shares) - r.blk0;
     return r;
 }
 
@@ -136,19 +149,85 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
-// FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: B [n,
-// k], 1 x 128 tiles.  The cluster's size is the number of shares.
+// The end of a gated item, of the tokens j0 .. j1 - 1 that this CTA joins: both sums of
+// this lane's column over the cluster (the gate's in even ranks, the up projection's in
+// odd ones), h from them, quantized in tiles of the CTA's 128 columns: four warps, of
+// which the CTA has one set or two that take the tokens in turn.
+template <int ACT, int TOKENS>
+__device__ __forceinline__ void finish_gated(const GemmProblem& p, Shared<TOKENS, kGated>& sh, const Item& item, int warp, int lane,
+                                             int j0, int j1, int split) {
+    constexpr int kSets = Shape<TOKENS, false>::kScalers / 4;
+    constexpr int kMost = 4;  // tokens of a warp at a time: their sums stay in registers
+    const GatedOut& out = p.gated;
+    const int row = (warp & 3) * 32 + lane, first = j0 + (warp >> 2);
+    const int64_t col = item.col0 + row, nb = blocks_of(p.n);
+    const bool keep = out.gu != nullptr;
+#pragma unroll 1
+    for (int from = first; from < j1; from += kMost * kSets) {
+        float g[kMost], u[kMost];
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            const int j = from + i * kSets;
+            if (j >= j1) break;
+            g[i] = u[i] = 0.0f;
+            // A lane without a column reads nothing: what it read it would not wait for, and the
+            // CTA that holds it may leave once this one's warps have met it.
+            if (col < p.n) {
+                float x[kMostSplit];
+#pragma unroll
+                for (int r = 0; r < kMostSplit; ++r)
+                    x[r] = r < split ? ld_cluster(cluster_addr(smem_addr(&sh.part[j][row]), r)) : 0.0f;
+                g[i] = x[0], u[i] = x[1];
+#pragma unroll
+                for (int r = 2; r < kMostSplit; r += 2)
+                    if (r < split) g[i] = __fadd_rn(g[i], x[r]), u[i] = __fadd_rn(u[i], x[r + 1]);
+            }
+            const uint32_t mh = warp_max_u32(abs_bits(gated<ACT>(g[i], u[i])));
+            uint32_t mg = 0, mu = 0;
+            if (keep) mg = warp_max_u32(abs_bits(g[i])), mu = warp_max_u32(abs_bits(u[i]));
+            if (lane == 0) {
+                sh.most[0][j - j0][warp & 3] = mh;
+                sh.most[1][j - j0][warp & 3] = mg;
+                sh.most[2][j - j0][warp & 3] = mu;
+            }
+        }
+        group_sync(1 + (warp >> 2), 128);
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            const int j = from + i * kSets;
+            if (j >= j1) break;
+            const int64_t token = item.row0 + j;
+            const auto write = [&](int kind, float v, uint8_t* codes, float* factors, int64_t line) {
+                const uint4 m = *reinterpret_cast<const uint4*>(sh.most[kind][j - j0]);
+                float scale, factor;
+                scale_from_amax<kE4M3>(__uint_as_float(umax(umax(m.x, m.y), umax(m.z, m.w))), 0, &scale, &factor);
+                if (col < p.n) codes[line * p.n + col] = (uint8_t)cvt2<kE4M3>(__fmul_rn(v, scale), 0.0f);
+                if (row == 0) factors[line * nb + item.col0 / kBlk] = factor;
+            };
+            write(0, gated<ACT>(g[i], u[i]), out.h, out.sh, token);
+            if (keep) {
+                write(1, g[i], out.gu, out.sgu, 2 * token);
+                write(2, u[i], out.gu, out.sgu, 2 * token + 1);
+            }
+        }
+        group_sync(1 + (warp >> 2), 128);  // the maxima have been read
+    }
+}
+
+// The cluster's size is the number of shares (gated: of both projections).
 template <int FORM, int TOKENS>
-__global__ void __launch_bounds__(Shape<TOKENS, FORM == 2>::kThreads, Shape<TOKENS, FORM == 2>::kCtas)
+__global__ void __launch_bounds__(Shape<TOKENS, FORM == kTiles>::kThreads, Shape<TOKENS, FORM == kTiles>::kCtas)
 gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ CUtensorMap map_a,
                    const __grid_constant__ CUtensorMap map_b, int split) {
-    constexpr bool B_KN = FORM == 1, B_TILES = FORM == 2;
+    constexpr bool B_KN = FORM == 1, B_TILES = FORM == kTiles, GATED = FORM == kGated;
     using S = Shape<TOKENS, B_TILES>;
     extern __shared__ uint8_t raw[];
     uint8_t* const tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    Shared<TOKENS, B_TILES>& sh = *reinterpret_cast<Shared<TOKENS, B_TILES>*>(tiles + S::kStages * S::kStageBytes);
+    Shared<TOKENS, FORM>& sh = *reinterpret_cast<Shared<TOKENS, FORM>*>(tiles + S::kStages * S::kStageBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = split > 1 ? (int)cluster_rank() : 0;
+    // this CTA's share of the contraction, of how many, and (gated) its projection
+    const int share = GATED ? rank >> 1 : rank, shares = GATED ? split >> 1 : split, half = GATED ? rank & 1 : 0;
 
     if (threadIdx.x == 0) {
         sh.dead = 0;
@@ -198,7 +277,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + token0;
         uint32_t it = 0, group = 0, items = 0;
         for (int t = first; t < total; t += step, ++items) {
-            const Item item = locate<TOKENS>(p, groups, tiles_n, t, rank, split);
+            const Item item = locate<TOKENS>(p, groups, tiles_n, t, share, shares);
             float acc[kMine];
 #pragma unroll
             for (int i = 0; i < kMine; ++i) acc[i] = 0.0f;
@@ -236,7 +315,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
             for (int j = 0; j < kMine; ++j) {
                 if (token0 + j < tokens) sh.part[token0 + j][row] = acc[j];
             }
-            if (split == 1) {
+            if (!GATED && split == 1) {
                 if (col < p.n) {
 #pragma unroll 4
                     for (int j = token0; j < min(token0 + kMine, tokens); ++j)
@@ -248,19 +327,25 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
             if (lane < split) cluster_arrive<true>(cluster_addr(smem_addr(&sh.part_full), lane));
             w.template wait<true>(smem_addr(&sh.part_full), items & 1);
             __syncwarp();
-            // A lane without a column reads nothing: what it read it would not wait for, and the
-            // CTA that holds it may leave once this one's warps have met it.
-            const int j0 = tokens * rank / split, j1 = col < p.n ? tokens * (rank + 1) / split : j0;
-            for (int j = j0 + (warp >> 2); j < j1; j += S::kScalers / 4) {
-                float v[kMostSplit];
+            const int first_token = tokens * rank / split, last_token = tokens * (rank + 1) / split;
+            if constexpr (GATED) {
+                if (p.gated.act == kSilu) finish_gated<kSilu, TOKENS>(p, sh, item, warp, lane, first_token, last_token, split);
+                else finish_gated<kGeluTanh, TOKENS>(p, sh, item, warp, lane, first_token, last_token, split);
+            } else {
+                // A lane without a column reads nothing: what it read it would not wait for, and the
+                // CTA that holds it may leave once this one's warps have met it.
+                const int j0 = first_token, j1 = col < p.n ? last_token : j0;
+                for (int j = j0 + (warp >> 2); j < j1; j += S::kScalers / 4) {
+                    float v[kMostSplit];
 #pragma unroll
-                for (int r = 0; r < kMostSplit; ++r)
-                    v[r] = r < split ? ld_cluster(cluster_addr(smem_addr(&sh.part[j][row]), r)) : 0.0f;
-                float sum = v[0];
+                    for (int r = 0; r < kMostSplit; ++r)
+                        v[r] = r < split ? ld_cluster(cluster_addr(smem_addr(&sh.part[j][row]), r)) : 0.0f;
+                    float sum = v[0];
 #pragma unroll
-                for (int r = 1; r < kMostSplit; ++r)
-                    if (r < split) sum = __fadd_rn(sum, v[r]);
-                store_out(p, (int64_t)(item.row0 + j) * p.n + col, sum);
+                    for (int r = 1; r < kMostSplit; ++r)
+                        if (r < split) sum = __fadd_rn(sum, v[r]);
+                    store_out(p, (int64_t)(item.row0 + j) * p.n + col, sum);
+                }
             }
             __syncwarp();
             // (nothing overwrites the last item's sums)
@@ -285,7 +370,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
                 }
             } else {
                 const int64_t cb = item.col0 / kBlk;
-                const float* const sb = p.sb + (int64_t)item.group * kb * nb;
+                const float* const sb = p.sb + (GATED ? 2 * (int64_t)item.group + half : (int64_t)item.group) * kb * nb;
                 if constexpr (B_KN) {
                     const float* const at = sb + (int64_t)g0 * nb + cb;
                     ws[0] = make_float4(__ldg(at), to > 1 ? __ldg(at + nb) : 0.0f, to > 2 ? __ldg(at + 2 * nb) : 0.0f,
@@ -333,7 +418,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
         uint32_t it = 0, stage = 0, phase = 0;
         bool loaded = false;  // the next group's scales are in registers
         for (int t = first; t < total; t += step) {
-            const Item item = locate<TOKENS>(p, groups, tiles_n, t, rank, split);
+            const Item item = locate<TOKENS>(p, groups, tiles_n, t, share, shares);
             if (!loaded && item.blks > 0) load_group(item, 0);
             for (int b = 0; b < item.blks; ++b, ++it) {
                 const uint32_t wt = base + stage * S::kStageBytes, xt = wt + kTileBytes, bar = smem_addr(&sh.full[stage]);
@@ -342,7 +427,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
                 __syncwarp();
                 if (elect_one() && !w.dead) {
                     mbar_arrive_expect_tx(&sh.full[stage], S::kStageBytes);
-                    const int matrix = B_TILES ? 0 : item.group;
+                    const int matrix = B_TILES ? 0 : GATED ? 2 * item.group + half : item.group;
                     if constexpr (B_KN) tma_tile<false>(wt, &map_b, item.col0, x, matrix, bar);
                     else tma_tile<false>(wt, &map_b, x, item.col0, matrix, bar);
                     tma_tile<false>(xt, &map_a, x, item.row0, 0, bar);
@@ -360,7 +445,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
                     if (next < item.blks) {
                         load_group(item, next);
                     } else if (t + step < total) {
-                        const Item after = locate<TOKENS>(p, groups, tiles_n, t + step, rank, split);
+                        const Item after = locate<TOKENS>(p, groups, tiles_n, t + step, share, shares);
                         loaded = after.blks > 0;
                         if (loaded) load_group(after, 0);
                     }
@@ -377,7 +462,7 @@ gemm_stream_kernel(const __grid_constant__ GemmProblem p, const __grid_constant_
         uint32_t it = 0, stage = 0, phase = 0;
         bool ready = false;  // the next block's tiles and buffer, asked for while this block's products are issued
         for (int t = first; t < total; t += step) {
-            const int blks = locate<TOKENS>(p, groups, tiles_n, t, rank, split).blks;
+            const int blks = locate<TOKENS>(p, groups, tiles_n, t, share, shares).blks;
             for (int b = 0; b < blks; ++b, ++it) {
                 const uint32_t buf = it % S::kBufs;
                 if (!ready) {
@@ -437,7 +522,7 @@ int clusters_per_turn(int split, int sms) {
     if (n > 0) return n;
     using S = Shape<128, false>;
     const int most = sms / split;
-    n = max_clusters(reinterpret_cast<const void*>(gemm_stream_kernel<0, 128>), S::kThreads, smem_bytes<128, false>(1), split);
+    n = max_clusters(reinterpret_cast<const void*>(gemm_stream_kernel<0, 128>), S::kThreads, smem_bytes<128, 0>(1), split);
     n = n <= 0 || n > most ? most : n;
     known[split].store(n, std::memory_order_relaxed);
     return n;
@@ -449,8 +534,11 @@ StreamPlan plan(const GemmProblem& p, int sms) {
     const int64_t tiles_n = (p.n + kRows - 1) / kRows, tiles_m = (p.m + TOKENS - 1) / TOKENS, kb = blocks_of(p.k);
     const int64_t busy = p.groups < p.m ? p.groups : p.m;  // groups with rows, at most
     StreamPlan r = {(tiles_m + busy - 1) * tiles_n, 1, ctas * sms};
-    // shares of the contraction: as many as run at one time, each at least two blocks long
-    for (int split = 2; split <= kMostSplit && kb >= 2 * split; ++split) {
+    // shares of the contraction: as many as run at one time, each at least two blocks
+    // long; gated: CTAs for both projections of each
+    const int each = p.gated.h != nullptr ? 2 : 1;
+    if (each == 2) r = {r.items, 2, ctas * clusters_per_turn(2, sms)};
+    for (int split = each * 2; split <= kMostSplit && kb >= 2 * (split / each); split += each) {
         const int clusters = ctas * clusters_per_turn(split, sms);
         if (r.items <= clusters) r = {r.items, split, clusters};
     }
@@ -465,9 +553,11 @@ fp8_status_t run(const char* fn, const GemmProblem& p, const CUtensorMap& a, con
         return launch_cluster(fn, kernel, dim3((unsigned)(clusters * how.split)), dim3(Shape<TOKENS, false>::kThreads), smem,
                               how.split, st, p, a, b, how.split);
     };
-    return p.b_tiles ? go(gemm_stream_kernel<2, TOKENS>, smem_bytes<TOKENS, true>(p.groups))
-           : p.b_kn  ? go(gemm_stream_kernel<1, TOKENS>, smem_bytes<TOKENS, false>(p.groups))
-                     : go(gemm_stream_kernel<0, TOKENS>, smem_bytes<TOKENS, false>(p.groups));
+    if constexpr (TOKENS <= 64)
+        if (p.gated.h != nullptr) return go(gemm_stream_kernel<kGated, TOKENS>, smem_bytes<TOKENS, kGated>(p.groups));
+    return p.b_tiles ? go(gemm_stream_kernel<kTiles, TOKENS>, smem_bytes<TOKENS, kTiles>(p.groups))
+           : p.b_kn  ? go(gemm_stream_kernel<1, TOKENS>, smem_bytes<TOKENS, 1>(p.groups))
+                     : go(gemm_stream_kernel<0, TOKENS>, smem_bytes<TOKENS, 0>(p.groups));
 }
 
 }  // namespace
@@ -482,7 +572,8 @@ StreamPlan stream_plan(const GemmProblem& p, int tokens, int sms) {
 }
 
 fp8_status_t run_gemm_stream(const char* fn, const GemmProblem& p, int tokens, cudaStream_t st) {
-    const Operand oa = {p.a, p.k, p.m, 1, tokens}, ob = {p.b, p.b_kn ? p.n : p.k, p.b_kn ? p.k : p.n, p.groups, 128};
+    const int matrices = p.groups * (p.gated.h != nullptr ? 2 : 1);
+    const Operand oa = {p.a, p.k, p.m, 1, tokens}, ob = {p.b, p.b_kn ? p.n : p.k, p.b_kn ? p.k : p.n, matrices, 128};
     CUtensorMap a = {}, b = {};
     StreamUse use(st);
     const fp8_status_t s = operand_maps(fn, oa, &a, ob, &b, use, st);

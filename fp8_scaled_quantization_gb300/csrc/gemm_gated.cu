@@ -9,6 +9,8 @@
 // activation reads them and writes h, and the cast reads that and writes codes: 9
 // bytes an element and two launches more, where 1 byte (with the checkpoint 3)
 // leaves this kernel.
+#include <cmath>
+
 #include "fp8q_host.h"
 #include "gemm_block.cuh"
 
@@ -39,7 +41,43 @@ fp8_status_t check(const char* fn, const GemmProblem& p) {
     return FP8_OK;
 }
 
-fp8_status_t run(const char* fn, const GemmProblem& p, cudaStream_t st) { return run_gemm_pair(fn, p, st); }
+// Which kernel, by estimated times in microseconds as for the plain products, whose
+// kernels these are: the pair kernel (0), or the stream kernel by tiles of 16, 32 or 64
+// tokens.  Measured on GB300 ([m, n, k] silu, without a checkpoint; in a CUDA graph, cold weights):
+//   [1, 18432, 7168]   stream/16 44  stream/32 45  pair 79    [16, 7168, 7168]  stream/16 22  stream/64 26  pair 37
+//   [32, 14336, 4096]  stream/32 28  stream/64 31  pair 38    [48, 14336, 4096] stream/64 33  stream/32 43  pair 39
+//   [64, 2048, 7168]   stream/32 15  stream/64 17  pair 29    [128, 4096, 4096] pair 20  stream/64 21
+//   [256, 7168, 7168]  pair 33  stream/32 84       [300, 1024, 2048] pair 13  stream/64 13
+//   experts: 96 rows over 64 (2048 x 7168 each) stream/16 273  stream/64 301  pair 383; 512 over 32: 146, 181, 203;
+//   1024 over 16 (2048 x 2048) pair 46  stream/64 53
+// (tiles of 128 tokens: never the fastest).
+int choose(const GemmProblem& p) {
+    const int64_t kb = blocks_of(p.k), sms = sm_count();
+    const double busy = (double)(p.groups < p.m ? p.groups : p.m);
+    const auto tiles = [&](int rows) {  // along m: the groups' last tiles are half full on average
+        return p.groups > 1 ? (double)p.m / rows + 0.5 * busy : (double)((p.m + rows - 1) / rows);
+    };
+    const auto most = [](double a, double b) { return a > b ? a : b; };
+    const double memory = (2.0 * busy * (double)p.n * (double)p.k + (double)p.m * (double)(p.k + p.n)) / 6.5e6;
+    const double columns = (double)((p.n + 127) / 128);
+    const double pair = ceil(tiles(256) * columns / (double)(sms / 2)) * (0.46 * (double)kb + 2.0);
+    double best = 4.0 + most(pair, memory * 6.5 / 4.5);
+    int choice = 0;
+    constexpr double kBlock[3] = {0.40, 0.39, 0.66}, kJoin[3] = {1.0, 1.8, 2.2};
+    for (int i = 0; i < 3; ++i) {
+        const int tokens = 16 << i;
+        const StreamPlan plan = stream_plan(p, tokens, (int)sms);
+        const double compute = ceil(tiles(tokens) * columns / plan.clusters) * ceil((double)kb / (plan.split / 2)) * kBlock[i];
+        const double us = 5.0 + kJoin[i] + most(compute, memory);
+        if (us < best) best = us, choice = tokens;
+    }
+    return choice;
+}
+
+fp8_status_t run(const char* fn, const GemmProblem& p, cudaStream_t st) {
+    const int tokens = p.k > 0 ? choose(p) : 0;
+    return tokens > 0 ? run_gemm_stream(fn, p, tokens, st) : run_gemm_pair(fn, p, st);
+}
 
 }  // namespace
 }  // namespace fp8q
