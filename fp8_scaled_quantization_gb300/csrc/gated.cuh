@@ -70,10 +70,19 @@ __device__ __forceinline__ float gated(float g, float u) {
     return g * gate<ACT, false>(g, nullptr) * u;
 }
 
+// The same of two columns; the same values, and h the same bits, as gated().
+template <int ACT>
+__device__ __forceinline__ uint64_t gated2(uint64_t g, uint64_t u) {
+    return mul2(mul2(g, gate2<ACT, false>(g, nullptr)), u);
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// The larger magnitude; a NaN in either is the result (bit patterns of
-// magnitudes order as the magnitudes do, with Inf and then NaN above them).
-__device__ __forceinline__ uint32_t max_abs(uint32_t m, float v) { return umax(m, abs_bits(v)); }
+// max(m, |a|, |b|), a NaN if any of them is one.
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
 
 }  // namespace fp8q

@@ -131,13 +131,6 @@ __device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int 
     }
 }
 
-// max(m, |a|, |b|), a NaN if any of them is one.
-__device__ __forceinline__ float max_abs3(float m, float a, float b) {
-    float r;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
-    return r;
-}
-
 // Four codes of scaled values.  cvt.satfinite gives every code by the rule but that of
 // an E5M2 infinity, which is the code of the largest value and one more; `special`:
 // there may be some (a finite value times its tile's scale is finite).

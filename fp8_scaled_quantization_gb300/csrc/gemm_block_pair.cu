@@ -385,15 +385,20 @@ __device__ __forceinline__ void copy_codes(uint8_t* out, int64_t pitch, uint32_t
         constexpr int kPieces = WORDS / 4, kAtOnce = 32 / kPieces;  // lanes per row, rows per step
         const int piece = lane % kPieces;
         if (piece * 16 >= to) return;
+        uint8_t* q = out + lane / kPieces * pitch + piece * 16;
+        const int left = rows - lane / kPieces;
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += kAtOnce) {
-            const int r = r0 + lane / kPieces;
-            uint32_t v[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(staged<WORDS>(stage, r, piece))
-                         : "memory");
-            if (r < rows) *reinterpret_cast<uint4*>(out + r * pitch + piece * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+        for (int r0 = 0; r0 < 32; r0 += 4 * kAtOnce) {
+            uint32_t v[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
+                             : "r"(staged<WORDS>(stage, r0 + i * kAtOnce + lane / kPieces, piece))
+                             : "memory");
+#pragma unroll
+            for (int i = 0; i < 4; ++i, q += kAtOnce * pitch)
+                if (r0 + i * kAtOnce < left) *reinterpret_cast<uint4*>(q) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
         }
     } else {
         constexpr int kAtOnce = 32 / WORDS;
@@ -428,7 +433,7 @@ __device__ __forceinline__ float tile_scale(uint32_t amax_bits, float* factor) {
 // warp), into its sums; the other warp's half of them at `theirs`.  Their largest |h|.
 template <int ACT, int HALF>
 __device__ __forceinline__ uint32_t gate_columns(float* v, uint32_t theirs, int lane) {
-    uint32_t most = 0;
+    float most = 0.0f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         float o[4];
@@ -437,13 +442,15 @@ __device__ __forceinline__ uint32_t gate_columns(float* v, uint32_t theirs, int 
                      : "r"(theirs + j * 512 + lane * 16)
                      : "memory");
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float& x = v[HALF * 64 + j * 4 + i];
-            x = HALF == 0 ? gated<ACT>(x, o[i]) : gated<ACT>(o[i], x);
-            most = max_abs(most, x);
+        for (int i = 0; i < 4; i += 2) {
+            float* const x = v + HALF * 64 + j * 4 + i;
+            const uint64_t a = pack2(x[0], x[1]), b = pack2(o[i], o[i + 1]);
+            const float2 h = unpack2(HALF == 0 ? gated2<ACT>(a, b) : gated2<ACT>(b, a));
+            x[0] = h.x, x[1] = h.y;
+            most = max_abs3(most, h.x, h.y);
         }
     }
-    return most;
+    return __float_as_uint(most);
 }
 
 // A warp's part of a gated tile: rows row0 .. (at most 32, before row_end), columns col0 ..
@@ -461,11 +468,11 @@ __device__ __forceinline__ void store_gated(const GemmProblem& p, Sums<false>& a
         for (int i = 0; i < 128; ++i) acc.v[i] = i < there ? acc.v[i] : 0.0f;
     }
     if (out.gu != nullptr) {
-        uint32_t most = 0;
+        float most[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 128; ++i) most = max_abs(most, acc.v[i]);
+        for (int i = 0; i < 128; i += 2) most[i / 2 % 4] = max_abs3(most[i / 2 % 4], acc.v[i], acc.v[i + 1]);
         float factor;
-        const float scale = tile_scale(most, &factor);
+        const float scale = tile_scale(__float_as_uint(max_abs3(max_abs3(most[0], most[1], most[2]), most[3], 0.0f)), &factor);
         stage_codes<32>(acc.v, scale, mine, lane);
         if (lane < rows) out.sgu[(row * 2 + HALF) * nb + col0 / kBlk] = factor;
         __syncwarp();
