@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kTile = 128, kWarps = 16, kThreads = kWarps * 32;
 constexpr int kRows = kTile / kWarps;  // of a warp
+constexpr int kGroup = 4;              // tiles whose factors are read and written together
 
 struct Backward {
     const void* dh;      // [rows, n]
@@ -40,6 +41,7 @@ struct Backward {
     uint8_t* h_t;        // [n, rows] E4M3, factors [n, blocks of rows]; nullable
     float* sh_t;
     int copy_in;         // columns of dh and gu that one asynchronous copy takes: 16, 4 (aligned to that) or 0
+    bool factors_in, factors_out;  // four tiles' factors of a row lie in aligned pieces of 16 bytes
     bool words_out;      // 4 columns store to dgu as an aligned word
     bool pieces_t;       // transposed rows are multiples of 16 bytes, 16-byte aligned
 };
@@ -52,7 +54,6 @@ struct Stage {  // a tile's inputs; rows and columns that are not there are zero
     using Grad = typename std::conditional<F32, float, uint16_t>::type;
     alignas(16) Grad dh[kTile][kTile];
     alignas(16) uint8_t gu[2][kTile][kTile];
-    float factor[kTile][2];
 };
 
 template <bool F32>
@@ -63,6 +64,10 @@ struct Smem {
     alignas(16) float scale[3][kTile];
     alignas(16) uint8_t codes[3][kTile * kTile];  // transposed codes, 8-byte pieces swizzled
     alignas(16) float exchange[kWarps][2 * kRows];  // row maxima and scales within a warp
+    // Factors of four tiles along a row of tiles, in and out, of row i / 2, gate or up projection
+    // i % 2: words that lie a row apart in memory cost a request each (for one tile at a
+    // time 25 us of 122, 4096 x 14336).
+    alignas(16) float factor_in[2][2 * kTile][kGroup], factor_out[2 * kTile][kGroup];
 };
 
 template <int BYTES>
@@ -108,7 +113,7 @@ __device__ __forceinline__ void load_pieces(const Backward& p, Stage<F32>& s, in
 }
 
 template <bool F32>
-__device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int tr, int tc, int nb) {
+__device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int tr, int tc) {
     const int r0 = tr * kTile, c0 = tc * kTile;
     if (p.copy_in == 16) {
         load_pieces<16>(p, s, r0, c0);
@@ -125,9 +130,32 @@ __device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int 
             s.gu[1][y][x] = there ? __ldg(p.gu + at + row + p.n) : 0;
         }
     }
-    if (threadIdx.x < 2 * kTile) {
-        const bool there = r0 + (int)(threadIdx.x >> 1) < p.rows;
-        copy_async<4>(&s.factor[0][0] + threadIdx.x, p.sgu + (there ? wide(2 * r0 + threadIdx.x, nb) + tc : 0), there);
+}
+
+// The factors of a tile, or of the four tiles around it where they lie in aligned pieces.
+__device__ __forceinline__ void load_factors(const Backward& p, float (&in)[2 * kTile][kGroup], int tr, int tc, int nb, bool whole) {
+    if (threadIdx.x >= 2 * kTile) return;
+    const int at = 2 * tr * kTile + threadIdx.x;
+    const bool there = (at >> 1) < p.rows;
+    const float* const from = p.sgu + (there ? wide(at, nb) + tc : 0);
+    if (whole) copy_async<16>(in[threadIdx.x], there ? from - tc % kGroup : from, there);
+    else copy_async<4>(&in[threadIdx.x][tc % kGroup], from, there);
+}
+
+// The factors of dg and du of the tiles tc - tc % 4 + first .. tc.
+__device__ __forceinline__ void store_factors(const Backward& p, const float (&out)[2 * kTile][kGroup], int tr, int tc, int nb, int first) {
+    if (threadIdx.x >= 2 * kTile) return;
+    const int at = 2 * tr * kTile + threadIdx.x, last = tc % kGroup;
+    if ((at >> 1) >= p.rows) return;
+    float* const to = p.sdgu + wide(at, nb) + (tc - last);
+    const float4 v = *reinterpret_cast<const float4*>(out[threadIdx.x]);
+    if (p.factors_out && first == 0 && last == kGroup - 1) {
+        *reinterpret_cast<float4*>(to) = v;
+    } else {
+        if (first == 0) to[0] = v.x;
+        if (first <= 1 && last >= 1) to[1] = v.y;
+        if (first <= 2 && last >= 2) to[2] = v.z;
+        if (last == 3) to[3] = v.w;
     }
 }
 
@@ -209,6 +237,15 @@ __device__ __forceinline__ uint64_t values2(uint32_t c, uint64_t factor) {
     return mul2(pack2(f16_lo_to_f32(v), f16_hi_to_f32(v)), factor);
 }
 
+// The scale of a tile by the rule of scale_from_amax, its format known at run time.
+__device__ __forceinline__ void scale_of(float amax, bool e5m2, float* scale, float* factor) {
+    const bool usual = amax > 0.0f && !isinf(amax);
+    float s = __fdiv_rn(e5m2 ? Fmt<kE5M2>::kMax : Fmt<kE4M3>::kMax, usual ? amax : 1.0f);
+    s = usual ? fminf(fmaxf(s, 1.175494351e-38f), 3.402823466e+38f) : 1.0f;
+    *scale = s;
+    *factor = __fdiv_rn(1.0f, s);
+}
+
 template <int FMT, int ACT, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __grid_constant__ Backward p) {
     extern __shared__ __align__(128) uint8_t raw[];
@@ -217,26 +254,31 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
     // (a shuffle tells the compiler that the number is the same in the whole warp)
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int nb = (p.n + kTile - 1) / kTile, rb = (p.rows + kTile - 1) / kTile;
-    // tiles blockIdx.x + i * gridDim.x, along the columns first; a step in tiles along both
-    const int step_r = gridDim.x / nb, step_c = gridDim.x % nb;
-    int tr = blockIdx.x / nb, tc = blockIdx.x % nb;
+    // a share of the tiles, one after another along the columns
+    const int total = nb * rb, end = (int)(wide(total, blockIdx.x + 1) / gridDim.x);
+    int t = (int)(wide(total, blockIdx.x) / gridDim.x), tr = t / nb, tc = t % nb;
     pdl_begin();
-    const auto load = [&](int r, int c, int stage) {
-        if (r < rb) load_tile<F32>(p, sm.stage[stage], r, c, nb);
+    const auto load = [&](int r, int c, int stage, bool there) {
+        if (there) load_tile<F32>(p, sm.stage[stage], r, c);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    load(tr, tc, 0);
+    load_factors(p, sm.factor_in[0], tr, tc, nb, p.factors_in);
+    load(tr, tc, 0, true);
     const bool columns = p.dgu_t != nullptr || p.h_t != nullptr;
-    int at = 0, last_r = -1, last_c = 0;  // the tile whose transposed codes wait in shared memory
-    for (int next_r, next_c; tr < rb; tr = next_r, tc = next_c) {
-        next_r = tr + step_r, next_c = tc + step_c;
-        if (next_c >= nb) next_c -= nb, ++next_r;
+    int at = 0, last_r = -1, last_c = 0;    // the tile whose transposed codes wait in shared memory
+    int group = 0, first = tc % kGroup;     // the place of this tile's factors, the first one of its four that is this CTA's
+    for (int next_r, next_c, next_group; t < end; ++t, tr = next_r, tc = next_c, group = next_group) {
+        next_r = tr, next_c = tc + 1;
+        if (next_c == nb) next_c = 0, ++next_r;
+        const bool more = t + 1 < end, last_of_group = next_c % kGroup == 0;
+        next_group = last_of_group ? group ^ 1 : group;
         const int r0 = tr * kTile + warp * kRows, c0 = tc * kTile + lane * 4;
         const int cols = min(p.n - c0, 4), rows = min(p.rows - r0, kRows);  // here
         const Stage<F32>& st = sm.stage[at];
+        const float (&factors)[2 * kTile][kGroup] = sm.factor_in[group];
         if (kStages == 2) {  // the other stage was left by all before the last tile's maxima
-            load(next_r, next_c, at ^ 1);
             at ^= 1;
+            load(next_r, next_c, at, more);
         }
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         __syncthreads();  // this tile's inputs have landed, and the last one's codes are all there
@@ -256,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
             }
             const uint32_t gq = *reinterpret_cast<const uint32_t*>(&st.gu[0][y][lane * 4]);
             const uint32_t uq = *reinterpret_cast<const uint32_t*>(&st.gu[1][y][lane * 4]);
-            const float2 f = *reinterpret_cast<const float2*>(st.factor[y]);
-            const uint64_t sg = pack2(f.x, f.x), su = pack2(f.y, f.y);
+            const float fg = factors[2 * y][tc % kGroup], fu = factors[2 * y + 1][tc % kGroup];
+            const uint64_t sg = pack2(fg, fg), su = pack2(fu, fu);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint64_t g = values2(gq >> (16 * j), sg), u = values2(uq >> (16 * j), su);
@@ -281,30 +323,10 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
             }
             *reinterpret_cast<float4*>(&sm.most[k][warp][lane * 4]) = make_float4(m[0], m[1], m[2], m[3]);
         }
-        __syncthreads();
-        if (kStages == 1) load(next_r, next_c, 0);
-
-        // ---- scales of the columns, a thread each; meanwhile the rows
-        if (columns && threadIdx.x < 3 * kTile) {
-            const int k = threadIdx.x / kTile, col = threadIdx.x % kTile;
-            float most = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; w += 2) most = max_abs3(most, sm.most[k][w][col], sm.most[k][w + 1][col]);
-            const uint32_t m = __float_as_uint(most);
-            float scale, factor;
-            if (k < 2) scale_from_amax<FMT>(most, 0, &scale, &factor);
-            else scale_from_amax<kE4M3>(most, 0, &scale, &factor);
-            // the sign, which no scale has, marks a tile with Inf or NaN
-            sm.scale[k][col] = m >= 0x7F800000u ? -scale : scale;
-            const int c = tc * kTile + col;
-            float* const out = k < 2 ? p.sdgu_t : p.sh_t;
-            if (out != nullptr && c < p.n) out[wide((k == 1 ? (uint32_t)p.n : 0u) + c, rb) + tr] = factor;
-        }
-        // A warp's row maxima are the same in all lanes: they go through shared memory four words
-        // at a time, lane 2 i + k derives the scale of row i of dg (k 0) or du (k 1), and all
-        // come back the same way (fewer instructions than selects and shuffles).
-        if (p.dgu != nullptr) {
-            float* const exchange = sm.exchange[warp];
+        // A warp's row maxima are the same in all lanes, and go through shared memory four words
+        // at a time (fewer instructions than selects and shuffles): 2 i + k of row i of dg (k 0) or du.
+        float* const exchange = sm.exchange[warp];
+        {
             uint32_t most[2 * kRows];
 #pragma unroll
             for (int i = 0; i < 2 * kRows; ++i) {
@@ -316,17 +338,43 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
                 for (int i = 0; i < 2 * kRows; i += 4)
                     *reinterpret_cast<uint4*>(exchange + i) = make_uint4(most[i], most[i + 1], most[i + 2], most[i + 3]);
             }
-            __syncwarp();
-            uint32_t top = 0;
-            if (lane < 2 * kRows) {
-                const float amax = exchange[lane];
-                float factor, scale;
-                scale_from_amax<FMT>(amax, 0, &scale, &factor);
-                top = __float_as_uint(amax);
-                exchange[lane] = scale;
-                if ((lane >> 1) < rows) p.sdgu[wide(2 * r0 + lane, nb) + tc] = factor;
+        }
+        __syncthreads();
+        if (more && (last_of_group || !p.factors_in)) load_factors(p, sm.factor_in[next_group], next_r, next_c, nb, p.factors_in);
+        load(next_r, next_c, 0, kStages == 1 && more);
+
+        // ---- scales: a warp's 16 of its rows, and the tile's 384 of columns, a thread each, in one
+        // chain of divisions.  The sign, which no scale has, marks a tile with Inf or NaN.
+        {
+            const int k = threadIdx.x / kTile, col = threadIdx.x % kTile;  // (k 3: no column)
+            float most = 0.0f;
+            if (k < 3) {
+#pragma unroll
+                for (int w = 0; w < kWarps; w += 2) most = max_abs3(most, sm.most[k][w][col], sm.most[k][w + 1][col]);
             }
-            const bool special = __any_sync(0xFFFFFFFFu, top >= 0x7F800000u);
+            const float amax = exchange[lane % (2 * kRows)];
+            float scale, factor, row_scale, row_factor;
+            scale_of(most, FMT == kE5M2 && k < 2, &scale, &factor);
+            scale_of(amax, FMT == kE5M2, &row_scale, &row_factor);
+            __syncwarp();
+            if (lane < 2 * kRows) {
+                exchange[lane] = __float_as_uint(amax) >= 0x7F800000u ? -row_scale : row_scale;
+                sm.factor_out[warp * 2 * kRows + lane][tc % kGroup] = row_factor;
+            }
+            if (k < 3) {
+                sm.scale[k][col] = __float_as_uint(most) >= 0x7F800000u ? -scale : scale;
+                const int c = tc * kTile + col;
+                float* const out = k < 2 ? p.sdgu_t : p.sh_t;
+                if (out != nullptr && c < p.n) out[wide((k == 1 ? (uint32_t)p.n : 0u) + c, rb) + tr] = factor;
+            }
+        }
+        __syncthreads();
+
+        if (p.dgu != nullptr && (last_of_group || !more)) store_factors(p, sm.factor_out, tr, tc, nb, first);
+        if (last_of_group) first = 0;
+
+        // ---- codes along the rows
+        if (p.dgu != nullptr) {
             uint8_t* q = p.dgu + wide(2 * r0, p.n) + c0;
             const auto codes = [&](auto store) {
 #pragma unroll
@@ -336,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
 #pragma unroll
                     for (int i = 0; i < 4; ++i, q += p.n) {
                         const float (&v)[4] = i & 1 ? du[(i0 + i) >> 1] : dg[(i0 + i) >> 1];
-                        const float2 a = fmul2_rn(v[0], v[1], s[i]), b = fmul2_rn(v[2], v[3], s[i]);
-                        store((i0 + i) >> 1, codes4<FMT>(a.x, a.y, b.x, b.y, special));
+                        const float2 a = fmul2_rn(v[0], v[1], fabsf(s[i])), b = fmul2_rn(v[2], v[3], fabsf(s[i]));
+                        store((i0 + i) >> 1, codes4<FMT>(a.x, a.y, b.x, b.y, s[i] < 0.0f));
                     }
                 }
             };
@@ -352,7 +400,6 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
                 });
         }
         if (!columns) continue;
-        __syncthreads();
 
         // ---- transposed codes: products of two columns at a time, codes of four rows
 #pragma unroll
@@ -442,6 +489,9 @@ extern "C" fp8_status_t fp8_gated_block_backward(const void* dh, fp8_dtype_t dty
         return n % columns == 0 && aligned(gu, columns) && aligned(dh, bytes < 16 ? bytes : 16);
     };
     p.copy_in = copies(16) ? 16 : copies(4) ? 4 : 0;
+    const bool pieces = (n + kTile - 1) / kTile % kGroup == 0;
+    p.factors_in = pieces && aligned16(scale_inv_gu);
+    p.factors_out = pieces && aligned16(scale_inv_dgu);
     p.words_out = n % 4 == 0 && aligned(dgu, 4);
     p.pieces_t = rows % 16 == 0 && aligned16(dgu_t) && aligned16(h_t);
     return run(fn, p, dtype == FP8_DT_FP32, (int)fmt_grad, (int)act, static_cast<cudaStream_t>(stream));
