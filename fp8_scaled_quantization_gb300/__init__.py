@@ -362,10 +362,14 @@ def _operand(q, scale_inv, shape, scale_shape, name):
 
 
 def _ptrs(*tensors):
-    """Data pointers of contiguous tensors on the current CUDA device (one look at the device for all)."""
+    """Data pointers of contiguous tensors on the current CUDA device (one look at the device for
+    all); None for None (not the first one)."""
     here = torch.cuda.current_device() if tensors[0].is_cuda else None
     out = []
     for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
         if t.get_device() != here or not t.is_contiguous():
             _p(t)  # says what is wrong with it
         out.append(t.data_ptr() or None)
@@ -439,14 +443,14 @@ def fp8_gemm_block_grouped_wgrad(a, scale_inv_a, b, scale_inv_b, group_ends, d, 
                                                   int(accumulate), _stream(stream)))
 
 
-def _codes(q, scale_inv, shape, scale_shape, name):
-    """Pointers of an optional pair of codes and scales of these shapes."""
+def _pair(q, scale_inv, shape, scale_shape, name):
+    """The tensors of an optional pair of codes and scales of these shapes, as a tuple of two or none."""
     if q is None and scale_inv is None:
-        return None, None
+        return ()
     if q is None or scale_inv is None:
         raise ValueError(f"{name} and scale_inv_{name} go together")
     _operand(q, scale_inv, shape, scale_shape, name)
-    return _ptrs(q, scale_inv)
+    return q, scale_inv
 
 
 def fp8_gemm_block_gated(a, scale_inv_a, b, scale_inv_b, h, scale_inv_h, gu=None, scale_inv_gu=None, fmt_a=E4M3,
@@ -460,8 +464,8 @@ def fp8_gemm_block_gated(a, scale_inv_a, b, scale_inv_b, h, scale_inv_h, gu=None
     _operand(a, scale_inv_a, (m, k), (m, kb), "a")
     _operand(b, scale_inv_b, (2, n, k), (2, nb, kb), "b")
     _operand(h, scale_inv_h, (m, n), (m, nb), "h")
-    pgu, psgu = _codes(gu, scale_inv_gu, (m, 2, n), (m, 2, nb), "gu")
-    pa, psa, pb, psb, ph, psh = _ptrs(a, scale_inv_a, b, scale_inv_b, h, scale_inv_h)
+    pa, psa, pb, psb, ph, psh, pgu, psgu = _ptrs(a, scale_inv_a, b, scale_inv_b, h, scale_inv_h,
+                                                 *_pair(gu, scale_inv_gu, (m, 2, n), (m, 2, nb), "gu") or (None, None))
     _check(library().fp8_gemm_block_gated(pa, fmt_a, psa, pb, fmt_b, psb, act, m, n, k, ph, psh, pgu, psgu,
                                           _stream(stream)))
 
@@ -478,8 +482,9 @@ def fp8_gemm_block_gated_grouped(a, scale_inv_a, b, scale_inv_b, group_ends, h, 
     _operand(a, scale_inv_a, (rows, k), (rows, kb), "a")
     _operand(b, scale_inv_b, (groups, 2, n, k), (groups, 2, nb, kb), "b")
     _operand(h, scale_inv_h, (rows, n), (rows, nb), "h")
-    pgu, psgu = _codes(gu, scale_inv_gu, (rows, 2, n), (rows, 2, nb), "gu")
-    ends, pa, psa, pb, psb, ph, psh = _ptrs(group_ends, a, scale_inv_a, b, scale_inv_b, h, scale_inv_h)
+    ends, pa, psa, pb, psb, ph, psh, pgu, psgu = _ptrs(
+        group_ends, a, scale_inv_a, b, scale_inv_b, h, scale_inv_h,
+        *_pair(gu, scale_inv_gu, (rows, 2, n), (rows, 2, nb), "gu") or (None, None))
     _check(library().fp8_gemm_block_gated_grouped(groups, ends, pa, fmt_a, psa, pb, fmt_b, psb, act, rows, n, k, ph,
                                                   psh, pgu, psgu, _stream(stream)))
 
@@ -492,10 +497,11 @@ def fp8_gated_block_backward(dh, gu, scale_inv_gu, dgu=None, scale_inv_dgu=None,
     rows, n = _rows_cols(dh)
     nb, rb = -(-n // 128), -(-rows // 128)
     _operand(gu, scale_inv_gu, (rows, 2, n), (rows, 2, nb), "gu")
-    outs = (*_codes(dgu, scale_inv_dgu, (rows, 2, n), (rows, 2, nb), "dgu"),
-            *_codes(dgu_t, scale_inv_dgu_t, (2, n, rows), (2, n, rb), "dgu_t"),
-            *_codes(h_t, scale_inv_h_t, (n, rows), (n, rb), "h_t"))
-    pd, pgu, psgu = _ptrs(dh, gu, scale_inv_gu)
+    none = (None, None)
+    pd, pgu, psgu, *outs = _ptrs(dh, gu, scale_inv_gu,
+                                 *_pair(dgu, scale_inv_dgu, (rows, 2, n), (rows, 2, nb), "dgu") or none,
+                                 *_pair(dgu_t, scale_inv_dgu_t, (2, n, rows), (2, n, rb), "dgu_t") or none,
+                                 *_pair(h_t, scale_inv_h_t, (n, rows), (n, rb), "h_t") or none)
     _check(library().fp8_gated_block_backward(pd, _dt(dh), pgu, psgu, act, rows, n, fmt_grad, *outs, _stream(stream)))
 
 

@@ -16,6 +16,8 @@ call into the CUDA library.
   BlockLinearStep    "Low Precision Training and Rollout" / "Megatron FP8" §6, §21: one training step of
                      a layer (or of an MoE layer's experts) in block-scaled FP8 -- quantize, the
                      forward product, both gradients, and the clipped weight gradient
+  GatedBlockStep     the same of a gated feed-forward block (or of an MoE layer's experts), its
+                     projections kept as an 8-bit checkpoint for the backward pass
   GradientQDQ        E5M2 current scaling then fp8_dequantize back to BF16, per tensor or
                      with one grouped amax + scale call over all tensors (§21)
 """
@@ -28,7 +30,8 @@ import torch
 from . import (AMAX_MAX, B_KN, E4M3, E5M2, fp8_amax, fp8_amax_grouped, fp8_dequantize, fp8_quantize, fp8_quantize_block,
                fp8_quantize_cast_transpose, fp8_quantize_current, fp8_quantize_delayed, fp8_quantize_grouped,
                fp8_update_scale_delayed)
-from . import (fp8_gemm_block, fp8_gemm_block_grouped, fp8_gemm_block_grouped_wgrad, fp8_grad_clip_grouped,
+from . import (ACT_SILU, fp8_gated_block_backward, fp8_gemm_block, fp8_gemm_block_gated, fp8_gemm_block_gated_grouped,
+               fp8_gemm_block_grouped, fp8_gemm_block_grouped_wgrad, fp8_grad_clip_grouped,
                fp8_quantize_block_cast_transpose)
 
 
@@ -266,6 +269,120 @@ class BlockLinearStep:
         b.add("dgrad", rows * out + scales[out] + codes + blocks + rows * inn * 2)
         b.add("wgrad", rows * (out + inn) + columns[out] + columns[inn] + w.numel() * 4)
         b.add("clip", w.numel() * 4 * 2)
+        return b
+
+
+class GatedBlockStep:
+    """The training step of a gated feed-forward block in block-scaled FP8,
+      y = (act(x Wg^T) * (x Wu^T)) Wd^T:
+      quantize   both weights (128 x 128 blocks), x (1 x 128 tiles, both directions)
+      forward    h as FP8 codes from one call, with both projections kept as an 8-bit checkpoint
+      down       y = h Wd^T
+      quantize   dy (both directions)
+      dh         = dy Wd, in BF16
+      backward   gradients of both projections from dh and the checkpoint, along their rows and
+                 transposed, and h transposed
+      dx         = dg Wg + du Wu, one product over both
+      wgrad      dWg and dWu in one product, dWd, in fp32
+      clip       all of them to `max_norm`, in place
+    gate_up [2, hidden, in] (gate, then up) and down [in, hidden] are one block's weights;
+    with a leading experts axis and group_ends (int64 [experts], device: rows of x and dy
+    sorted by expert) they are an MoE layer's.  hidden must be a multiple of 128 (both
+    projections' codes are one operand of the backward products), with experts in too."""
+
+    def __init__(self, x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, dy: torch.Tensor,
+                 group_ends: torch.Tensor = None, act: int = ACT_SILU, fmt: int = E4M3, grad_fmt: int = E4M3,
+                 max_norm: float = 1.0):
+        experts = group_ends is not None
+        if gate_up.dim() != 3 + experts or down.dim() != 2 + experts:
+            raise ValueError("gate_up [experts, 2, hidden, in] and down [experts, in, hidden] go with group_ends, "
+                             "[2, hidden, in] and [in, hidden] without")
+        two, hidden, inn = gate_up.shape[-3:]
+        if two != 2 or down.shape != (*gate_up.shape[:-3], inn, hidden):
+            raise ValueError("gate_up must be [.., 2, hidden, in] and down [.., in, hidden]")
+        if hidden % 128 or (experts and inn % 128):
+            raise ValueError("hidden must be a multiple of 128, and with experts in too")
+        self.x, self.gate_up, self.down, self.dy, self.ends = x, gate_up, down, dy, group_ends
+        self.act, self.fmt, self.grad_fmt, self.max_norm = act, fmt, grad_fmt, max_norm
+        dev, rows, nb, kb, rb = x.device, x.shape[0], hidden // 128, -(-inn // 128), -(-x.shape[0] // 128)
+
+        def u8(*shape):
+            return torch.empty(shape, dtype=torch.uint8, device=dev)
+
+        def both(c):  # rowwise and columnwise codes with their factors
+            return [u8(rows, c), _f32(dev, (rows, -(-c // 128))), u8(c, rows), _f32(dev, (c, rb))]
+
+        self.qx, self.qdy = both(inn), both(inn)
+        self.qgu, self.sgu_w = u8(*gate_up.shape), _f32(dev, (*gate_up.shape[:-2], nb, kb))
+        self.qd, self.sd_w = u8(*down.shape), _f32(dev, (*down.shape[:-2], kb, nb))
+        self.h, self.kept = [u8(rows, hidden), _f32(dev, (rows, nb))], [u8(rows, 2, hidden), _f32(dev, (rows, 2, nb))]
+        self.grads = [u8(rows, 2, hidden), _f32(dev, (rows, 2, nb)), u8(2, hidden, rows), _f32(dev, (2, hidden, rb)),
+                      u8(hidden, rows), _f32(dev, (hidden, rb))]
+        self.y = torch.empty((rows, inn), dtype=torch.bfloat16, device=dev)
+        self.dh = torch.empty((rows, hidden), dtype=torch.bfloat16, device=dev)
+        self.dx = torch.empty((rows, inn), dtype=torch.bfloat16, device=dev)
+        self.dgate_up, self.ddown = _f32(dev, gate_up.shape), _f32(dev, down.shape)
+        self.norm = _f32(dev)
+
+    def _quantize(self, w, q, s):
+        fp8_quantize_block(w.view(-1, w.shape[-1]), 128, 128, self.fmt, q.view(-1, w.shape[-1]), s.view(-1, s.shape[-1]))
+
+    def _forward(self):
+        args = (*self.qx[:2], self.qgu, self.sgu_w)
+        if self.ends is None:
+            fp8_gemm_block_gated(*args, *self.h, *self.kept, self.fmt, self.fmt, self.act)
+        else:
+            fp8_gemm_block_gated_grouped(*args, self.ends, *self.h, *self.kept, self.fmt, self.fmt, self.act)
+
+    def _product(self, a, sa, fmt_a, w, sw, d, layout):
+        if self.ends is None:
+            fp8_gemm_block(a, sa, w, sw, d, fmt_a, self.fmt, b_layout=layout)
+        else:
+            fp8_gemm_block_grouped(a, sa, w, sw, self.ends, d, fmt_a, self.fmt, b_layout=layout)
+
+    def _wgrad(self, a, sa, fmt_a, b, sb, fmt_b, d):
+        if self.ends is None:
+            fp8_gemm_block(a, sa, b, sb, d, fmt_a, fmt_b, b_block_rows=1)
+        else:
+            fp8_gemm_block_grouped_wgrad(a, sa, b, sb, self.ends, d, fmt_a, fmt_b)
+
+    def run(self, timer=None):
+        rows, lead = self.x.shape[0], self.gate_up.shape[:-3]
+        hidden, inn = self.gate_up.shape[-2:]
+        dgu, sdgu, dgu_t, sdgu_t, h_t, sh_t = self.grads
+        one_gu = (self.qgu.view(*lead, 2 * hidden, inn), self.sgu_w.view(*lead, hidden // 64, -1))  # one [2 hidden, in] weight
+        _t(timer, "quantize_weight", lambda: (self._quantize(self.gate_up, self.qgu, self.sgu_w),
+                                              self._quantize(self.down, self.qd, self.sd_w)))
+        _t(timer, "quantize_x", lambda: fp8_quantize_block_cast_transpose(self.x, self.fmt, *self.qx))
+        _t(timer, "forward", self._forward)
+        _t(timer, "down", lambda: self._product(*self.h, E4M3, self.qd, self.sd_w, self.y, 0))
+        _t(timer, "quantize_dy", lambda: fp8_quantize_block_cast_transpose(self.dy, self.grad_fmt, *self.qdy))
+        _t(timer, "dh", lambda: self._product(*self.qdy[:2], self.grad_fmt, self.qd, self.sd_w, self.dh, B_KN))
+        _t(timer, "backward", lambda: fp8_gated_block_backward(self.dh, *self.kept, *self.grads, self.grad_fmt, self.act))
+        _t(timer, "dx", lambda: self._product(dgu.view(rows, -1), sdgu.view(rows, -1), self.grad_fmt, *one_gu, self.dx, B_KN))
+        _t(timer, "wgrad_gate_up", lambda: self._wgrad(dgu_t.view(2 * hidden, rows), sdgu_t.view(2 * hidden, -1),
+                                                       self.grad_fmt, *self.qx[2:], self.fmt,
+                                                       self.dgate_up.view(*lead, 2 * hidden, inn)))
+        _t(timer, "wgrad_down", lambda: self._wgrad(*self.qdy[2:], self.grad_fmt, h_t, sh_t, E4M3, self.ddown))
+        _t(timer, "clip", lambda: fp8_grad_clip_grouped([self.dgate_up, self.ddown], self.max_norm, self.norm))
+
+    def bytes(self) -> KernelBytes:
+        b, rows = KernelBytes(), self.x.shape[0]
+        hidden, inn = self.gate_up.shape[-2:]
+        sizes = lambda *ts: sum(t.numel() * t.element_size() for t in ts)  # noqa: E731
+        weights = (self.qgu, self.sgu_w), (self.qd, self.sd_w)
+        b.add("quantize_weight", sizes(self.gate_up, *weights[0]))
+        b.add("quantize_weight", sizes(self.down, *weights[1]))
+        b.add("quantize_x", sizes(self.x, *self.qx))
+        b.add("forward", sizes(*self.qx[:2], *weights[0], *self.h, *self.kept))
+        b.add("down", sizes(*self.h, *weights[1], self.y))
+        b.add("quantize_dy", sizes(self.dy, *self.qdy))
+        b.add("dh", sizes(*self.qdy[:2], *weights[1], self.dh))
+        b.add("backward", sizes(self.dh, *self.kept, *self.grads))
+        b.add("dx", sizes(*self.grads[:2], *weights[0], self.dx))
+        b.add("wgrad_gate_up", sizes(*self.grads[2:4], *self.qx[2:], self.dgate_up))
+        b.add("wgrad_down", sizes(*self.qdy[2:], *self.grads[4:], self.ddown))
+        b.add("clip", 2 * sizes(self.dgate_up, self.ddown))
         return b
 
 

@@ -145,3 +145,28 @@ def test_reference_slope_against_differences(act):
     usual = g / (1 + torch.exp(-g)) if act == G.SILU else 0.5 * g * (1 + torch.tanh(0.7978845608028654 * (g + 0.044715 * g ** 3)))
     assert ((a - usual).abs() <= 1e-13 * (1 + g.abs())).all()
     assert slope.abs().max() < 1.2
+
+
+def test_gated_block_step_refuses_and_accounts():
+    from fp8_scaled_quantization_gb300 import pipelines as P
+    meta = torch.device("meta")
+    mk = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=meta)  # noqa: E731
+    ends = torch.empty(2, dtype=torch.int64, device=meta)
+    with pytest.raises(ValueError, match="group_ends"):
+        P.GatedBlockStep(mk(8, 256), mk(2, 2, 128, 256), mk(2, 256, 128), mk(8, 256))
+    with pytest.raises(ValueError, match="group_ends"):
+        P.GatedBlockStep(mk(8, 256), mk(2, 128, 256), mk(256, 128), mk(8, 256), ends)
+    with pytest.raises(ValueError, match="gate_up must be"):
+        P.GatedBlockStep(mk(8, 256), mk(3, 128, 256), mk(256, 128), mk(8, 256))
+    with pytest.raises(ValueError, match="gate_up must be"):
+        P.GatedBlockStep(mk(8, 256), mk(2, 128, 256), mk(128, 256), mk(8, 256))
+    with pytest.raises(ValueError, match="multiple of 128"):
+        P.GatedBlockStep(mk(8, 256), mk(2, 100, 256), mk(256, 100), mk(8, 256))
+    with pytest.raises(ValueError, match="multiple of 128"):
+        P.GatedBlockStep(mk(8, 200), mk(2, 2, 128, 200), mk(2, 200, 128), mk(8, 200), ends)
+    b = P.GatedBlockStep(mk(512, 256), mk(2, 128, 256), mk(256, 128), mk(512, 256)).bytes()
+    t, k, n = 512, 256, 128
+    assert b.per_kernel["forward"] == (t * k + 4 * t * 2 + 2 * n * k + 4 * 4 + 3 * (t * n + 4 * t), 1)
+    assert b.per_kernel["backward"] == (t * n * (2 + 2 + 2 + 2 + 1) + 4 * t * 4 + 4 * 3 * n * 4, 1)
+    assert b.per_kernel["dx"] == (2 * t * n + 4 * 2 * t + 2 * n * k + 4 * 4 + 2 * t * k, 1)
+    assert b.per_kernel["clip"] == (3 * n * k * 8, 1) and b.launches == 12
