@@ -43,7 +43,7 @@ struct Backward {
     int copy_in;         // columns of dh and gu that one asynchronous copy takes: 16, 4 (aligned to that) or 0
     bool factors_in, factors_out;  // four tiles' factors of a row lie in aligned pieces of 16 bytes
     bool words_out;      // 4 columns store to dgu as an aligned word
-    bool pieces_t;       // transposed rows are multiples of 16 bytes, 16-byte aligned
+    bool pieces_t, words_t;  // transposed rows are multiples of 16 (4) bytes, and aligned to that
 };
 
 // A 64-bit product of two sizes or indexes, none of them negative.
@@ -121,7 +121,7 @@ __device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int 
         load_pieces<4>(p, s, r0, c0);
     } else {
         const int x = threadIdx.x % kTile;
-#pragma unroll 1
+#pragma unroll 8
         for (int y = threadIdx.x / kTile; y < kTile; y += kThreads / kTile) {
             const bool there = r0 + y < p.rows && c0 + x < p.n;
             const int64_t row = wide(r0 + y, p.n), at = row + c0 + x;
@@ -194,26 +194,30 @@ __device__ __forceinline__ void write_columns(const Backward& p, const uint8_t (
                 const uint4 v = *reinterpret_cast<const uint4*>(&codes[k][piece_at(col + step * 64, 2 * piece) & ~15u]);
                 if (step * 64 < left) stg_stream(q, warp & 1 ? make_uint4(v.z, v.w, v.x, v.y) : v);
             }
-        } else {  // a column per warp and step, 4 bytes of it per lane
-#pragma unroll 1
-            for (int col = warp; col < there; col += kWarps) {
-                uint8_t* const q = base + wide(col, p.rows);
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(&codes[k][piece_at(col, lane >> 1) + (lane & 1) * 4]);
-                const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, w, 1);
-                const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(q) & 3u);
-                if (rows == kTile && off + lane > 0) {
-                    // the aligned word that starts `off` bytes before this lane's
-                    if (lane > 0) *reinterpret_cast<uint32_t*>(q + lane * 4 - off) = __funnelshift_l(before, w, 8 * off);
-                    if (lane == 0 || lane == 31)
+        } else {  // a column per warp, 4 bytes of it per lane, all columns at once
+            constexpr int kEach = kTile / kWarps;
+            uint32_t w[kEach];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)  // the first one's last bytes, the last one's first
-                            if (lane == 0 ? i < 4 - (int)off : i >= 4 - (int)off) q[lane * 4 + i] = (uint8_t)(w >> (8 * i));
-                } else if (rows == kTile) {
-                    *reinterpret_cast<uint32_t*>(q) = w;
-                } else {
+            for (int i = 0; i < kEach; ++i)
+                w[i] = *reinterpret_cast<const uint32_t*>(&codes[k][piece_at(i * kWarps + warp, lane >> 1) + (lane & 1) * 4]);
+            uint8_t* q = base + wide(warp, p.rows) + lane * 4;
+            if (p.words_t) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (lane * 4 + i < rows) q[lane * 4 + i] = (uint8_t)(w >> (8 * i));
+                for (int i = 0; i < kEach; ++i, q += wide(kWarps, p.rows))
+                    if (i * kWarps + warp < there && lane * 4 < rows) *reinterpret_cast<uint32_t*>(q) = w[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < kEach; ++i, q += wide(kWarps, p.rows)) {
+                    // the aligned word that starts `off` bytes before this lane's, where it lies in the
+                    // column; the column's first and last bytes, which share words with others, one by one
+                    const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, w[i], 1);
+                    const int off = (int)(reinterpret_cast<uintptr_t>(q) & 3u), left = rows - lane * 4;
+                    if (i * kWarps + warp >= there) continue;
+                    if ((lane > 0 || off == 0) && left >= 4 - off) *reinterpret_cast<uint32_t*>(q - off) = __funnelshift_l(before, w[i], 8 * off);
+                    const int head = lane == 0 ? -off & 3 : 0, tail = left - ((rows + off) & 3);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (x < left && (x < head || x >= tail)) q[x] = (uint8_t)(w[i] >> (8 * x));
                 }
             }
         }
@@ -493,6 +497,7 @@ extern "C" fp8_status_t fp8_gated_block_backward(const void* dh, fp8_dtype_t dty
     p.factors_in = pieces && aligned16(scale_inv_gu);
     p.factors_out = pieces && aligned16(scale_inv_dgu);
     p.words_out = n % 4 == 0 && aligned(dgu, 4);
+    p.words_t = rows % 4 == 0 && aligned(dgu_t, 4) && aligned(h_t, 4);
     p.pieces_t = rows % 16 == 0 && aligned16(dgu_t) && aligned16(h_t);
     return run(fn, p, dtype == FP8_DT_FP32, (int)fmt_grad, (int)act, static_cast<cudaStream_t>(stream));
 }
