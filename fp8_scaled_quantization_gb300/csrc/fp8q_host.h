@@ -43,6 +43,11 @@ fp8_status_t encode_tile_map_u8(CUtensorMap* map, const void* base, int64_t inne
 // swizzle.
 fp8_status_t encode_out_map(CUtensorMap* map, void* base, bool f32, int64_t cols, int64_t rows, int64_t groups);
 
+// Tensor map of codes [rows, groups, cols] (16-byte aligned base, cols a multiple of
+// 16), written as 32 rows of box_cols bytes (128 or 64) of one group in the swizzle
+// of that width.
+fp8_status_t encode_code_map(CUtensorMap* map, void* base, int64_t cols, int64_t groups, int64_t rows, int box_cols);
+
 // The wait-timeout counter of the pipelined kernels' translation unit on the
 // current device (no synchronisation: call after the device is idle).
 fp8_status_t block_ct_wait_timeouts(unsigned long long* count);

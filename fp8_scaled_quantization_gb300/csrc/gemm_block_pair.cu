@@ -352,8 +352,9 @@ __device__ __forceinline__ void store_tile(const GemmProblem& p, const CUtensorM
 // (h).  Each of the two warps passes half of its columns to the other through the
 // staging buffers and computes h for 64 columns.
 
-// `WORDS` words of E4M3 codes (v * scale, four per word) of a lane's row to the
-// warp's staging buffer, whose rows are 4 * WORDS bytes.
+// A lane's row of `WORDS` words of E4M3 codes (v * scale, four per word) goes through the
+// warp's staging buffer, whose rows are 4 * WORDS bytes, swizzled as the bulk copies
+// of 128 and 64 bytes a row expect it.
 template <int WORDS>
 __device__ __forceinline__ uint32_t staged(uint32_t stage, int row, int piece) {
     const int swizzle = WORDS == 32 ? row & 7 : row >> 1 & 3;  // 16-byte pieces: rows spread over the banks
@@ -429,13 +430,12 @@ __device__ __forceinline__ float tile_scale(uint32_t amax_bits, float* factor) {
     return s;
 }
 
-// h for the 64 columns that this lane keeps (the first of a gate warp, the last of an up
-// warp), into its sums; the other warp's half of them at `theirs`.  Their largest |h|.
+// h for 32 of the 64 columns that this lane keeps (the first 64 of a gate warp, the last of
+// an up warp), into its sums; the other warp's half of them at `theirs`.  The largest |h|.
 template <int ACT, int HALF>
-__device__ __forceinline__ uint32_t gate_columns(float* v, uint32_t theirs, int lane) {
-    float most = 0.0f;
+__device__ __forceinline__ float gate_columns(float* v, uint32_t theirs, int lane, float most) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < 8; ++j) {
         float o[4];
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                      : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
@@ -443,21 +443,30 @@ __device__ __forceinline__ uint32_t gate_columns(float* v, uint32_t theirs, int 
                      : "memory");
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-            float* const x = v + HALF * 64 + j * 4 + i;
+            float* const x = v + j * 4 + i;
             const uint64_t a = pack2(x[0], x[1]), b = pack2(o[i], o[i + 1]);
             const float2 h = unpack2(HALF == 0 ? gated2<ACT>(a, b) : gated2<ACT>(b, a));
             x[0] = h.x, x[1] = h.y;
             most = max_abs3(most, h.x, h.y);
         }
     }
-    return __float_as_uint(most);
+    return most;
+}
+
+// 32 rows of codes at `stage` to the output by the bulk-copy engine.
+__device__ __forceinline__ void bulk_codes(const CUtensorMap* map, int x, int half, int64_t row0, uint32_t stage) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(half), "r"((int)row0), "r"(stage)
+                 : "memory");
 }
 
 // A warp's part of a gated tile: rows row0 .. (at most 32, before row_end), columns col0 ..
 // of h; HALF 0: acc holds the gate's sums, 1: the up projection's.
 template <int HALF>
-__device__ __forceinline__ void store_gated(const GemmProblem& p, Sums<false>& acc, uint32_t (&peer)[2][128], uint32_t stages,
-                                            int warp, int lane, int64_t row0, int64_t row_end, int col0) {
+__device__ __forceinline__ void store_gated(const GemmProblem& p, const CUtensorMap* map_h, const CUtensorMap* map_gu, bool bulk,
+                                            Sums<false>& acc, uint32_t (&peer)[2][128], uint32_t stages, int warp, int lane,
+                                            int64_t row0, int64_t row_end, int col0) {
     const GatedOut& out = p.gated;
     const uint32_t mine = stages + warp * kOuts * kOutBytes, theirs = stages + (warp ^ 4) * kOuts * kOutBytes;
     const int rows = (int)(row_end - row0 < 32 ? row_end - row0 : 32), quarter = warp & 3;  // (rows may be negative)
@@ -467,6 +476,12 @@ __device__ __forceinline__ void store_gated(const GemmProblem& p, Sums<false>& a
 #pragma unroll
         for (int i = 0; i < 128; ++i) acc.v[i] = i < there ? acc.v[i] : 0.0f;
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last tile's codes have been read
+    __syncwarp();
+    const bool async = bulk && rows == 32;  // all rows are in the group
+    // The lower 4 KB of the warp's buffers take the checkpoint's codes, which may leave meanwhile;
+    // the upper ones 32 columns at a time for the other warp, then h's codes.
+    const uint32_t upper = mine + kOutBytes;
     if (out.gu != nullptr) {
         float most[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -475,32 +490,43 @@ __device__ __forceinline__ void store_gated(const GemmProblem& p, Sums<false>& a
         const float scale = tile_scale(__float_as_uint(max_abs3(max_abs3(most[0], most[1], most[2]), most[3], 0.0f)), &factor);
         stage_codes<32>(acc.v, scale, mine, lane);
         if (lane < rows) out.sgu[(row * 2 + HALF) * nb + col0 / kBlk] = factor;
+        if (async) fence_to_async();
         __syncwarp();
-        copy_codes<32>(out.gu + (row0 * 2 + HALF) * p.n + col0, 2 * p.n, mine, lane, rows, there,
-                       unit_of(out.gu, p.n));
-        __syncwarp();
+        if (!async)
+            copy_codes<32>(out.gu + (row0 * 2 + HALF) * p.n + col0, 2 * p.n, mine, lane, rows, there, unit_of(out.gu, p.n));
+        else if (lane == 0)
+            bulk_codes(map_gu, col0, HALF, row0, mine);
     }
+    float largest = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float* const x = acc.v + (1 - HALF) * 64 + j * 4;
-        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + j * 512 + lane * 16), "f"(x[0]), "f"(x[1]),
-                     "f"(x[2]), "f"(x[3])
-                     : "memory");
+    for (int part = 0; part < 2; ++part) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float* const x = acc.v + (1 - HALF) * 64 + part * 32 + j * 4;
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(upper + j * 512 + lane * 16), "f"(x[0]), "f"(x[1]),
+                         "f"(x[2]), "f"(x[3])
+                         : "memory");
+        }
+        group_sync(1 + quarter, 64);
+        float* const x = acc.v + HALF * 64 + part * 32;
+        largest = out.act == kSilu ? gate_columns<kSilu, HALF>(x, theirs + kOutBytes, lane, largest)
+                                   : gate_columns<kGeluTanh, HALF>(x, theirs + kOutBytes, lane, largest);
+        if (part == 1) peer[HALF][quarter * 32 + lane] = __float_as_uint(largest);
+        group_sync(1 + quarter, 64);  // (and the other warp has read this one's columns)
     }
-    group_sync(1 + quarter, 64);
-    uint32_t most = out.act == kSilu ? gate_columns<kSilu, HALF>(acc.v, theirs, lane)
-                                     : gate_columns<kGeluTanh, HALF>(acc.v, theirs, lane);
-    peer[HALF][quarter * 32 + lane] = most;
-    group_sync(1 + quarter, 64);  // (and the other warp has read this one's columns)
-    most = umax(most, peer[1 - HALF][quarter * 32 + lane]);
+    const uint32_t most = umax(__float_as_uint(largest), peer[1 - HALF][quarter * 32 + lane]);
     float factor;
     const float scale = tile_scale(most, &factor);
     if (HALF == 0 && lane < rows) out.sh[row * nb + col0 / kBlk] = factor;
-    stage_codes<16>(acc.v + HALF * 64, scale, mine, lane);
+    stage_codes<16>(acc.v + HALF * 64, scale, upper, lane);
+    if (async) fence_to_async();
     __syncwarp();
-    copy_codes<16>(out.h + row0 * p.n + col0 + HALF * 64, p.n, mine, lane, rows, there - HALF * 64,
-                   unit_of(out.h, p.n));
-    __syncwarp();
+    if (!async) {
+        copy_codes<16>(out.h + row0 * p.n + col0 + HALF * 64, p.n, upper, lane, rows, there - HALF * 64, unit_of(out.h, p.n));
+        __syncwarp();
+    } else if (lane == 0 && there > HALF * 64) {
+        bulk_codes(map_h, col0 + HALF * 64, 0, row0, upper);
+    }
 }
 
 // FORM 0: B [n, k], 128 x 128 blocks; 1: B [k, n], 128 x 128 blocks; 2: both
@@ -508,7 +534,8 @@ __device__ __forceinline__ void store_gated(const GemmProblem& p, Sums<false>& a
 template <int FORM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ CUtensorMap map_a,
-                 const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d, bool bulk_store) {
+                 const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_d,
+                 const __grid_constant__ CUtensorMap map_gu, bool bulk_store) {
     constexpr bool RAGGED_K = FORM == 2, B_KN = FORM == 1, B_TILES = FORM == 2, GATED = FORM == 3;
     constexpr int kTileN = GATED ? kPairN / 2 : kPairN;  // columns of the output
     extern __shared__ uint8_t raw[];
@@ -650,8 +677,10 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
             at_place = (at_place + 1) % kPlaces;
             const int64_t r0 = place.x + (int)rank * 128 + (warp & 3) * 32, c0 = place.z + half * 128;
             if constexpr (GATED) {
-                if (half == 0) store_gated<0>(p, acc, sh.peer, smem_addr(out), warp, lane, r0, place.y, place.z);
-                else store_gated<1>(p, acc, sh.peer, smem_addr(out), warp, lane, r0, place.y, place.z);
+                if (half == 0)
+                    store_gated<0>(p, &map_d, &map_gu, bulk_store, acc, sh.peer, smem_addr(out), warp, lane, r0, place.y, place.z);
+                else
+                    store_gated<1>(p, &map_d, &map_gu, bulk_store, acc, sh.peer, smem_addr(out), warp, lane, r0, place.y, place.z);
             } else {
                 store_tile<B_TILES>(p, &map_d, bulk_store, acc, smem_addr(out) + warp * kOuts * kOutBytes, lane, r0, place.y,
                                     c0, matrix);
@@ -848,20 +877,24 @@ gemm_pair_kernel(const __grid_constant__ GemmProblem p, const __grid_constant__ 
 fp8_status_t run_gemm_pair(const char* fn, const GemmProblem& p, cudaStream_t st) {
     const int64_t inner_b = p.b_kn ? p.n : p.k, rows_b = p.b_kn ? p.k : p.n;
     const bool gated = p.gated.h != nullptr;
-    const bool bulk = !gated && aligned16(p.d) && p.n % (p.out_f32 ? 4 : 8) == 0 && !p.accumulate;
+    const GatedOut& o = p.gated;
+    const bool bulk = gated ? p.n % 16 == 0 && aligned16(o.h) && aligned16(o.gu)
+                            : aligned16(p.d) && p.n % (p.out_f32 ? 4 : 8) == 0 && !p.accumulate;
     const Operand oa = {p.a, p.k, p.m, 1, 128}, ob = {p.b, inner_b, rows_b, p.b_tiles ? 1 : p.groups * (gated ? 2 : 1), 128};
-    CUtensorMap a = {}, b = {}, d = {};
+    CUtensorMap a = {}, b = {}, d = {}, gu = {};
     StreamUse use(st);
     fp8_status_t s = FP8_OK;
     if (p.k > 0) s = operand_maps(fn, oa, &a, ob, &b, use, st);
-    if (bulk && s == FP8_OK) s = encode_out_map(&d, p.d, p.out_f32, p.n, p.m, p.b_tiles ? p.groups : 1);
+    if (bulk && gated && s == FP8_OK) s = encode_code_map(&d, o.h, p.n, 1, p.m, 64);
+    if (bulk && o.gu != nullptr && s == FP8_OK) s = encode_code_map(&gu, o.gu, p.n, 2, p.m, 128);
+    if (bulk && !gated && s == FP8_OK) s = encode_out_map(&d, p.d, p.out_f32, p.n, p.m, p.b_tiles ? p.groups : 1);
     if (s != FP8_OK) return s;
     const int64_t tile_n = gated ? kPairN / 2 : kPairN;
     const int64_t tiles_n = (p.n + tile_n - 1) / tile_n, tiles_m = (p.m + kPairM - 1) / kPairM;
     const int64_t most = p.b_tiles ? tiles_m * tiles_n * p.groups : (tiles_m + p.groups - 1) * tiles_n;
     const int sms = sm_count() / 2, pairs = (int)(most < sms ? most : sms);
     const auto go = [&](auto kernel, size_t smem) {
-        return launch_smem(fn, kernel, dim3(2 * pairs), dim3(kThreads), smem, st, p, a, b, d, bulk);
+        return launch_smem(fn, kernel, dim3(2 * pairs), dim3(kThreads), smem, st, p, a, b, d, gu, bulk);
     };
     return gated     ? go(gemm_pair_kernel<3>, smem_bytes<false>())
            : p.b_tiles ? go(gemm_pair_kernel<2>, smem_bytes<true>())

@@ -168,6 +168,21 @@ fp8_status_t encode_out_map(CUtensorMap* map, void* base, bool f32, int64_t cols
     return FP8_OK;
 }
 
+fp8_status_t encode_code_map(CUtensorMap* map, void* base, int64_t cols, int64_t groups, int64_t rows, int box_cols) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    const fp8_status_t s = tile_map_encoder(&encode);
+    if (s != FP8_OK) return s;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)groups, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols, (cuuint64_t)cols * (cuuint64_t)groups};
+    const cuuint32_t box[3] = {(cuuint32_t)box_cols, 1, 32};
+    const cuuint32_t elem_strides[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, elem_strides,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FP8_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return FP8_OK;
+}
+
 bool StreamUse::take(fp8_status_t* st) {
     *st = FP8_OK;
     if (held_ != nullptr) return true;
