@@ -208,16 +208,23 @@ __device__ __forceinline__ void write_columns(const Backward& p, const uint8_t (
             } else {
 #pragma unroll
                 for (int i = 0; i < kEach; ++i, q += wide(kWarps, p.rows)) {
-                    // the aligned word that starts `off` bytes before this lane's, where it lies in the
-                    // column; the column's first and last bytes, which share words with others, one by one
+                    // the aligned word that starts `off` bytes before this lane's, where it lies in the column
                     const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, w[i], 1);
                     const int off = (int)(reinterpret_cast<uintptr_t>(q) & 3u), left = rows - lane * 4;
-                    if (i * kWarps + warp >= there) continue;
-                    if ((lane > 0 || off == 0) && left >= 4 - off) *reinterpret_cast<uint32_t*>(q - off) = __funnelshift_l(before, w[i], 8 * off);
-                    const int head = lane == 0 ? -off & 3 : 0, tail = left - ((rows + off) & 3);
+                    if (i * kWarps + warp < there && (lane > 0 || off == 0) && left >= 4 - off)
+                        *reinterpret_cast<uint32_t*>(q - off) = __funnelshift_l(before, w[i], 8 * off);
+                }
+                // What is left of a column shares words with others and goes byte by byte: its first
+                // -off mod 4 bytes and its last (rows + off) mod 4, six at most.  A column's on 4 lanes.
+                static_assert(kEach * 4 == 32, "a warp's columns, 4 lanes each");
+                const int col = (lane >> 2) * kWarps + warp;
+                uint8_t* const line = base + wide(col, p.rows);
+                const int off = (int)(reinterpret_cast<uintptr_t>(line) & 3u), head = min(-off & 3, rows);
+                const int tail = min((rows + off) & 3, rows - head);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (x < left && (x < head || x >= tail)) q[x] = (uint8_t)(w[i] >> (8 * x));
+                for (int turn = 0; turn < 2; ++turn) {
+                    const int e = turn * 4 + (lane & 3), x = e < head ? e : rows - tail + e - head;
+                    if (e < head + tail && col < there) line[x] = codes[k][piece_at(col, x >> 3) + (x & 7)];
                 }
             }
         }
