@@ -41,6 +41,7 @@ struct Backward {
     uint8_t* h_t;        // [n, rows] E4M3, factors [n, blocks of rows]; nullable
     float* sh_t;
     int copy_in;         // columns of dh and gu that one asynchronous copy takes: 16, 4 (aligned to that) or 0
+    int run;             // tiles along a row of tiles that a CTA takes one after another: 4 or 1
     bool factors_in, factors_out;  // four tiles' factors of a row lie in aligned pieces of 16 bytes
     bool words_out;      // 4 columns store to dgu as an aligned word
     bool pieces_t, words_t;  // transposed rows are multiples of 16 (4) bytes, and aligned to that
@@ -65,8 +66,8 @@ struct Smem {
     alignas(16) uint8_t codes[3][kTile * kTile];  // transposed codes, 8-byte pieces swizzled
     alignas(16) float exchange[kWarps][2 * kRows];  // row maxima and scales within a warp
     // Factors of four tiles along a row of tiles, in and out, of row i / 2, gate or up projection
-    // i % 2: words that lie a row apart in memory cost a request each (for one tile at a
-    // time 25 us of 122, 4096 x 14336).
+    // i % 2.  Words that lie a row apart in memory cost a request each, and as single words,
+    // which go through L1, more: 139 us for 4096 x 14336, in pieces of four past L1 122.
     alignas(16) float factor_in[2][2 * kTile][kGroup], factor_out[2 * kTile][kGroup];
 };
 
@@ -135,8 +136,8 @@ __device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int 
 // The factors of a tile, or of the four tiles around it where they lie in aligned pieces.
 __device__ __forceinline__ void load_factors(const Backward& p, float (&in)[2 * kTile][kGroup], int tr, int tc, int nb, bool whole) {
     if (threadIdx.x >= 2 * kTile) return;
-    const int at = 2 * tr * kTile + threadIdx.x;
-    const bool there = (at >> 1) < p.rows;
+    const uint32_t at = 2u * tr * kTile + threadIdx.x;
+    const bool there = (int)(at >> 1) < p.rows;
     const float* const from = p.sgu + (there ? wide(at, nb) + tc : 0);
     if (whole) copy_async<16>(in[threadIdx.x], there ? from - tc % kGroup : from, there);
     else copy_async<4>(&in[threadIdx.x][tc % kGroup], from, there);
@@ -145,8 +146,9 @@ __device__ __forceinline__ void load_factors(const Backward& p, float (&in)[2 * 
 // The factors of dg and du of the tiles tc - tc % 4 + first .. tc.
 __device__ __forceinline__ void store_factors(const Backward& p, const float (&out)[2 * kTile][kGroup], int tr, int tc, int nb, int first) {
     if (threadIdx.x >= 2 * kTile) return;
-    const int at = 2 * tr * kTile + threadIdx.x, last = tc % kGroup;
-    if ((at >> 1) >= p.rows) return;
+    const uint32_t at = 2u * tr * kTile + threadIdx.x;
+    const int last = tc % kGroup;
+    if ((int)(at >> 1) >= p.rows) return;
     float* const to = p.sdgu + wide(at, nb) + (tc - last);
     const float4 v = *reinterpret_cast<const float4*>(out[threadIdx.x]);
     if (p.factors_out && first == 0 && last == kGroup - 1) {
@@ -265,9 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
     // (a shuffle tells the compiler that the number is the same in the whole warp)
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int nb = (p.n + kTile - 1) / kTile, rb = (p.rows + kTile - 1) / kTile;
-    // a share of the tiles, one after another along the columns
-    const int total = nb * rb, end = (int)(wide(total, blockIdx.x + 1) / gridDim.x);
-    int t = (int)(wide(total, blockIdx.x) / gridDim.x), tr = t / nb, tc = t % nb;
+    // Runs of p.run tiles along the columns, every gridDim.x-th of them: what the CTAs work on at
+    // one time lies close together, and the pieces of a cache line that two tiles of a column
+    // share meet in L2.  (One long run per CTA: 16400 x 18432 in 1117 us instead of 622.)
+    const int runs = (nb + p.run - 1) / p.run, step_r = gridDim.x / runs, step_c = gridDim.x % runs;
+    int run_r = blockIdx.x / runs, run_c = blockIdx.x % runs, tr = run_r, tc = run_c * p.run;
     pdl_begin();
     const auto load = [&](int r, int c, int stage, bool there) {
         if (there) load_tile<F32>(p, sm.stage[stage], r, c);
@@ -277,12 +281,16 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
     load(tr, tc, 0, true);
     const bool columns = p.dgu_t != nullptr || p.h_t != nullptr;
     int at = 0, last_r = -1, last_c = 0;    // the tile whose transposed codes wait in shared memory
-    int group = 0, first = tc % kGroup;     // the place of this tile's factors, the first one of its four that is this CTA's
-    for (int next_r, next_c, next_group; t < end; ++t, tr = next_r, tc = next_c, group = next_group) {
-        next_r = tr, next_c = tc + 1;
-        if (next_c == nb) next_c = 0, ++next_r;
-        const bool more = t + 1 < end, last_of_group = next_c % kGroup == 0;
-        next_group = last_of_group ? group ^ 1 : group;
+    int group = 0, first = tc % kGroup;     // the place of this run's factors, its first tile of four
+    for (int next_r, next_c, next_group; tr < rb; tr = next_r, tc = next_c, group = next_group) {
+        next_r = tr, next_c = tc + 1, next_group = group;
+        const bool last_of_run = next_c == nb || next_c % p.run == 0;
+        if (last_of_run) {
+            run_r += step_r, run_c += step_c;
+            if (run_c >= runs) run_c -= runs, ++run_r;
+            next_r = run_r, next_c = run_c * p.run, next_group = group ^ 1;
+        }
+        const bool more = next_r < rb;
         const int r0 = tr * kTile + warp * kRows, c0 = tc * kTile + lane * 4;
         const int cols = min(p.n - c0, 4), rows = min(p.rows - r0, kRows);  // here
         const Stage<F32>& st = sm.stage[at];
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
             }
         }
         __syncthreads();
-        if (more && (last_of_group || !p.factors_in)) load_factors(p, sm.factor_in[next_group], next_r, next_c, nb, p.factors_in);
+        if (more && (last_of_run || !p.factors_in)) load_factors(p, sm.factor_in[next_group], next_r, next_c, nb, p.factors_in);
         load(next_r, next_c, 0, kStages == 1 && more);
 
         // ---- scales: a warp's 16 of its rows, and the tile's 384 of columns, a thread each, in one
@@ -381,12 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
         }
         __syncthreads();
 
-        if (p.dgu != nullptr && (last_of_group || !more)) store_factors(p, sm.factor_out, tr, tc, nb, first);
-        if (last_of_group) first = 0;
+        if (last_of_run) {
+            if (p.dgu != nullptr) store_factors(p, sm.factor_out, tr, tc, nb, first);
+            first = next_c % kGroup;
+        }
 
         // ---- codes along the rows
         if (p.dgu != nullptr) {
-            uint8_t* q = p.dgu + wide(2 * r0, p.n) + c0;
+            uint8_t* q = p.dgu + wide(2u * r0, p.n) + c0;
             const auto codes = [&](auto store) {
 #pragma unroll
                 for (int i0 = 0; i0 < 2 * kRows; i0 += 4) {
@@ -446,11 +456,20 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
     }
 }
 
-fp8_status_t run(const char* fn, const Backward& p, bool f32, int fmt, int act, cudaStream_t st) {
-    const int64_t tiles = (int64_t)((p.n + kTile - 1) / kTile) * ((p.rows + kTile - 1) / kTile);
+fp8_status_t run(const char* fn, Backward p, bool f32, int fmt, int act, cudaStream_t st) {
+    // Runs of four tiles share reads and writes of factors (4096 x 14336: 119 us, single tiles 122.5;
+    // 16384 x 18432: 590 and 599), but their last round may leave more CTAs idle (8192 x 2048: 43 and 39).
+    const int64_t nb = (p.n + kTile - 1) / kTile, rb = (p.rows + kTile - 1) / kTile;
     const int sms = sm_count();
+    int64_t ctas = 0;
+    double best = 0.0;
+    for (int run : {4, 1}) {
+        const int64_t runs = (nb + run - 1) / run * rb;
+        const double cost = (double)((runs + sms - 1) / sms) * run * (run == 4 ? 1.0 : 1.02);
+        if (ctas == 0 || cost < best) best = cost, p.run = run, ctas = runs < sms ? runs : sms;
+    }
     const auto go = [&](auto kernel) {
-        return launch_smem(fn, kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kThreads), f32 ? sizeof(Smem<true>) : sizeof(Smem<false>), st, p);
+        return launch_smem(fn, kernel, dim3((unsigned)ctas), dim3(kThreads), f32 ? sizeof(Smem<true>) : sizeof(Smem<false>), st, p);
     };
     const auto pick = [&](auto silu, auto gelu) { return act == kSilu ? go(silu) : go(gelu); };
     if (fmt == kE4M3)

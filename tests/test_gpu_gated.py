@@ -336,6 +336,26 @@ def test_past_32_bits():
     assert (sdgu[:rows - 200] == 1).all() and not (dgu[:64] & 0x7F).any()
 
 
+def test_more_rows_than_half_of_32_bits():
+    """Rows of both projections beyond 2^31: one column, of which the last rows are looked at."""
+    rows = 2 ** 30 + 300
+    gu, sgu = torch.zeros((rows, 2, 1), dtype=torch.uint8, device=DEV), torch.ones((rows, 2, 1), device=DEV)
+    dh = torch.zeros((rows, 1), dtype=torch.bfloat16, device=DEV)
+    r = slice(rows - 300, rows)
+    gu[r], sgu[r] = checkpoint(300, 1, 4)
+    dh[r] = torch.randn((300, 1), generator=gen(1), device=DEV).bfloat16()
+    dgu, sdgu = torch.full((rows, 2, 1), 9, dtype=torch.uint8, device=DEV), torch.zeros((rows, 2, 1), device=DEV)
+    dgu_t, sdgu_t = torch.full((2, 1, rows), 9, dtype=torch.uint8, device=DEV), torch.zeros((2, 1, G.blocks(rows)), device=DEV)
+    fq.fp8_gated_block_backward(dh, gu, sgu, dgu, sdgu, dgu_t, sdgu_t)
+    g, u = (R.values(gu[r, i], sgu[r, i], R.E4M3, 1) for i in (0, 1))
+    (dg, eg), (du, eu), _ = G.backward(dh[r].double(), g, u, G.SILU)
+    first = -(rows - 300) % 128  # from the first tile of a column that lies in these rows whole
+    for i, (v, e) in enumerate(((dg, eg), (du, eu))):
+        G.check_tiles(dgu[r, i], sdgu[r, i], v, e, R.E4M3)
+        G.check_tiles(dgu_t[i][:, rows - 300 + first:], sdgu_t[i][:, (rows - 300 + first) // 128:], v[first:].T, e[first:].T, R.E4M3)
+    assert (sdgu[:2 ** 20] == 1).all() and not (dgu_t[:, :, :2 ** 20] & 0x7F).any()
+
+
 # ---------------------------------------------------------- streams and graphs
 
 def test_on_a_stream_and_in_a_graph():
