@@ -8,7 +8,8 @@ fp32 scalars, int64 saturation counters (read as unsigned 64-bit).
 
 Entry points (same names as the C ABI):
   fp8_amax, fp8_update_scale_delayed, fp8_quantize,
-  fp8_quantize_cast_transpose, fp8_quantize_block, fp8_dequantize.
+  fp8_quantize_cast_transpose, fp8_quantize_block, fp8_dequantize and the others
+  in ``__all__``.
 """
 from __future__ import annotations
 
@@ -382,11 +383,11 @@ def _ends(group_ends):
     return group_ends.shape[0]
 
 
-def _out(d, rows):
+def _out(d, rows, name="d"):
     """Columns of an output [rows, n]."""
     shape = d.shape
     if len(shape) != 2 or shape[0] != rows:
-        raise ValueError(f"d must be [{rows}, n]")
+        raise ValueError(f"{name} must be [{rows}, n]")
     return shape[1]
 
 
@@ -459,7 +460,7 @@ def fp8_gemm_block_gated(a, scale_inv_a, b, scale_inv_b, h, scale_inv_h, gu=None
     factors, b [2, n, k] (gate, up) with 128 x 128 factors each.  gu [m, 2, n]: the checkpoint,
     E4M3 codes (1 x 128 factors) of both projections, which fp8_gated_block_backward reads."""
     m, k = _rows_cols(a)
-    n = _out(h, m)
+    n = _out(h, m, "h")
     kb, nb = -(-k // 128), -(-n // 128)
     _operand(a, scale_inv_a, (m, k), (m, kb), "a")
     _operand(b, scale_inv_b, (2, n, k), (2, nb, kb), "b")
@@ -477,7 +478,7 @@ def fp8_gemm_block_gated_grouped(a, scale_inv_a, b, scale_inv_b, group_ends, h, 
     codes 0 and factors 1.  group_ends: int64 on the device."""
     rows, k = _rows_cols(a)
     groups = _ends(group_ends)
-    n = _out(h, rows)
+    n = _out(h, rows, "h")
     kb, nb = -(-k // 128), -(-n // 128)
     _operand(a, scale_inv_a, (rows, k), (rows, kb), "a")
     _operand(b, scale_inv_b, (groups, 2, n, k), (groups, 2, nb, kb), "b")

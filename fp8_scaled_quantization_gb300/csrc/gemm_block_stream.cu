@@ -11,8 +11,11 @@
 //
 // The gated form gives the gate's weight to the even CTAs of a cluster and the up
 // projection's to the odd ones, each half of them sharing the contraction; both
-// sums of a token meet where they are joined.  (A CTA that streamed both, one
-// after the other, needs twice the sums, and 64 tokens no longer fit an SM twice.)
+// sums of a token meet where they are joined.  A CTA that streamed both, one after the
+// other, needs twice the sums, and 64 tokens no longer fit an SM twice: 48 x 14336 x
+// 4096 (tokens, n, k) in 38 us instead of 33, 16 x 7168 x 7168 in 23 instead of 22.
+// As the plain product with twice the columns takes, so does the gated one: 1 x 18432
+// x 7168 44 us (6.0 TB/s), 96 rows over 64 experts of 2048 x 7168 273 us (6.9 TB/s).
 //
 // Roles per CTA: four warps (eight from 32 tokens on, each pair of them sharing
 // the tokens of 32 columns) scale, add, join and store; then one warp fills the

@@ -611,8 +611,8 @@ fp8_status_t fp8_gemm_block_gated_grouped(int groups, const int64_t* group_ends,
  * each quantized in 1 x 128 tiles from fp32 by the rule of fp8_quantize_block(1,
  * 128): dg and du to fmt_grad along their rows (for the input gradient) and
  * transposed (tiles along the rows of dh; for the weights' gradients), h to E4M3
- * transposed (for the down projection's weight gradient).  Precision of act and
- * act' as above (act' to (|y| + 8) * 2^-22, absolute).
+ * transposed (for the down projection's weight gradient).  act is as precise as
+ * above, act' to (|y| + 8) (1 + |g| y') * 2^-22.
  *
  *   dh               device [rows, n] of dtype (BF16 or fp32), element-aligned.
  *   gu, scale_inv_gu device uint8[rows, 2, n] and float[rows, 2, ceil(n/128)], E4M3.

@@ -96,7 +96,7 @@ def _u8(*s):
     (dict(b=_u8(130, 256)), "b must be uint8"),
     (dict(b=_u8(260, 256)), "b must be uint8"),
     (dict(sb=torch.zeros(3, 2)), "scale_inv_b"),
-    (dict(h=_u8(5, 130)), "d must be"),
+    (dict(h=_u8(5, 130)), "h must be"),
     (dict(h=torch.zeros(4, 130)), "h must be uint8"),
     (dict(sh=torch.zeros(4, 1)), "scale_inv_h"),
     (dict(gu=_u8(4, 2, 130)), "go together"),

@@ -384,3 +384,64 @@ def test_on_a_stream_and_in_a_graph():
     assert all(torch.equal(a, o.flat) for a, o in zip(first, outs + grads))
     check(outs, *projections(*ops), G.SILU)
     check_backward(grads, dh, outs[2].t, outs[3].t, G.SILU, R.E4M3)
+
+
+def test_threads_and_streams_at_once():
+    """Calls that copy odd operands into their stream's scratch, from four host threads on three
+    streams (two threads share one), give what they give alone."""
+    import threading
+    shapes = [(3, 300, 515), (70, 257, 770), (260, 520, 333), (40, 130, 901)]
+    ops = [operands(*s, i + 1) for i, s in enumerate(shapes)]
+    alone, failed = [], []
+
+    def call(i, outs, grads):
+        fq.fp8_gemm_block_gated(*ops[i], *[o.t for o in outs])
+        back(outs[0].t.bfloat16(), outs[2].t, outs[3].t, grads)
+
+    fresh = lambda i: (outputs(*shapes[i][:2], True), gradient_outputs(*shapes[i][:2]))  # noqa: E731
+    for i in range(4):
+        alone.append(fresh(i))
+        call(i, *alone[-1])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i % 3]):
+                for _ in range(20):
+                    outs, grads = fresh(i)
+                    call(i, outs, grads)
+                    streams[i % 3].synchronize()
+                    if not all(torch.equal(a.flat, b.flat) for a, b in zip(outs + grads, alone[i][0] + alone[i][1])):
+                        failed.append(i)
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failed
+
+
+def test_a_captured_call_keeps_its_scratch():
+    """Odd operands of a captured call: larger eager calls on the stream leave the graph's copy alone."""
+    small, large = operands(20, 200, 331, 1), operands(300, 1000, 1501, 2)
+    a, b = outputs(20, 200, False), outputs(300, 1000, False)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fq.fp8_gemm_block_gated(*small, *[o.t for o in a])
+    s.synchronize()
+    first = [o.flat.clone() for o in a]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        fq.fp8_gemm_block_gated(*small, *[o.t for o in a])
+    with torch.cuda.stream(s):
+        fq.fp8_gemm_block_gated(*large, *[o.t for o in b])
+    for o in a:
+        o.t.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, o.flat) for x, o in zip(first, a))
+    check(b, *projections(*large), G.SILU)
