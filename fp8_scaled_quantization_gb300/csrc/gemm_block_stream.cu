@@ -13,7 +13,7 @@
 // projection's to the odd ones, each half of them sharing the contraction; both
 // sums of a token meet where they are joined.  A CTA that streamed both, one after the
 // other, needs twice the sums, and 64 tokens no longer fit an SM twice: 48 x 14336 x
-// 4096 (tokens, n, k) in 38 us instead of 33, 16 x 7168 x 7168 in 23 instead of 22.
+// 4096 (tokens, n, k) took 38 us when this took 33, 16 x 7168 x 7168 23 when this took 22.
 // As the plain product with twice the columns takes, so does the gated one: 1 x 18432
 // x 7168 44 us (6.0 TB/s), 96 rows over 64 experts of 2048 x 7168 273 us (6.9 TB/s).
 //
@@ -152,68 +152,83 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
-// The end of a gated item, of the tokens j0 .. j1 - 1 that this CTA joins: both sums of
-// this lane's column over the cluster (the gate's in even ranks, the up projection's in
-// odd ones), h from them, quantized in tiles of the CTA's 128 columns: four warps, of
-// which the CTA has one set or two that take the tokens in turn.
+// Both sums of token j and this lane's column over the cluster: the gate's in even ranks,
+// the up projection's in odd ones, added in their order.
+template <int TOKENS>
+__device__ __forceinline__ float2 join_gated(const Shared<TOKENS, kGated>& sh, int j, int row, int split) {
+    float x[kMostSplit];
+#pragma unroll
+    for (int r = 0; r < kMostSplit; ++r) x[r] = r < split ? ld_cluster(cluster_addr(smem_addr(&sh.part[j][row]), r)) : 0.0f;
+    float2 v = make_float2(x[0], x[1]);
+#pragma unroll
+    for (int r = 2; r < kMostSplit; r += 2)
+        if (r < split) v.x = __fadd_rn(v.x, x[r]), v.y = __fadd_rn(v.y, x[r + 1]);
+    return v;
+}
+
+// The end of a gated item, of the tokens j0 .. j1 - 1 that this CTA joins: h of this lane's
+// column, quantized in tiles of the CTA's 128 columns, by four warps, of which the CTA has
+// one set or two that take the tokens in turn.  One pass for the maxima and one for the
+// codes; in between a lane per token derives the scales.  (Four tokens at a time through
+// both, a scale in every lane: 48 x 14336 x 4096 34 us instead of 31.)
 template <int ACT, int TOKENS>
 __device__ __forceinline__ void finish_gated(const GemmProblem& p, Shared<TOKENS, kGated>& sh, const Item& item, int warp, int lane,
                                              int j0, int j1, int split) {
     constexpr int kSets = Shape<TOKENS, false>::kScalers / 4;
-    constexpr int kMost = 4;  // tokens of a warp at a time: their sums stay in registers
+    static_assert(TOKENS / 2 / kSets <= 32, "a lane per token");
     const GatedOut& out = p.gated;
-    const int row = (warp & 3) * 32 + lane, first = j0 + (warp >> 2);
+    const int quarter = warp & 3, row = quarter * 32 + lane, first = j0 + (warp >> 2);
     const int64_t col = item.col0 + row, nb = blocks_of(p.n);
-    const bool keep = out.gu != nullptr;
-#pragma unroll 1
-    for (int from = first; from < j1; from += kMost * kSets) {
-        float g[kMost], u[kMost];
+    const bool keep = out.gu != nullptr, mine = col < p.n;
+#pragma unroll 4
+    for (int j = first; j < j1; j += kSets) {
+        // A lane without a column reads nothing: what it read it would not wait for, and the
+        // CTA that holds it may leave once this one's warps have met it.
+        const float2 v = mine ? join_gated<TOKENS>(sh, j, row, split) : make_float2(0.0f, 0.0f);
+        const float h = gated<ACT>(v.x, v.y);
+        const uint32_t mh = warp_max_u32(abs_bits(h));
+        if (lane == 0) sh.most[0][j - j0][quarter] = mh;
+        if (keep) {
+            const uint32_t mg = warp_max_u32(abs_bits(v.x)), mu = warp_max_u32(abs_bits(v.y));
+            if (lane == 0) sh.most[1][j - j0][quarter] = mg, sh.most[2][j - j0][quarter] = mu;
+        } else {
+            sh.part[j][row] = h;  // in the place of this CTA's sum, which no other one reads
+        }
+    }
+    group_sync(1 + (warp >> 2), 128);  // (the next item's maxima come after all warps have met over its sums)
+    float scale[3] = {1.0f, 1.0f, 1.0f};  // of h, g and u of token first + lane * kSets
+    const int own = first + lane * kSets;
+    if (own < j1) {
+        const int64_t token = item.row0 + own, block = item.col0 / kBlk;
 #pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int j = from + i * kSets;
-            if (j >= j1) break;
-            g[i] = u[i] = 0.0f;
-            // A lane without a column reads nothing: what it read it would not wait for, and the
-            // CTA that holds it may leave once this one's warps have met it.
-            if (col < p.n) {
-                float x[kMostSplit];
-#pragma unroll
-                for (int r = 0; r < kMostSplit; ++r)
-                    x[r] = r < split ? ld_cluster(cluster_addr(smem_addr(&sh.part[j][row]), r)) : 0.0f;
-                g[i] = x[0], u[i] = x[1];
-#pragma unroll
-                for (int r = 2; r < kMostSplit; r += 2)
-                    if (r < split) g[i] = __fadd_rn(g[i], x[r]), u[i] = __fadd_rn(u[i], x[r + 1]);
-            }
-            const uint32_t mh = warp_max_u32(abs_bits(gated<ACT>(g[i], u[i])));
-            uint32_t mg = 0, mu = 0;
-            if (keep) mg = warp_max_u32(abs_bits(g[i])), mu = warp_max_u32(abs_bits(u[i]));
-            if (lane == 0) {
-                sh.most[0][j - j0][warp & 3] = mh;
-                sh.most[1][j - j0][warp & 3] = mg;
-                sh.most[2][j - j0][warp & 3] = mu;
+        for (int kind = 0; kind < 3; ++kind) {
+            if (kind > 0 && !keep) break;
+            const uint4 m = *reinterpret_cast<const uint4*>(sh.most[kind][own - j0]);
+            float factor;
+            scale_from_amax<kE4M3>(__uint_as_float(umax(umax(m.x, m.y), umax(m.z, m.w))), 0, &scale[kind], &factor);
+            if (quarter == 0) {
+                if (kind == 0) out.sh[token * nb + block] = factor;
+                else out.sgu[(2 * token + kind - 1) * nb + block] = factor;
             }
         }
-        group_sync(1 + (warp >> 2), 128);
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-            const int j = from + i * kSets;
-            if (j >= j1) break;
-            const int64_t token = item.row0 + j;
-            const auto write = [&](int kind, float v, uint8_t* codes, float* factors, int64_t line) {
-                const uint4 m = *reinterpret_cast<const uint4*>(sh.most[kind][j - j0]);
-                float scale, factor;
-                scale_from_amax<kE4M3>(__uint_as_float(umax(umax(m.x, m.y), umax(m.z, m.w))), 0, &scale, &factor);
-                if (col < p.n) codes[line * p.n + col] = (uint8_t)cvt2<kE4M3>(__fmul_rn(v, scale), 0.0f);
-                if (row == 0) factors[line * nb + item.col0 / kBlk] = factor;
-            };
-            write(0, gated<ACT>(g[i], u[i]), out.h, out.sh, token);
-            if (keep) {
-                write(1, g[i], out.gu, out.sgu, 2 * token);
-                write(2, u[i], out.gu, out.sgu, 2 * token + 1);
-            }
+    }
+#pragma unroll 4
+    for (int j = first; j < j1; j += kSets) {
+        const int64_t token = item.row0 + j;
+        const auto write = [&](float v, float s, uint8_t* at) {
+            const uint8_t code = (uint8_t)cvt2<kE4M3>(__fmul_rn(v, s), 0.0f);
+            if (mine) *at = code;
+        };
+        const int i = (j - first) / kSets;
+        const float s = __shfl_sync(0xFFFFFFFFu, scale[0], i);
+        if (!keep) {
+            write(sh.part[j][row], s, out.h + token * p.n + col);
+        } else {
+            const float2 v = mine ? join_gated<TOKENS>(sh, j, row, split) : make_float2(0.0f, 0.0f);
+            write(gated<ACT>(v.x, v.y), s, out.h + token * p.n + col);
+            write(v.x, __shfl_sync(0xFFFFFFFFu, scale[1], i), out.gu + 2 * token * p.n + col);
+            write(v.y, __shfl_sync(0xFFFFFFFFu, scale[2], i), out.gu + (2 * token + 1) * p.n + col);
         }
-        group_sync(1 + (warp >> 2), 128);  // the maxima have been read
     }
 }
 

@@ -41,34 +41,40 @@ fp8_status_t check(const char* fn, const GemmProblem& p) {
     return FP8_OK;
 }
 
-// Which kernel, by estimated times in microseconds as for the plain products, whose
-// kernels these are: the pair kernel (0), or the stream kernel by tiles of 16, 32 or 64
-// tokens.  Measured on GB300 ([m, n, k] silu, without a checkpoint; in a CUDA graph, cold weights):
-//   [1, 18432, 7168]   stream/16 44  stream/32 45  pair 79    [16, 7168, 7168]  stream/16 22  stream/64 26  pair 37
-//   [32, 14336, 4096]  stream/32 28  stream/64 31  pair 38    [48, 14336, 4096] stream/64 33  stream/32 43  pair 39
-//   [64, 2048, 7168]   stream/32 15  stream/64 17  pair 29    [128, 4096, 4096] pair 20  stream/64 21
-//   [256, 7168, 7168]  pair 33  stream/32 84       [300, 1024, 2048] pair 13  stream/64 13
-//   experts: 96 rows over 64 (2048 x 7168 each) stream/16 273  stream/64 301  pair 383; 512 over 32: 146, 181, 203;
-//   1024 over 16 (2048 x 2048) pair 46  stream/64 53
-// (tiles of 128 tokens: never the fastest).
+// Which kernel, by estimated times in microseconds from what they measured on GB300: the
+// pair kernel (0), or the stream kernel by tiles of 16, 32 or 64 tokens.  [m, n, k] silu,
+// without a checkpoint, in a CUDA graph, cold weights:
+//   [3, 1024, 1024]    stream/16 5.4  /32 5.8  /64 6.1  pair 8.5    [1, 18432, 7168]  44  46  60  79
+//   [16, 7168, 7168]   22  22  25  37      [32, 14336, 4096]  36  27  29  37    [48, 14336, 4096]  48  40  31  38
+//   [64, 2048, 7168]   15  14  16  29      [4864, 6144, 128]  503  299  235  42
+//   experts: 96 rows over 64 of 2048 x 7168  280  286  300  383;  512 over 32  143 to 158  161  176  203;
+//   1024 over 16 of 2048 x 2048  78  55  45  44
+// Over 73 random sizes of this range (1 to 8192 rows, up to 64 experts) the choices take
+// 2% more than the fastest kernel does, 22% at worst.
 int choose(const GemmProblem& p) {
     const int64_t kb = blocks_of(p.k), sms = sm_count();
-    const double busy = (double)(p.groups < p.m ? p.groups : p.m);
-    const auto tiles = [&](int rows) {  // along m: the groups' last tiles are half full on average
-        return p.groups > 1 ? (double)p.m / rows + 0.5 * busy : (double)((p.m + rows - 1) / rows);
-    };
+    const double busy = (double)(p.groups < p.m ? p.groups : p.m), rows = (double)p.m / busy;  // groups with rows, and theirs
     const auto most = [](double a, double b) { return a > b ? a : b; };
+    const auto tiles = [&](int high) {  // along m: one per group at least, the last one of longer ones half full on average
+        return p.groups > 1 ? most(busy, (double)p.m / high + 0.5 * busy) : (double)((p.m + high - 1) / high);
+    };
     const double memory = (2.0 * busy * (double)p.n * (double)p.k + (double)p.m * (double)(p.k + p.n)) / 6.5e6;
     const double columns = (double)((p.n + 127) / 128);
-    const double pair = ceil(tiles(256) * columns / (double)(sms / 2)) * (0.46 * (double)kb + 2.0);
-    double best = 4.0 + most(pair, memory * 6.5 / 4.5);
+    const bool keep = p.gated.gu != nullptr;
+    // the pair kernel: 0.46 per block, and the end of a tile
+    const double pair = ceil(tiles(256) * columns / (double)(sms / 2)) * (0.46 * (double)kb + (keep ? 3.8 : 2.4));
+    double best = 3.5 + most(pair, memory * 6.5 / 4.5);
     int choice = 0;
-    constexpr double kBlock[3] = {0.40, 0.39, 0.66}, kJoin[3] = {1.0, 1.8, 2.2};
+    // the stream kernel: per block, and the end of an item by the tokens that a CTA joins; the
+    // next one starts 2.7 later
+    constexpr double kBlock[3] = {0.40, 0.39, 0.66};
     for (int i = 0; i < 3; ++i) {
         const int tokens = 16 << i;
         const StreamPlan plan = stream_plan(p, tokens, (int)sms);
-        const double compute = ceil(tiles(tokens) * columns / plan.clusters) * ceil((double)kb / (plan.split / 2)) * kBlock[i];
-        const double us = 5.0 + kJoin[i] + most(compute, memory);
+        const double rounds = ceil(tiles(tokens) * columns / plan.clusters);
+        const double join = 0.6 + (keep ? 0.36 : 0.18) * (rows < tokens ? rows : tokens) / plan.split;
+        const double compute = rounds * ceil((double)kb / (plan.split / 2)) * kBlock[i] + (rounds - 1.0) * (2.7 + join);
+        const double us = 5.0 + 0.3 * i + join + most(compute, memory);
         if (us < best) best = us, choice = tokens;
     }
     return choice;
