@@ -124,6 +124,30 @@ __device__ __forceinline__ void load_pieces(const Backward& p, Stage<F32>& s, in
     }
 }
 
+// Bytes 4 word .. 4 word + 3 of a line of len bytes, zeros from its end on.  Only aligned
+// words are read that hold a byte of the line.
+__device__ __forceinline__ uint32_t word_of_line(const uint8_t* line, int word, int len) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(line) & 3u), left = len - 4 * word;
+    const uint32_t* const from = reinterpret_cast<const uint32_t*>(line - off) + word;
+    const uint32_t lo = left + off > 0 && len > 0 ? __ldg(from) : 0u, hi = left + off > 4 && off > 0 ? __ldg(from + 1) : 0u;
+    const uint32_t v = __funnelshift_r(lo, hi, 8 * off);
+    return left >= 4 ? v : left <= 0 ? 0u : v & (0xFFFFFFFFu >> (32 - 8 * left));
+}
+
+// A line of `len` codes that starts anywhere, a word per lane, to q: aligned words, and the
+// line's first and last bytes, which share words with other lines, one by one.
+__device__ __forceinline__ void store_line(uint8_t* q, uint32_t w, int len, int lane) {
+    const uint32_t before = __shfl_up_sync(0xFFFFFFFFu, w, 1);
+    const int off = (int)(reinterpret_cast<uintptr_t>(q) & 3u), left = len - lane * 4;
+    if ((lane > 0 || off == 0) && left >= 4 - off) *reinterpret_cast<uint32_t*>(q + lane * 4 - off) = __funnelshift_l(before, w, 8 * off);
+    const int head = lane == 0 ? -off & 3 : 0, tail = left - ((len + off) & 3);
+    if (head > 0 || tail < 4) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (x < left && (x < head || x >= tail)) q[lane * 4 + x] = (uint8_t)(w >> (8 * x));
+    }
+}
+
 template <bool F32>
 __device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int tr, int tc) {
     const int r0 = tr * kTile, c0 = tc * kTile;
@@ -132,14 +156,26 @@ __device__ __forceinline__ void load_tile(const Backward& p, Stage<F32>& s, int 
     } else if (p.copy_in == 4) {
         load_pieces<4>(p, s, r0, c0);
     } else {
-        const int x = threadIdx.x % kTile;
-#pragma unroll 8
-        for (int y = threadIdx.x / kTile; y < kTile; y += kThreads / kTile) {
-            const bool there = r0 + y < p.rows && c0 + x < p.n;
-            const int64_t row = wide(r0 + y, p.n), at = row + c0 + x;
-            s.dh[y][x] = there ? __ldg(static_cast<const typename Stage<F32>::Grad*>(p.dh) + at) : 0;
-            s.gu[0][y][x] = there ? __ldg(p.gu + at + row) : 0;
-            s.gu[1][y][x] = there ? __ldg(p.gu + at + row + p.n) : 0;
+        // Rows that start anywhere, by the warp that uses them: each word put together from the two
+        // aligned ones that hold it.
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cols = min(p.n - c0, kTile);
+#pragma unroll 4
+        for (int i = 0; i < kRows; ++i) {
+            const int y = warp * kRows + i;
+            const bool there = r0 + y < p.rows;
+            const int64_t row = wide(r0 + y, p.n), at = row + c0;
+            const int len = there ? cols : 0;
+            *reinterpret_cast<uint32_t*>(&s.gu[0][y][lane * 4]) = word_of_line(p.gu + at + row, lane, len);
+            *reinterpret_cast<uint32_t*>(&s.gu[1][y][lane * 4]) = word_of_line(p.gu + at + row + p.n, lane, len);
+            if constexpr (F32) {
+#pragma unroll
+                for (int x = lane; x < kTile; x += 32) s.dh[y][x] = x < len ? __ldg(static_cast<const float*>(p.dh) + at + x) : 0.0f;
+            } else {
+                const uint8_t* const line = static_cast<const uint8_t*>(p.dh) + 2 * at;
+#pragma unroll
+                for (int w = lane; w < kTile / 2; w += 32)
+                    *reinterpret_cast<uint32_t*>(&s.dh[y][2 * w]) = word_of_line(line, w, 2 * len);
+            }
         }
     }
 }
@@ -303,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
         }
         const bool more = next_r < rb;
         const int r0 = tr * kTile + warp * kRows, c0 = tc * kTile + lane * 4;
-        const int cols = min(p.n - c0, 4), rows = min(p.rows - r0, kRows);  // here
+        const int rows = min(p.rows - r0, kRows);  // here
         const Stage<F32>& st = sm.stage[at];
         const float (&factors)[2 * kTile][kGroup] = sm.factor_in[group];
         if (kStages == 2) {  // the other stage was left by all before the last tile's maxima
@@ -425,10 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
                 codes([&](int, uint32_t c) { *reinterpret_cast<uint32_t*>(q) = c; });
             else
                 codes([&](int i, uint32_t c) {
-                    if (i < rows)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (j < cols) q[j] = (uint8_t)(c >> (8 * j));
+                    if (i < rows) store_line(q - lane * 4, c, min(p.n - tc * kTile, kTile), lane);
                 });
         }
         if (!columns) continue;
