@@ -34,21 +34,20 @@ constexpr double kLog2E = 1.4426950408889634, kGeluTwoC = 1.5957691216057308 /* 
 // Beyond it the sigmoid of GELU is 0 or 1, and g^2 stays finite (0 * Inf would make a NaN of 0).
 constexpr float kGeluFar = 32.0f;
 
-// s(g), and y'(g) where DERIVATIVE (1 for SiLU).
-template <int ACT, bool DERIVATIVE>
-__device__ __forceinline__ float gate(float g, float* dy) {
+// s(g).
+template <int ACT>
+__device__ __forceinline__ float gate(float g) {
     float t;  // -y log2 e
     if constexpr (ACT == kSilu) {
         t = g * (float)-kLog2E;
     } else {
         const float c = fminf(fmaxf(g, -kGeluFar), kGeluFar), c2 = c * c;
         t = c * __fmaf_rn(c2, (float)(-kLog2E * kGeluTwoC * kGeluCube), (float)(-kLog2E * kGeluTwoC));
-        if constexpr (DERIVATIVE) *dy = __fmaf_rn(c2, (float)(3.0 * kGeluTwoC * kGeluCube), (float)kGeluTwoC);
     }
     return rcp_approx(1.0f + exp2_approx(t));
 }
 
-// The same of two values as a packed pair.
+// The same of two values as a packed pair, and y'(g) where DERIVATIVE (not set for SiLU, 1).
 template <int ACT, bool DERIVATIVE>
 __device__ __forceinline__ uint64_t gate2(uint64_t g, uint64_t* dy) {
     const auto both = [](double v) { return pack2((float)v, (float)v); };
@@ -67,7 +66,7 @@ __device__ __forceinline__ uint64_t gate2(uint64_t g, uint64_t* dy) {
 
 template <int ACT>
 __device__ __forceinline__ float gated(float g, float u) {
-    return g * gate<ACT, false>(g, nullptr) * u;
+    return g * gate<ACT>(g) * u;
 }
 
 // The same of two columns; the same values, and h the same bits, as gated().

@@ -283,7 +283,7 @@ __device__ __forceinline__ void write_columns(const Backward& p, const uint8_t (
 // Two columns at once, as packed pairs (fma.rn.f32x2 and its like).
 template <int ACT>
 __device__ __forceinline__ void differentiate(uint64_t d, uint64_t g, uint64_t u, uint64_t* dg, uint64_t* du, uint64_t* h) {
-    uint64_t dy;
+    uint64_t dy = 0;
     const uint64_t s = gate2<ACT, true>(g, &dy), a = mul2(g, s), rest = fma2(s, pack2(-1.0f, -1.0f), pack2(1.0f, 1.0f));
     const uint64_t slope = fma2(ACT == kSilu ? a : mul2(a, dy), rest, s);
     *dg = mul2(mul2(d, u), slope);
