@@ -18,15 +18,18 @@
 // per lane while the next tile is computed; that one's inputs are copied into
 // shared memory a tile ahead.
 //
-// What bounds it: latency.  96 values and four warps per scheduler fill the
-// registers, and 37 instructions per element issue in 0.45 of the slots, at
-// 4.4 to 4.6 TB/s (reads or stores taken out, 119 us become 112 and 101).
-// Measured: 4096 x 14336 119 us, 16384 x 18432 590 (4.6 TB/s), 8192 x 2048 39;
+// What bounds it: 4096 x 14336 takes 117 us, without any arithmetic 101, without the
+// factors (single words a row of memory apart: a tenth of the requests) 88, which is
+// nine tenths of the copy's rate.  96 values and four warps per scheduler fill the
+// registers, and 37 instructions per element issue in half of the slots.
+// Measured: 4096 x 14336 117 us, 16384 x 18432 581 (4.7 TB/s), 8192 x 2048 38;
 // rows that are no multiple of 16 share cache lines between tiles of a column
-// (16400 x 18432 631, 8195 x 2048 47, with fp32 gradients 56).
-// Others of the same mathematics: values computed twice, by warps that have whole
-// rows and warps that have whole columns, no barrier, three CTAs per SM: 162 us for
-// 4096 x 14336 when this form took 139; 32 warps of 64 registers: 179 (spills).
+// (16400 x 18432 609 to 631, 8195 x 2048 46, with fp32 gradients 54).
+// Others of the same mathematics, 4096 x 14336: values computed twice, by warps that
+// have whole rows and warps that have whole columns, no barrier, three CTAs per SM,
+// 162 us when this form took 139; 32 warps of 64 registers 179 (spills); pairs of CTAs
+// with half a tile's columns each, two per SM, that exchange the rows' maxima through
+// distributed shared memory 131; tiles walked down strips of 2 to 32 rows of them 122.
 #include <type_traits>
 
 #include "fp8q_host.h"
