@@ -350,7 +350,11 @@ class GatedBlockStep:
         rows, lead = self.x.shape[0], self.gate_up.shape[:-3]
         hidden, inn = self.gate_up.shape[-2:]
         dgu, sdgu, dgu_t, sdgu_t, h_t, sh_t = self.grads
-        one_gu = (self.qgu.view(*lead, 2 * hidden, inn), self.sgu_w.view(*lead, hidden // 64, -1))  # one [2 hidden, in] weight
+        nb, kb, rb = hidden // 128, self.sgu_w.shape[-1], sdgu_t.shape[-1]
+        # both projections as one operand, all sizes named: without rows a -1 has no value
+        one_gu = (self.qgu.view(*lead, 2 * hidden, inn), self.sgu_w.view(*lead, 2 * nb, kb))
+        one_d = (dgu.view(rows, 2 * hidden), sdgu.view(rows, 2 * nb))
+        one_dt = (dgu_t.view(2 * hidden, rows), sdgu_t.view(2 * hidden, rb))
         _t(timer, "quantize_weight", lambda: (self._quantize(self.gate_up, self.qgu, self.sgu_w),
                                               self._quantize(self.down, self.qd, self.sd_w)))
         _t(timer, "quantize_x", lambda: fp8_quantize_block_cast_transpose(self.x, self.fmt, *self.qx))
@@ -359,9 +363,8 @@ class GatedBlockStep:
         _t(timer, "quantize_dy", lambda: fp8_quantize_block_cast_transpose(self.dy, self.grad_fmt, *self.qdy))
         _t(timer, "dh", lambda: self._product(*self.qdy[:2], self.grad_fmt, self.qd, self.sd_w, self.dh, B_KN))
         _t(timer, "backward", lambda: fp8_gated_block_backward(self.dh, *self.kept, *self.grads, self.grad_fmt, self.act))
-        _t(timer, "dx", lambda: self._product(dgu.view(rows, -1), sdgu.view(rows, -1), self.grad_fmt, *one_gu, self.dx, B_KN))
-        _t(timer, "wgrad_gate_up", lambda: self._wgrad(dgu_t.view(2 * hidden, rows), sdgu_t.view(2 * hidden, -1),
-                                                       self.grad_fmt, *self.qx[2:], self.fmt,
+        _t(timer, "dx", lambda: self._product(*one_d, self.grad_fmt, *one_gu, self.dx, B_KN))
+        _t(timer, "wgrad_gate_up", lambda: self._wgrad(*one_dt, self.grad_fmt, *self.qx[2:], self.fmt,
                                                        self.dgate_up.view(*lead, 2 * hidden, inn)))
         _t(timer, "wgrad_down", lambda: self._wgrad(*self.qdy[2:], self.grad_fmt, h_t, sh_t, E4M3, self.ddown))
         _t(timer, "clip", lambda: fp8_grad_clip_grouped([self.dgate_up, self.ddown], self.max_norm, self.norm))
