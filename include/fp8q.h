@@ -509,7 +509,8 @@ fp8_status_t fp8_block128_scales_to_mx(const float* scale_inv, int64_t rows, int
  * Two kernels: CTA pairs over 256 x 256 outputs, or, with few rows of A, CTAs
  * that stream 128 columns' worth of B and split the contraction over a cluster;
  * which one is chosen by sizes alone.  Their waits are bounded and counted by
- * fp8_wait_timeouts.  One launch, plus one per operand that is copied.
+ * fp8_wait_timeouts.  One launch, plus one where an operand is copied (both
+ * operands in the same one).
  *
  * The forward product of a layer with weight W [out, in] and tokens X [t, in]
  * is (A = X, B = W, FP8_B_NK); the input gradient is (A = dY [t, out], B = W,
@@ -587,8 +588,9 @@ fp8_status_t fp8_gemm_block_grouped_wgrad(int groups, const int64_t* group_ends,
  *                    Outputs may start anywhere; n % 16 == 0 and 16-byte aligned
  *                    codes are written faster.
  * An output must not overlap another or an input.  Results do not depend on the
- * stream, on other calls or on earlier ones.  One launch, plus one per operand
- * that is copied; the kernels' waits are bounded and counted by fp8_wait_timeouts. */
+ * stream, on other calls or on earlier ones.  One launch, plus one where an operand
+ * is copied (both operands in the same one); the kernels' waits are bounded and
+ * counted by fp8_wait_timeouts. */
 fp8_status_t fp8_gemm_block_gated(const uint8_t* a, fp8_format_t fmt_a, const float* scale_inv_a, const uint8_t* b,
                                   fp8_format_t fmt_b, const float* scale_inv_b, fp8_activation_t act, int64_t m,
                                   int64_t n, int64_t k, uint8_t* h, float* scale_inv_h, uint8_t* gu,
