@@ -288,7 +288,8 @@ template <int ACT>
 __device__ __forceinline__ void differentiate(uint64_t d, uint64_t g, uint64_t u, uint64_t* dg, uint64_t* du, uint64_t* h) {
     uint64_t dy = 0;
     const uint64_t s = gate2<ACT, true>(g, &dy), a = mul2(g, s), rest = fma2(s, pack2(-1.0f, -1.0f), pack2(1.0f, 1.0f));
-    const uint64_t slope = fma2(ACT == kSilu ? a : mul2(a, dy), rest, s);
+    // y' with 1 - s first, which is 0 where g is large: a y' would be Inf for g beyond 1.5e36
+    const uint64_t slope = fma2(a, ACT == kSilu ? rest : mul2(rest, dy), s);
     *dg = mul2(mul2(d, u), slope);
     *du = mul2(d, a);
     *h = mul2(a, u);
