@@ -18,13 +18,14 @@
 // per lane while the next tile is computed; that one's inputs are copied into
 // shared memory a tile ahead.
 //
-// What bounds it: 4096 x 14336 takes 117 us, without any arithmetic 101, without the
+// What bounds it: 4096 x 14336 takes 116 us, without any arithmetic 101, without the
 // factors (single words a row of memory apart: a tenth of the requests) 88, which is
 // nine tenths of the copy's rate.  96 values and four warps per scheduler fill the
 // registers, and 37 instructions per element issue in half of the slots.
-// Measured: 4096 x 14336 117 us, 16384 x 18432 581 (4.7 TB/s), 8192 x 2048 38;
-// rows that are no multiple of 16 share cache lines between tiles of a column
-// (16400 x 18432 609 to 631, 8195 x 2048 46, with fp32 gradients 54).
+// Measured, one call after another on inputs larger than L2: 4096 x 14336 116 us,
+// 16384 x 18432 574 (4.7 TB/s), 8192 x 2048 38; rows that are no multiple of 16 share
+// cache lines between tiles of a column (16400 x 18432 617, 8195 x 2048 46, with fp32
+// gradients 54, 1337 x 13841 102).
 // Others of the same mathematics, 4096 x 14336: values computed twice, by warps that
 // have whole rows and warps that have whole columns, no barrier, three CTAs per SM,
 // 162 us when this form took 139; 32 warps of 64 registers 179 (spills); pairs of CTAs
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
     const int nb = (p.n + kTile - 1) / kTile, rb = (p.rows + kTile - 1) / kTile;
     // Runs of p.run tiles along the columns, every gridDim.x-th of them: what the CTAs work on at
     // one time lies close together, and the pieces of a cache line that two tiles of a column
-    // share meet in L2.  (One long run per CTA: 16400 x 18432 in 1117 us instead of 622.)
+    // share meet in L2.  (One long run per CTA: 1.8 times as long for 16400 x 18432.)
     const int runs = (nb + p.run - 1) / p.run, step_r = gridDim.x / runs, step_c = gridDim.x % runs;
     int run_r = blockIdx.x / runs, run_c = blockIdx.x % runs, tr = run_r, tc = run_c * p.run;
     pdl_begin();
@@ -505,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_backward_kernel(const __gri
 }
 
 fp8_status_t run(const char* fn, Backward p, bool f32, int fmt, int act, cudaStream_t st) {
-    // Runs of four tiles share reads and writes of factors (4096 x 14336: 119 us, single tiles 122.5;
-    // 16384 x 18432: 590 and 599), but their last round may leave more CTAs idle (8192 x 2048: 43 and 39).
+    // Runs of four tiles share reads and writes of factors (single tiles: 3% longer for 4096 x 14336,
+    // 1.5% for 16384 x 18432), but their last round may leave more CTAs idle (8192 x 2048: 10% longer).
     const int64_t nb = (p.n + kTile - 1) / kTile, rb = (p.rows + kTile - 1) / kTile;
     const int sms = sm_count();
     int64_t ctas = 0;

@@ -19,8 +19,8 @@ namespace {
 // together from single bytes at the array's two ends, so that nothing outside is
 // read.  A few MB are bound by latency: the loads of kPackSteps pieces are issued
 // before the first is used, and both operands share a launch.  [777, 2 x 4100, 1032]
-// with checkpoint takes 30.0 us, 33.8 with a launch for each and a piece at a time;
-// [1, 2 x 18432, 7161], bound by memory, 137 and 148.  Two or three pieces: the same.
+// with checkpoint takes 29.5 us, with a launch for each and a piece at a time 4 more;
+// [1, 2 x 18432, 7161], bound by memory, 136 and 11 more.  Two or three pieces: the same.
 constexpr int kPackThreads = 256;
 constexpr int kPackSteps = 4, kPackCtas = 16;  // (CTAs per SM, most)
 

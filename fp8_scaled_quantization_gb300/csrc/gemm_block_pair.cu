@@ -356,9 +356,9 @@ __device__ __forceinline__ void store_tile(const GemmProblem& p, const CUtensorM
 // (activation and exchange; 0.6 us more with the checkpoint).  Codes leave by bulk
 // copies; by plain stores of 16 bytes per lane instead the end took 0.8 us more.
 // Measured back to back in a graph (codes of one sign): 4001 x 18432 x 7168 (rows, n, k)
-// 828 us with the checkpoint (2550 TFLOP/s), 802 to 810 without; 18432 x 2048 312 and
-// 282; 16384 rows over 32 experts, 2048 x 7168, 396.  On normal values the power limit
-// makes the first 900.
+// 818 us with the checkpoint (2585 TFLOP/s), 793 without; 18432 x 2048 306 and 281;
+// 16384 rows over 32 experts, 2048 x 7168, 392; 777 x 4100 x 1024 21.7.  On normal
+// values the power limit makes the first 890 to 905.
 
 // A lane's row of `WORDS` words of E4M3 codes (v * scale, four per word) goes through the
 // warp's staging buffer, whose rows are 4 * WORDS bytes, swizzled as the bulk copies
@@ -489,8 +489,8 @@ __device__ __forceinline__ void store_gated(const GemmProblem& p, const CUtensor
     const bool async = bulk && rows == 32;  // all rows are in the group
     // The lower 4 KB of the warp's buffers take the checkpoint's codes, which may leave meanwhile;
     // the upper ones 32 columns at a time for the other warp, then h's codes.  The first 32 are
-    // written before the checkpoint's codes are made: 777 x 4100 x 1024 takes 21.4 us (22.2 with
-    // them written after), 4001 x 18432 x 2048 308 (312), x 7168 826 (829).
+    // written before the checkpoint's codes are made: written after them, 777 x 4100 x 1024 takes
+    // 0.8 us more, 4001 x 18432 x 2048 4, x 7168 3.
     const uint32_t upper = mine + kOutBytes;
     const auto pass_on = [&](int part) {
 #pragma unroll

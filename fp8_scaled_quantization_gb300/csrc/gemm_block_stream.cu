@@ -12,10 +12,10 @@
 // The gated form gives the gate's weight to the even CTAs of a cluster and the up
 // projection's to the odd ones, each half of them sharing the contraction; both
 // sums of a token meet where they are joined.  A CTA that streamed both, one after the
-// other, needs twice the sums, and 64 tokens no longer fit an SM twice: 48 x 14336 x
-// 4096 (tokens, n, k) took 38 us when this took 33, 16 x 7168 x 7168 23 when this took 22.
-// As the plain product with twice the columns takes, so does the gated one: 1 x 18432
-// x 7168 44 us (6.0 TB/s), 96 rows over 64 experts of 2048 x 7168 273 us (6.9 TB/s).
+// other, needs twice the sums, and 64 tokens no longer fit an SM twice: 15% longer for 48
+// x 14336 x 4096 (tokens, n, k), 5% for 16 x 7168 x 7168.  As the plain product with
+// twice the columns takes, so does the gated one: 1 x 18432 x 7168 44 us (6.0 TB/s), 16 x
+// 7168 x 7168 22, 48 x 14336 x 4096 30, 96 rows over 64 experts of 2048 x 7168 274 (6.9 TB/s).
 //
 // Roles per CTA: four warps (eight from 32 tokens on, each pair of them sharing
 // the tokens of 32 columns) scale, add, join and store; then one warp fills the
@@ -170,7 +170,7 @@ __device__ __forceinline__ float2 join_gated(const Shared<TOKENS, kGated>& sh, i
 // column, quantized in tiles of the CTA's 128 columns, by four warps, of which the CTA has
 // one set or two that take the tokens in turn.  One pass for the maxima and one for the
 // codes; in between a lane per token derives the scales.  (Four tokens at a time through
-// both, a scale in every lane: 48 x 14336 x 4096 34 us instead of 31.)
+// both, a scale in every lane: 10% longer for 48 x 14336 x 4096.)
 template <int ACT, int TOKENS>
 __device__ __forceinline__ void finish_gated(const GemmProblem& p, Shared<TOKENS, kGated>& sh, const Item& item, int warp, int lane,
                                              int j0, int j1, int split) {
